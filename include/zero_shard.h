@@ -618,6 +618,242 @@ ZS_API int32_t zero_qwz_dequantize(const int8_t* codes_dev, const float* scales_
                                    uint16_t* params_dev, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The loss end of a fine-tuning step: token log-probabilities, the clipped  */
+/* policy loss and the preference loss, with their gradients.  The pages     */
+/* describe the optimizer end only; these calls make the loss-scaled         */
+/* gradient of the logits that the backward pass turns into contributions.   */
+/* ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define ZS_F32 0
+#define ZS_F16 1
+#define ZS_BF16 2
+
+/* Bytes of the caller's scratch buffer (`work_dev`, DEVICE, 8-byte aligned) of
+ * the calls that add up over a whole batch.  Cleared (zero bytes) once before
+ * its first use; every call leaves it ready for the next.  Calls that may run
+ * at the same time (other streams) need a buffer each. */
+#define ZS_WORK_BYTES 65536
+
+/* A matrix of logits, one row per token.
+ *   data         DEVICE, element type `type`, aligned to its element
+ *   rows, vocab  rows >= 0; 1 <= vocab <= 2^30
+ *   row_stride   elements from one row to the next, >= vocab; any value is
+ *                allowed, rows need not start on vector boundaries
+ *   type         ZS_F32, ZS_F16 or ZS_BF16; reserved must be 0
+ *   inv_temperature  it > 0: the distribution of a row is softmax(x it) */
+typedef struct zs_logits {
+    const void* data;
+    int64_t rows;
+    int64_t vocab;
+    int64_t row_stride;
+    int32_t type;
+    int32_t reserved;
+    double inv_temperature;
+} zs_logits;
+
+/* Log-probability of each row's label, and the row's entropy.  With
+ * top = max_i x_i, d_i = (x_i - top) it and S = sum_i exp(d_i), all in fp32:
+ *   logp = d_label - ln S,   entropy = ln S - sum_i exp(d_i) d_i / S,
+ *   saved[2 row] = top,  saved[2 row + 1] = ln S   (for the gradient call).
+ *   labels   DEVICE int64[rows]; a label outside [0, vocab) marks a row that
+ *            is ignored: its logits are not read and its outputs are 0.
+ *   logp, entropy, saved   DEVICE fp32 [rows], [rows], [2 rows]; entropy and
+ *            saved may be NULL.
+ * A logit of -inf has probability 0.  A row of nothing but -inf has no
+ * distribution: logp = -inf, entropy = 0.  A NaN or +inf in a row gives NaN.
+ * One pass over the logits, stream-ordered, one launch.
+ * Source: the softmax cross-entropy of a language model; no counterpart in the pages. */
+ZS_API int32_t zero_token_logp_async(const zs_logits* x, const int64_t* labels, float* logp, float* entropy,
+                                     float* saved, void* stream);
+
+/* Gradient of sum_rows (dlogp logp + dentropy entropy) with respect to the
+ * logits, times the loss scale L of *ctrl_dev (NULL: 1).  With
+ * p_i = exp(d_i - ln S):
+ *   dx_i = L it [ dlogp (1[i = label] - p_i) - dentropy p_i (ln p_i + entropy) ]
+ * in fp32, rounded once to the logits' type.
+ *   saved      DEVICE fp32[2 rows] of zero_token_logp_async
+ *   dlogp      DEVICE fp32[rows]
+ *   entropy, dentropy  DEVICE fp32[rows] each, or both NULL
+ *   dlogits    DEVICE, rows of dlogits_stride >= vocab elements, the logits'
+ *              type; may be the logits themselves (same pointer and stride).
+ * Rows that the forward call ignored, and rows of nothing but -inf, get zeros.
+ * Only [0, vocab) of each row is written.
+ * Source: derivative of zero_token_logp_async; loss scale: the dynamic loss-scale rule. */
+ZS_API int32_t zero_token_logp_grad_async(const zs_logits* x, const int64_t* labels, const float* saved,
+                                          const float* dlogp, const float* entropy, const float* dentropy,
+                                          const zs_ctrl* ctrl_dev, void* dlogits, int64_t dlogits_stride,
+                                          void* stream);
+
+/* Coefficients of the clipped policy loss.  clip_low in [0, 1], clip_high >= 0,
+ * kl_coef, entropy_coef finite; dual_clip = 0 (off) or > 1. */
+typedef struct zs_policy {
+    double clip_low;
+    double clip_high;
+    double dual_clip;
+    double kl_coef;
+    double entropy_coef;
+} zs_policy;
+
+/* Entries of the policy loss's totals. */
+#define ZS_POLICY_TOTALS 5
+
+/* The clipped policy loss of reinforcement-learning fine-tuning, its gradient
+ * with respect to the logits, and its statistics, in one launch that reads the
+ * logits from memory once.  Per row, with logp and entropy as in zero_token_logp_async:
+ *   r     = exp(logp - old_logp)
+ *   pg    = max(-A r, -A clip(r, 1 - clip_low, 1 + clip_high))
+ *           and, with dual_clip c > 0 and A < 0, at most -A c
+ *   kl    = exp(ref_logp - logp) - (ref_logp - logp) - 1      (0 without ref_logp)
+ *   loss  = pg + kl_coef kl - entropy_coef entropy
+ * and over the rows, w the row's weight:
+ *   totals = sum_rows w { loss, pg, kl, entropy, [the gradient of pg is cut off] }
+ *   dlogits = L d totals[0] / d logits   (L the loss scale of *ctrl_dev; NULL: 1)
+ *   old_logp, advantages   DEVICE fp32[rows]
+ *   ref_logp   DEVICE fp32[rows] or NULL
+ *   weights    DEVICE fp32[rows] or NULL (1 / rows each).  A row of weight 0 is
+ *              left out: neither its logits nor its other inputs are used, its
+ *              outputs and gradient are 0.  So are rows whose label is outside
+ *              [0, vocab) and rows of nothing but -inf (whose logp is -inf).
+ *   logp       DEVICE fp32[rows]
+ *   entropy, token_loss   DEVICE fp32[rows] or NULL.  The entropy (and its
+ *              total) is computed when entropy is set or entropy_coef != 0.
+ *   dlogits    as in zero_token_logp_grad_async, or NULL: forward only
+ *   totals     DEVICE fp32[ZS_POLICY_TOTALS]; summed in fp64 in a fixed order
+ *   work_dev   ZS_WORK_BYTES of scratch
+ * Source: the clipped surrogate objective with a KL penalty; no counterpart in the pages. */
+ZS_API int32_t zero_policy_loss_async(const zs_logits* x, const int64_t* labels, const float* old_logp,
+                                      const float* advantages, const float* ref_logp, const float* weights,
+                                      const zs_policy* hp, const zs_ctrl* ctrl_dev, float* logp, float* entropy,
+                                      float* token_loss, void* dlogits, int64_t dlogits_stride, float* totals,
+                                      void* work_dev, void* stream);
+
+/* Kinds of preference loss. */
+#define ZS_PREFERENCE_SIGMOID 0
+#define ZS_PREFERENCE_HINGE 1
+#define ZS_PREFERENCE_SQUARED 2
+
+/* Preference loss: beta > 0; kind; average: 0 sums a sequence's tokens, 1
+ * takes their mean; label_smoothing in [0, 0.5] (SIGMOID; else 0); margin
+ * finite, taken off beta h. */
+typedef struct zs_preference {
+    double beta;
+    double label_smoothing;
+    double margin;
+    int32_t kind;
+    int32_t average;
+} zs_preference;
+
+/* Entries of the preference loss's totals. */
+#define ZS_PREFERENCE_TOTALS 3
+
+/* The paired preference loss over packed token log-probabilities, and its
+ * gradient with respect to them.  Pair i is sequence 2 i (chosen) and 2 i + 1
+ * (rejected).  With s = the sum (average: the mean, 0 of nothing) over a
+ * sequence's unmasked tokens of logp - ref_logp, h = s_chosen - s_rejected and
+ * z = beta h - margin:
+ *   SIGMOID  loss = -(1 - ls) ln sigma(z) - ls ln sigma(-z)
+ *   HINGE    loss = max(0, 1 - z)
+ *   SQUARED  loss = (h - 1 / (2 beta))^2
+ *   totals = sum_pairs w { loss, [reward_chosen > reward_rejected], reward_chosen - reward_rejected }
+ *   dlogp = d totals[0] / d logp;   reward = beta s
+ *   logp       DEVICE fp32[n_tokens]
+ *   ref_logp   DEVICE fp32[n_tokens], or NULL (0: reference-free)
+ *   mask       DEVICE uint8[n_tokens], 0 = the token does not count (its
+ *              values, whatever they are, are not used), or NULL (all count)
+ *   cu_seqlens DEVICE int64[2 n_pairs + 1], ascending: sequence j is tokens
+ *              [cu[j], cu[j + 1]), cut to [0, n_tokens).  Tokens outside every
+ *              sequence keep their dlogp as it was.
+ *   weights    DEVICE fp32[n_pairs], or NULL (1 / n_pairs each); a pair of
+ *              weight 0 gets loss, rewards and gradient 0 and is not read
+ *   loss       DEVICE fp32[n_pairs];  reward  DEVICE fp32[2 n_pairs]
+ *   dlogp      DEVICE fp32[n_tokens] or NULL: forward only; 0 at masked tokens;
+ *              may not overlap another buffer
+ *   totals     DEVICE fp32[ZS_PREFERENCE_TOTALS]; summed in fp64 in a fixed order
+ *   work_dev   ZS_WORK_BYTES of scratch
+ * Source: direct preference optimization and its hinge and squared forms; no counterpart in the pages. */
+ZS_API int32_t zero_preference_loss_async(const float* logp, const float* ref_logp, const uint8_t* mask,
+                                          int64_t n_tokens, const int64_t* cu_seqlens, const float* weights,
+                                          int32_t n_pairs, const zs_preference* hp, float* loss, float* reward,
+                                          float* dlogp, float* totals, void* work_dev, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* AdamW over a list of tensors: weights that are not one flat fp16 shard     */
+/* (adapters, replicated or unpartitioned parameters, bf16 models).          */
+/* ------------------------------------------------------------------------ */
+
+/* Kinds of optimizer state. */
+#define ZS_STATE_F32 0
+#define ZS_STATE_U8 1
+
+/* Largest number of tensors of one call. */
+#define ZS_MAX_TENSORS 16384
+
+/* One tensor, as n consecutive elements.
+ *   grad      DEVICE, grad_type (ZS_F32, ZS_F16 or ZS_BF16), carries the loss scale
+ *   master    DEVICE fp32 weights, updated in place
+ *   m, v      DEVICE, updated in place: fp32[n] (ZS_STATE_F32), or uint8 codes
+ *             [n] (ZS_STATE_U8) with fp32 scales m_scale, v_scale
+ *             [ceil(n / ZS_ADAM8_BLOCK)], the format of zs_adam8_shard
+ *   param     DEVICE, param_type (ZS_F16 or ZS_BF16): the weights' copy that the
+ *             model computes with, rounded from the new master; or NULL
+ *   lr_mult, decay_mult   factors of the learning rate and the weight decay
+ * Buffers need the alignment of their element only; where all of a tensor's
+ * buffers are the same number of elements off a vector boundary (as parts of
+ * flat buffers are), accesses are vectors. */
+typedef struct zs_tensor {
+    const void* grad;
+    float* master;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    void* param;
+    int64_t n;
+    double lr_mult;
+    double decay_mult;
+    int32_t grad_type;
+    int32_t param_type;
+    int32_t state;
+    int32_t reserved;
+} zs_tensor;
+
+/* *sqnorm_dev (DEVICE fp64) = the sum of g^2 over every tensor, g = grad / L
+ * rounded to fp32 and L the loss scale of *ctrl_dev; squares are fp32, their
+ * sums fp64 in a fixed order.  A gradient that is not finite, or of magnitude
+ * 2^62 and more after unscaling, sets ctrl->overflow, so that the step that
+ * follows is skipped.  Only grad, grad_type and n of each tensor are used.
+ * The partial sums of up to some hundred tensors share a launch.
+ * Source: "DeepSpeed ZeRO Stages", sec. 2.1, Fact 1 (clipping); the non-finite test: the dynamic
+ *   loss-scale rule. */
+ZS_API int32_t zero_tensors_sqnorm_async(const zs_tensor* tensors, int32_t n_tensors, zs_ctrl* ctrl_dev,
+                                         double* sqnorm_dev, void* work_dev, void* stream);
+
+/* One AdamW step of every tensor, in place.  With ctrl->overflow set (by
+ * zero_tensors_sqnorm_async) nothing is written and the step is skipped: L <-
+ * max(L / 2, 1).  Otherwise, with t = ctrl->step + 1 and
+ * c = min(1, max_norm / (sqrt(*sqnorm_dev) + 1e-6)) (max_norm <= 0: c = 1 and
+ * sqnorm_dev may be NULL):
+ *   g = (grad (1 / L)) c, then m, v, u and theta as in zero_shard_step with
+ *   lr lr_mult and weight_decay decay_mult; 8-bit states as in
+ *   zero_shard_step_adam8_async, operation for operation.
+ * Every fp32 operation is one IEEE round-to-nearest step in both values of
+ * hp->math.  The last launch ends the step in the control block (ctrl->cur
+ * flips there, unused: the states are in place).  Without a norm pass the
+ * gradients are not tested.
+ * Source: "DeepSpeed ZeRO Stages", sec. 2.1, Fact 1; 8-bit states: sec. 1.2. */
+ZS_API int32_t zero_tensors_adamw_async(const zs_tensor* tensors, int32_t n_tensors, const zs_adam* hp,
+                                        double max_norm, const double* sqnorm_dev, zs_ctrl* ctrl_dev,
+                                        void* stream);
+
+/* out[j] = the value that an 8-bit state's code stands for: map[codes[j]] *
+ * scales[j / ZS_ADAM8_BLOCK] (DEVICE buffers), is_signed 1 for m, 0 for v.  For
+ * turning 8-bit states into fp32 ones.  Stream-ordered.
+ * Source: the dynamic map of Dettmers et al., "8-bit Optimizers via Block-wise Quantization". */
+ZS_API int32_t zero_adam8_dequantize(const uint8_t* codes_dev, const float* scales_dev, int64_t n,
+                                     int32_t is_signed, float* out_dev, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics.                                                              */
 /* ------------------------------------------------------------------------ */
 

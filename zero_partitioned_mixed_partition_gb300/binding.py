@@ -28,6 +28,13 @@ ZS_NOALLOC_MAX_SHARDS = 64
 ZS_QWZ_BLOCK = 256
 ZS_ADAM8_BLOCK = 2048
 ZS_MATH_IEEE, ZS_MATH_FAST = 0, 1
+ZS_F32, ZS_F16, ZS_BF16 = 0, 1, 2
+ZS_STATE_F32, ZS_STATE_U8 = 0, 1
+ZS_WORK_BYTES = 65536
+ZS_MAX_TENSORS = 16384
+ZS_POLICY_TOTALS = 5
+ZS_PREFERENCE_TOTALS = 3
+ZS_PREFERENCE_SIGMOID, ZS_PREFERENCE_HINGE, ZS_PREFERENCE_SQUARED = 0, 1, 2
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -70,6 +77,26 @@ class Sgd(ctypes.Structure):
     _fields_ = [("lr", _F64), ("momentum", _F64), ("weight_decay", _F64)]
 
 
+class Logits(ctypes.Structure):
+    _fields_ = [("data", _P), ("rows", _I64), ("vocab", _I64), ("row_stride", _I64), ("type", _I32),
+                ("reserved", _I32), ("inv_temperature", _F64)]
+
+
+class Policy(ctypes.Structure):
+    _fields_ = [("clip_low", _F64), ("clip_high", _F64), ("dual_clip", _F64), ("kl_coef", _F64),
+                ("entropy_coef", _F64)]
+
+
+class Preference(ctypes.Structure):
+    _fields_ = [("beta", _F64), ("label_smoothing", _F64), ("margin", _F64), ("kind", _I32), ("average", _I32)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("grad", _P), ("master", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P), ("param", _P),
+                ("n", _I64), ("lr_mult", _F64), ("decay_mult", _F64), ("grad_type", _I32), ("param_type", _I32),
+                ("state", _I32), ("reserved", _I32)]
+
+
 class Ctrl(ctypes.Structure):
     _fields_ = [("loss_scale", _F64), ("beta1_pow", _F64), ("beta2_pow", _F64), ("step", _I64),
                 ("skipped", _I64), ("cur", _I32), ("overflow", _I32), ("last_overflow", _I32),
@@ -109,6 +136,13 @@ _SIGNATURES = {
     "zero_adam8_maps": (_I32, [_P, _P]),
     "zero_qwz_quantize": (_I32, [_P, _I64, _P, _P, _P]),
     "zero_qwz_dequantize": (_I32, [_P, _P, _I64, _P, _P]),
+    "zero_token_logp_async": (_I32, [_P, _P, _P, _P, _P, _P]),
+    "zero_token_logp_grad_async": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "zero_policy_loss_async": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P]),
+    "zero_preference_loss_async": (_I32, [_P, _P, _P, _I64, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "zero_tensors_sqnorm_async": (_I32, [_P, _I32, _P, _P, _P, _P]),
+    "zero_tensors_adamw_async": (_I32, [_P, _I32, _P, _F64, _P, _P, _P]),
+    "zero_adam8_dequantize": (_I32, [_P, _P, _I64, _I32, _P, _P]),
     "zero_status_string": (ctypes.c_char_p, [_I32]),
     "zero_last_error": (ctypes.c_char_p, []),
     "zero_kernel_launches": (_I64, []),
@@ -631,6 +665,241 @@ def zero_qwz_dequantize(codes: torch.Tensor, scales: torch.Tensor, n: int, param
     rc = lib().zero_qwz_dequantize(_dev_ptr(codes, torch.int8, "codes"), _dev_ptr(scales, torch.float32, "scales"),
                                    int(n), _dev_ptr(params, torch.float16, "params"), _stream(stream))
     _check(rc, "zero_qwz_dequantize")
+
+
+# ------------------------------------------------------------------ losses ---
+
+_TYPES = {torch.float32: ZS_F32, torch.float16: ZS_F16, torch.bfloat16: ZS_BF16}
+
+
+def new_work(device="cuda") -> torch.Tensor:
+    """Scratch of the calls that add up over a batch (cleared; one per stream)."""
+    return torch.zeros(ZS_WORK_BYTES // 8, dtype=torch.int64, device=device)
+
+
+def _vector(t: Optional[torch.Tensor], dtype, n: int, what: str) -> Optional[int]:
+    """Device pointer of a contiguous tensor of at least n elements, or None."""
+    if t is None:
+        return None
+    ptr = _dev_ptr(t, dtype, what)
+    if t.numel() < n:
+        raise ValueError(f"{what}: {t.numel()} elements, {n} needed")
+    return ptr
+
+
+def _work_ptr(work: torch.Tensor) -> int:
+    return _vector(work, torch.int64, ZS_WORK_BYTES // 8, "work")
+
+
+def _matrix(t: torch.Tensor, what: str) -> int:
+    """Device pointer of a 2-D tensor whose rows are contiguous; any row stride."""
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise TypeError(f"{what}: expected two dimensions with contiguous rows")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    # a single row's stride is never used; torch may report any
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _logits(logits: torch.Tensor, inv_temperature: float) -> Logits:
+    ptr = _matrix(logits, "logits")
+    return Logits(ptr, logits.shape[0], logits.shape[1], _row_stride(logits), _TYPES[logits.dtype], 0,
+                  float(inv_temperature))
+
+
+def _dlogits(dlogits: torch.Tensor, logits: torch.Tensor):
+    ptr = _matrix(dlogits, "dlogits")
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        raise TypeError("dlogits: expected the logits' type and shape")
+    return ptr, _row_stride(dlogits)
+
+
+def zero_token_logp_async(logits: torch.Tensor, labels: torch.Tensor, logp: torch.Tensor,
+                          entropy: Optional[torch.Tensor] = None, saved: Optional[torch.Tensor] = None,
+                          inv_temperature: float = 1.0, stream=None):
+    """Log-probability of each row's label (and entropy) under softmax(logits *
+    inv_temperature); ``saved`` ([rows, 2] fp32) is what the gradient needs."""
+    x = _logits(logits, inv_temperature)
+    n = x.rows
+    rc = lib().zero_token_logp_async(ctypes.byref(x), _vector(labels, torch.int64, n, "labels"),
+                                     _vector(logp, torch.float32, n, "logp"),
+                                     _vector(entropy, torch.float32, n, "entropy"),
+                                     _vector(saved, torch.float32, 2 * n, "saved"), _stream(stream))
+    _check(rc, "zero_token_logp_async")
+
+
+def zero_token_logp_grad_async(logits: torch.Tensor, labels: torch.Tensor, saved: torch.Tensor,
+                               dlogp: torch.Tensor, dlogits: torch.Tensor, entropy: Optional[torch.Tensor] = None,
+                               dentropy: Optional[torch.Tensor] = None, inv_temperature: float = 1.0,
+                               ctrl_dev: Optional[torch.Tensor] = None, stream=None):
+    """Loss-scaled gradient of the logits; ``dlogits`` may be ``logits``."""
+    x = _logits(logits, inv_temperature)
+    n = x.rows
+    out, out_stride = _dlogits(dlogits, logits)
+    rc = lib().zero_token_logp_grad_async(ctypes.byref(x), _vector(labels, torch.int64, n, "labels"),
+                                          _vector(saved, torch.float32, 2 * n, "saved"),
+                                          _vector(dlogp, torch.float32, n, "dlogp"),
+                                          _vector(entropy, torch.float32, n, "entropy"),
+                                          _vector(dentropy, torch.float32, n, "dentropy"),
+                                          _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"), out, out_stride,
+                                          _stream(stream))
+    _check(rc, "zero_token_logp_grad_async")
+
+
+def policy(clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0, kl_coef: float = 0.0,
+           entropy_coef: float = 0.0) -> Policy:
+    """Coefficients of the clipped policy loss (dual_clip 0: off, else > 1)."""
+    return Policy(float(clip_low), float(clip_high), float(dual_clip), float(kl_coef), float(entropy_coef))
+
+
+def zero_policy_loss_async(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor,
+                           advantages: torch.Tensor, weights: Optional[torch.Tensor], hp: Policy,
+                           totals: torch.Tensor, work: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
+                           logp: Optional[torch.Tensor] = None, entropy: Optional[torch.Tensor] = None,
+                           token_loss: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                           inv_temperature: float = 1.0, ctrl_dev: Optional[torch.Tensor] = None, stream=None):
+    """Clipped policy loss of the rows' tokens and its loss-scaled gradient
+    (``dlogits`` None: forward only; it may be ``logits``).  ``logp`` [rows] is
+    required; ``totals``: loss, policy term, KL, entropy, clipped share."""
+    x = _logits(logits, inv_temperature)
+    n = x.rows
+    if logp is None:
+        raise ValueError("logp: an output of [rows] fp32 is needed")
+    out, out_stride = (None, 0) if dlogits is None else _dlogits(dlogits, logits)
+    f32 = torch.float32
+    rc = lib().zero_policy_loss_async(ctypes.byref(x), _vector(labels, torch.int64, n, "labels"),
+                                      _vector(old_logp, f32, n, "old_logp"),
+                                      _vector(advantages, f32, n, "advantages"),
+                                      _vector(ref_logp, f32, n, "ref_logp"), _vector(weights, f32, n, "weights"),
+                                      ctypes.byref(hp), _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"),
+                                      _vector(logp, f32, n, "logp"), _vector(entropy, f32, n, "entropy"),
+                                      _vector(token_loss, f32, n, "token_loss"), out, out_stride,
+                                      _vector(totals, f32, ZS_POLICY_TOTALS, "totals"), _work_ptr(work),
+                                      _stream(stream))
+    _check(rc, "zero_policy_loss_async")
+
+
+_PREFERENCE_KINDS = {"sigmoid": ZS_PREFERENCE_SIGMOID, "hinge": ZS_PREFERENCE_HINGE,
+                     "squared": ZS_PREFERENCE_SQUARED}
+
+
+def preference(beta: float, kind="sigmoid", label_smoothing: float = 0.0, margin: float = 0.0,
+               average: bool = False) -> Preference:
+    """Preference loss; kind "sigmoid", "hinge", "squared" or a ZS_PREFERENCE_* value."""
+    return Preference(float(beta), float(label_smoothing), float(margin), int(_PREFERENCE_KINDS.get(kind, kind)),
+                      1 if average else 0)
+
+
+def zero_preference_loss_async(logp: torch.Tensor, cu_seqlens: torch.Tensor, hp: Preference, loss: torch.Tensor,
+                               reward: torch.Tensor, totals: torch.Tensor, work: torch.Tensor,
+                               ref_logp: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                               weights: Optional[torch.Tensor] = None, dlogp: Optional[torch.Tensor] = None,
+                               stream=None):
+    """Paired preference loss over packed token log-probabilities (sequence 2 i
+    chosen, 2 i + 1 rejected) and its gradient; ``mask`` is bool or uint8."""
+    n, sequences = logp.numel(), cu_seqlens.numel() - 1
+    if sequences < 0 or sequences % 2:
+        raise ValueError("cu_seqlens: expected 2 n_pairs + 1 offsets")
+    pairs, f32 = sequences // 2, torch.float32
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"mask: expected bool or uint8, got {mask.dtype}")
+    rc = lib().zero_preference_loss_async(_dev_ptr(logp, f32, "logp"), _vector(ref_logp, f32, n, "ref_logp"),
+                                          _vector(mask, None if mask is None else mask.dtype, n, "mask"), n,
+                                          _dev_ptr(cu_seqlens, torch.int64, "cu_seqlens"),
+                                          _vector(weights, f32, pairs, "weights"), pairs, ctypes.byref(hp),
+                                          _vector(loss, f32, pairs, "loss"),
+                                          _vector(reward, f32, 2 * pairs, "reward"),
+                                          _vector(dlogp, f32, n, "dlogp"),
+                                          _vector(totals, f32, ZS_PREFERENCE_TOTALS, "totals"), _work_ptr(work),
+                                          _stream(stream))
+    _check(rc, "zero_preference_loss_async")
+
+
+# --------------------------------------------------------- lists of tensors ---
+
+class TensorView:
+    """One tensor of an AdamW step over a list, and the C struct that describes it.
+
+    grad: fp32, fp16 or bf16 CUDA tensor; master: fp32, updated in place; m, v:
+    both fp32, or both uint8 codes with m_scale, v_scale (fp32, one per
+    ZS_ADAM8_BLOCK elements); param: fp16 or bf16 copy of the weights, or None;
+    lr_mult, decay_mult: factors of the learning rate and the weight decay.
+    All contiguous, of as many elements as master (any shape)."""
+
+    def __init__(self, grad: torch.Tensor, master: torch.Tensor, m: torch.Tensor, v: torch.Tensor,
+                 param: Optional[torch.Tensor] = None, m_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, lr_mult: float = 1.0, decay_mult: float = 1.0):
+        self.grad, self.master, self.m, self.v, self.param = grad, master, m, v, param
+        self.m_scale, self.v_scale = m_scale, v_scale
+        self.n = n = master.numel()
+        if grad.dtype not in _TYPES:
+            raise TypeError(f"grad: expected float32, float16 or bfloat16, got {grad.dtype}")
+        if param is not None and param.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"param: expected float16 or bfloat16, got {param.dtype}")
+        if m.dtype not in (torch.float32, torch.uint8):
+            raise TypeError(f"m: expected float32 or uint8, got {m.dtype}")
+        small = m.dtype == torch.uint8
+        if small != (m_scale is not None) or small != (v_scale is not None):
+            raise ValueError("m_scale and v_scale go with uint8 states")
+        for t, what in ((grad, "grad"), (m, "m"), (v, "v"), (param, "param")):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"{what}: {t.numel()} elements, master has {n}")
+        blocks = (n + ZS_ADAM8_BLOCK - 1) // ZS_ADAM8_BLOCK
+        self.struct = Tensor(
+            _dev_ptr(grad, grad.dtype, "grad"), _dev_ptr(master, torch.float32, "master"), _dev_ptr(m, m.dtype, "m"),
+            _dev_ptr(v, m.dtype, "v"), _vector(m_scale, torch.float32, blocks, "m_scale"),
+            _vector(v_scale, torch.float32, blocks, "v_scale"),
+            None if param is None else _dev_ptr(param, param.dtype, "param"), n, float(lr_mult), float(decay_mult),
+            _TYPES[grad.dtype], ZS_F16 if param is None else _TYPES[param.dtype],
+            ZS_STATE_U8 if small else ZS_STATE_F32, 0)
+
+
+class TensorList:
+    """The tensors of one step, described once: the C array is kept, the
+    buffers must stay where they are (make a new list when they move)."""
+
+    def __init__(self, views: Sequence[TensorView]):
+        self.views = list(views)
+        self.array = (Tensor * max(len(self.views), 1))(*[v.struct for v in self.views])
+
+    def __len__(self) -> int:
+        return len(self.views)
+
+
+def zero_tensors_sqnorm_async(tensors: TensorList, sqnorm_dev: torch.Tensor, work: torch.Tensor,
+                              ctrl_dev: torch.Tensor, stream=None):
+    """Squared norm of the unscaled gradients into sqnorm_dev (fp64), and their
+    non-finite test into the control block."""
+    rc = lib().zero_tensors_sqnorm_async(tensors.array, len(tensors), _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"),
+                                         _dev_ptr(sqnorm_dev, torch.float64, "sqnorm_dev"), _work_ptr(work),
+                                         _stream(stream))
+    _check(rc, "zero_tensors_sqnorm_async")
+
+
+def zero_tensors_adamw_async(tensors: TensorList, hp: Adam, ctrl_dev: torch.Tensor, max_norm: float = 0.0,
+                             sqnorm_dev: Optional[torch.Tensor] = None, stream=None):
+    """AdamW step of every tensor in place, clipped to max_norm (> 0) by
+    sqnorm_dev; skipped on the device if the norm pass met a non-finite value."""
+    rc = lib().zero_tensors_adamw_async(tensors.array, len(tensors), ctypes.byref(hp), float(max_norm),
+                                        _dev_ptr(sqnorm_dev, torch.float64, "sqnorm_dev"),
+                                        _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"), _stream(stream))
+    _check(rc, "zero_tensors_adamw_async")
+
+
+def zero_adam8_dequantize(codes: torch.Tensor, scales: torch.Tensor, n: int, signed: bool, out: torch.Tensor,
+                          stream=None):
+    """fp32 values of an 8-bit state (signed: m; else v)."""
+    n = int(n)
+    rc = lib().zero_adam8_dequantize(_vector(codes, torch.uint8, n, "codes"),
+                                     _vector(scales, torch.float32, (n + ZS_ADAM8_BLOCK - 1) // ZS_ADAM8_BLOCK, "scales"),
+                                     n, 1 if signed else 0, _vector(out, torch.float32, n, "out"), _stream(stream))
+    _check(rc, "zero_adam8_dequantize")
 
 
 def read_ctrl(ctrl_dev: torch.Tensor) -> dict:

@@ -68,7 +68,8 @@ ZS_API int32_t zero_debug_checks(uint64_t* first_fault) {
     *first_fault = 0;
 #if ZS_CHECKED
     const uint64_t faults[] = {zs::take_fault_shard_step(), zs::take_fault_clip(), zs::take_fault_sgd(),
-                               zs::take_fault_adam8()};
+                               zs::take_fault_adam8(),      zs::take_fault_logits(), zs::take_fault_preference(),
+                               zs::take_fault_tensors()};
     for (uint64_t f : faults) {
         if (f == ~0ull) return zs::fail_with(ZS_ERR_CUDA, "zero_debug_checks: the fault record could not be read");
         if (f != 0 && *first_fault == 0) *first_fault = f;
