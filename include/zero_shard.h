@@ -655,7 +655,9 @@ typedef struct zs_logits {
 /* Log-probability of each row's label, and the row's entropy.  With
  * top = max_i x_i, d_i = (x_i - top) it and S = sum_i exp(d_i), all in fp32:
  *   logp = d_label - ln S,   entropy = ln S - sum_i exp(d_i) d_i / S,
- *   saved[2 row] = top,  saved[2 row + 1] = ln S   (for the gradient call).
+ *   saved[2 row] = t,  saved[2 row + 1] = ln sum_i exp((x_i - t) it)   for the
+ *   gradient call, t a logit near the row's largest (the two together give the
+ *   row's log-sum-exp, t it + saved[2 row + 1]).
  *   labels   DEVICE int64[rows]; a label outside [0, vocab) marks a row that
  *            is ignored: its logits are not read and its outputs are 0.
  *   logp, entropy, saved   DEVICE fp32 [rows], [rows], [2 rows]; entropy and

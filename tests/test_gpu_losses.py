@@ -66,7 +66,7 @@ def _forward(zs, x, y, it=1.0, **kw):
 
 SHAPES = [(1, 1, 0, 0), (3, 2, 1, 1), (5, 7, 0, 0), (4, 8, 0, 1), (7, 33, 3, 5), (2, 1000, 0, 0), (9, 4099, 5, 3),
           (3, 50257, 0, 0), (2, 50257, 47, 1), (160, 515, 0, 2), (700, 130, 0, 0), (1, 200_003, 0, 1), (2, 131072, 0, 0),
-          (1, 300_000, 0, 0)]
+          (1, 300_000, 0, 0), (2, 900_001, 0, 1)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -251,7 +251,7 @@ POLICIES = [dict(clip_low=0.2, clip_high=0.3, dual_clip=0.0, kl_coef=0.0, entrop
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("hp", POLICIES, ids=["plain", "all"])
 @pytest.mark.parametrize("rows,vocab,pad,offset", [(1, 1, 0, 0), (6, 9, 2, 1), (40, 1003, 0, 3), (5, 50257, 47, 0),
-                                                  (900, 260, 0, 0), (2, 200_001, 0, 0), (3, 131072, 0, 0)])
+                                                  (900, 260, 0, 0), (2, 200_001, 0, 0), (3, 131072, 0, 0), (2, 450_000, 0, 0), (2, 900_001, 0, 1), (3000, 1500, 0, 0)])
 def test_policy_loss(zs, cuda_device, rows, vocab, pad, offset, hp, dtype):
     x, y, old, ref, adv, g = _policy_inputs(rows, vocab, dtype, 3 * rows + vocab, pad, offset)
     ref = ref if hp["kl_coef"] else None
