@@ -4,6 +4,8 @@
 // step_end.cuh.
 #pragma once
 
+#include "packed.cuh"
+
 // ---------------------------------------------------------------- scratch ---
 
 // The caller's scratch buffer: an arrival counter, 0 between calls, and the

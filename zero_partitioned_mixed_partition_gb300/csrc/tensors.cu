@@ -21,33 +21,32 @@ namespace {
 #include "step_end.cuh"
 #include "loss_common.cuh"
 #include "adam8_math.cuh"
+#include "tensors_math.cuh"
 
 // index-check sites of this file
 [[maybe_unused]] constexpr uint32_t kSiteTensor = 14, kSiteTensorScale = 15, kSiteTensorNorm = 16;
 
 constexpr int kChunk = ZS_ADAM8_BLOCK;  // elements of a chunk: one block of 8-bit states
-constexpr int kThreads = 256;           // 8 elements each
-static_assert(kChunk == kThreads * 8, "a thread takes 8 elements of a chunk");
+constexpr int kShares = kChunk / 8;     // a chunk is taken in shares of 8 elements
 
 // ------------------------------------------------------------------ layout ---
 
-// Which elements of a chunk a thread takes, by the tensor's `peel`:
+// Which elements of a chunk a share is, by the tensor's `peel`:
 //   peel in [0, 8)  every buffer of the tensor is on a 16-byte boundary (8 for
-//                   codes) at element peel, and so at peel + 8 i: thread t < 255
-//                   takes the eight from peel + 8 t, as vectors; thread 255 takes
-//                   the chunk's edges, [0, peel) and [2040 + peel, 2048)
-//   kScattered      no such element: thread t takes t + 256 j, one at a time
+//                   codes) at element peel, and so at peel + 8 i: share v < 255
+//                   is the eight from peel + 8 v, as vectors; share 255 is the
+//                   chunk's edges, [0, peel) and [2040 + peel, 2048)
+//   kScattered      no such element: share v is v + 256 j, one at a time
 constexpr int kScattered = 8;
 
-__device__ __forceinline__ int chunk_element(int peel, int j) {
-    const int t = threadIdx.x;
-    if (peel == kScattered) return t + kThreads * j;
-    if (t < kThreads - 1) return peel + 8 * t + j;
+__device__ __forceinline__ int share_element(int peel, int v, int j) {
+    if (peel == kScattered) return v + kShares * j;
+    if (v < kShares - 1) return peel + 8 * v + j;
     return j < peel ? j : kChunk - 8 + j;
 }
-__device__ __forceinline__ bool chunk_vector(int peel, int rem) {
+__device__ __forceinline__ bool share_is_vector(int peel, int v, int rem) {
     if (peel == kScattered) return false;
-    if (threadIdx.x < kThreads - 1) return peel + 8 * (int)threadIdx.x + 8 <= rem;
+    if (v < kShares - 1) return peel + 8 * v + 8 <= rem;
     return peel == 0 && rem == kChunk;
 }
 
@@ -58,19 +57,44 @@ __device__ __forceinline__ float load_one(const void* p, int type, int64_t e) {
     const unsigned short h = __ldcs((const unsigned short*)p + e);
     return type == ZS_F16 ? __half2float(__ushort_as_half(h)) : __bfloat162float(__ushort_as_bfloat16(h));
 }
-__device__ __forceinline__ void load_grad8(const void* p, int type, int64_t e, float* g) {
+// Eight gradients as they lie in memory: 16-bit ones in w[0..3], else w[0..7].
+__device__ __forceinline__ void load_raw8(const void* p, int type, int64_t e, uint32_t* w) {
     if (type == ZS_F32) {
-        Mem<8>::load_f((const float*)p + e, g);
-    } else if (type == ZS_F16) {
-        Mem<8>::load_h((const uint16_t*)p + e, g);
+        const uint4 a = __ldcs(reinterpret_cast<const uint4*>((const float*)p + e));
+        const uint4 b = __ldcs(reinterpret_cast<const uint4*>((const float*)p + e + 4));
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     } else {
-        uint32_t w[4];
         Mem<8>::load_h_words((const uint16_t*)p + e, w);
+    }
+}
+// The same from eight fp32 values (every value of the types is one).
+__device__ __forceinline__ void raw_of(const float* g, int type, uint32_t* w) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // bf16 is the upper half of an fp32
-            g[2 * i] = __uint_as_float(w[i] << 16);
-            g[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(g[i]);
+    if (type == ZS_F32) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(g[2 * i], g[2 * i + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(g[2 * i], g[2 * i + 1]);
+        w[i] = type == ZS_F16 ? *reinterpret_cast<const uint32_t*>(&h) : *reinterpret_cast<const uint32_t*>(&b);
+    }
+}
+// As fp32 pairs.
+__device__ __forceinline__ void widen_raw(const uint32_t* w, int type, uint64_t* x) {
+    if (type == ZS_F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else if (type == ZS_F16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[i] = pair(f.x, f.y);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // bf16 is the upper half of an fp32
+            x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
 }
 __device__ __forceinline__ void store_one16(void* p, int type, int64_t e, float x) {
@@ -96,9 +120,11 @@ __device__ __forceinline__ void store_param8(void* p, int type, int64_t e, const
 struct NormEntry {
     const void* grad;
     int64_t n;
-    int32_t type, peel;
+    int32_t type;
 };
 constexpr int kNormGroup = 1024;
+constexpr int kNormThreads = 256, kNormVectors = 8;                // 16-byte vectors of a thread in a chunk
+constexpr int kNormChunk = kNormThreads * kNormVectors;            // vectors of a chunk
 
 struct NormArgs {
     NormEntry t[kNormGroup];
@@ -112,9 +138,17 @@ struct NormArgs {
 };
 static_assert(sizeof(NormArgs) <= 32764, "kernel parameters");
 
-// The tensor of chunk q: the last one whose first chunk is not above q.
-__device__ __forceinline__ int tensor_of(const uint32_t* first, int count, uint32_t q) {
-    int lo = 0, hi = count - 1;
+// The elements of a gradient before its first 16-byte vector.
+__host__ __device__ __forceinline__ int64_t norm_head(const void* grad, int size, int64_t n) {
+    const int64_t head = (int64_t)(((16u - ((uintptr_t)grad & 15u)) & 15u) / (unsigned)size);
+    return head < n ? head : n;
+}
+
+// The tensor of chunk q: the last one whose first chunk is not above q.  i: one
+// that is not past it (a block's chunks only go up, most often within a tensor).
+__device__ __forceinline__ int tensor_of(const uint32_t* first, int count, uint32_t q, int i) {
+    if (q < first[i + 1]) return i;
+    int lo = i + 1, hi = count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (first[mid] <= q) lo = mid; else hi = mid - 1;
@@ -122,59 +156,94 @@ __device__ __forceinline__ int tensor_of(const uint32_t* first, int count, uint3
     return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) tensors_sqnorm_kernel(const __grid_constant__ NormArgs p) {
-    __shared__ double s_part[kThreads / 32];
+// A sum in two fp32 parts, hi + lo: what hi's rounding drops goes to lo exactly
+// (the TwoSum of Knuth).  GB300's fp64 rate is a small part of its fp32 rate.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float p) {
+        const float s = __fadd_rn(hi, p), bp = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bp)), __fsub_rn(p, bp)));
+        hi = s;
+    }
+};
+
+// 2 or 4 bytes read for an element and some 4 instructions.  A chunk is 2048
+// vectors of one gradient, each thread's eight under way together; elements
+// outside whole vectors are taken by the first chunk of a tensor.
+__global__ void __launch_bounds__(kNormThreads) tensors_sqnorm_kernel(const __grid_constant__ NormArgs p) {
+    constexpr int kWarps = kNormThreads / 32;
+    __shared__ double s_part[kWarps];
     griddep_wait();
     griddep_launch_dependents();
     const float inv = __double2float_rn(__ddiv_rn(1.0, p.ctrl->loss_scale));
-    double sum = 0.0;
+    const uint64_t inv2 = pair(inv, inv);
+    Sum2 sum{0.0f, 0.0f};
     bool bad = false;
     const uint32_t total = p.first[p.count];
+    int i = 0;
+    // eight squares, or four: a gradient too large, an infinity or a NaN shows
+    auto add = [&](uint64_t part) {
+        float a, b;
+        split(part, a, b);
+        a = __fadd_rn(a, b);
+        bad |= !(a < 0x1p124f);
+        sum.add(a);
+    };
     for (uint32_t q = blockIdx.x; q < total; q += gridDim.x) {
-        const NormEntry& t = p.t[tensor_of(p.first, p.count, q)];
-        const int64_t at = (int64_t)(q - p.first[&t - p.t]) * kChunk;
-        const int rem = (int)(t.n - at < kChunk ? t.n - at : kChunk);
-        float g[8];
-        if (chunk_vector(t.peel, rem) && ZS_RANGE_OK(kSiteTensorNorm, at + chunk_element(t.peel, 0), 8, t.n)) {
-            load_grad8(t.grad, t.type, at + chunk_element(t.peel, 0), g);
-        } else {
+        i = tensor_of(p.first, p.count, q, i);
+        const NormEntry& t = p.t[i];
+        const int type = t.type, size = type == ZS_F32 ? 4 : 2;
+        const int64_t n = t.n, head = norm_head(t.grad, size, n), nvec = (n - head) * size / 16;
+        const uint32_t c = q - p.first[i];
+        const uint4* v = reinterpret_cast<const uint4*>((const char*)t.grad + head * size);
+        uint4 r[kNormVectors];
+        const int64_t v0 = (int64_t)c * kNormChunk + threadIdx.x;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = chunk_element(t.peel, j);
-                g[j] = e < rem && ZS_RANGE_OK(kSiteTensorNorm, at + e, 1, t.n) ? load_one(t.grad, t.type, at + e) : 0.0f;
+        for (int k = 0; k < kNormVectors; ++k) {
+            const int64_t x = v0 + k * kNormThreads;
+            const bool have = x < nvec && ZS_RANGE_OK(kSiteTensorNorm, head + x * (16 / size), 16 / size, n);
+            r[k] = have ? __ldcs(v + x) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (c == 0 && threadIdx.x < 16) {  // the head's elements, and the tail's
+            const int64_t e = threadIdx.x < 8 ? (int64_t)threadIdx.x : head + nvec * (16 / size) + threadIdx.x - 8;
+            if ((threadIdx.x < 8 ? e < head : e < n) && ZS_RANGE_OK(kSiteTensorNorm, e, 1, n)) {
+                const float x = __fmul_rn(load_one(t.grad, type, e), inv);
+                add(pair(__fmul_rn(x, x), 0.0f));
             }
         }
-        float part = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float x = __fmul_rn(g[j], inv);
-            bad |= !(fabsf(x) < 0x1p62f);  // also a NaN
-            part = __fmaf_rn(x, x, part);
+        for (int k = 0; k < kNormVectors; ++k) {
+            const uint32_t w[8] = {r[k].x, r[k].y, r[k].z, r[k].w, 0u, 0u, 0u, 0u};
+            uint64_t x[4], part = 0ull;
+            widen_raw(w, type, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= 2 && type == ZS_F32) break;
+                x[j] = mul2(x[j], inv2);
+                part = fma2(x[j], x[j], part);
+            }
+            add(part);
         }
-        sum += (double)part;
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(&p.ctrl->overflow, 1);
-    sum = warp_sum(sum);
-    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double b = 0.0;
-        for (int w = 0; w < kThreads / 32; ++w) b += s_part[w];
-        p.work->part[p.base + blockIdx.x] = b;
-    }
+    auto block_sum = [&](double x) {  // in the first thread; the order is fixed
+        x = warp_sum(x);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = x;
+        __syncthreads();
+        x = 0.0;
+        if (threadIdx.x == 0)
+            for (int w = 0; w < kWarps; ++w) x += s_part[w];
+        return x;
+    };
+    const double block = block_sum((double)sum.hi + (double)sum.lo);
+    if (threadIdx.x == 0) p.work->part[p.base + blockIdx.x] = block;
     if (!p.finish || !last_to_arrive(p.work, gridDim.x)) return;
-    sum = 0.0;
+    double all = 0.0;
     const int parts = p.base + (int)gridDim.x;
-    for (int i = threadIdx.x; i < parts; i += kThreads) sum += *(volatile double*)&p.work->part[i];
-    sum = warp_sum(sum);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double b = 0.0;
-        for (int w = 0; w < kThreads / 32; ++w) b += s_part[w];
-        *p.out = b;
-    }
+    for (int k = threadIdx.x; k < parts; k += kNormThreads) all += *(volatile double*)&p.work->part[k];
+    all = block_sum(all);
+    if (threadIdx.x == 0) *p.out = all;
 }
 
 // ------------------------------------------------------------------ update ---
@@ -202,6 +271,7 @@ struct StepShared {
     zs_ctrl* ctrl;
     int32_t count;
     int32_t finish;  // the call's last launch ends the step in the control block
+    float one;       // 1: see add2_apart
 };
 template <typename Entry, int G>
 struct StepArgs : StepShared {
@@ -233,163 +303,406 @@ __device__ __forceinline__ void step_coef(const StepShared& p, StepCoef* s) {
     s->skip = ctrl->overflow;
 }
 
-__global__ void __launch_bounds__(kThreads) tensors_adamw_kernel(const __grid_constant__ StepArgs32 p) {
+// The step's coefficients twice each, for pairs of elements.
+struct Coef2 {
+    uint64_t b1, c1, b2, c2, inv, clip, one;
+    float bc1, bc2, rcp_bc1, rcp_bc2, eps;
+};
+__device__ __forceinline__ Coef2 coef2_of(const StepCoef& s, float one) {
+    return Coef2{pair(s.c.b1, s.c.b1), pair(s.c.c1, s.c.c1), pair(s.c.b2, s.c.b2), pair(s.c.c2, s.c.c2),
+                 pair(s.c.inv, s.c.inv), pair(s.clip, s.clip), pair(one, one), s.c.bc1, s.c.bc2, __frcp_rn(s.c.bc1),
+                 __frcp_rn(s.c.bc2), s.c.eps};
+}
+
+// a + b for products of pairs that have been rounded: as a 1 + b, with a 1 that
+// the compiler does not see.  It makes one fused multiply-add of a packed
+// product and a packed sum, rounding modifiers or not, and m and v came out a
+// unit of the last place off.
+__device__ __forceinline__ uint64_t add2_apart(uint64_t a, uint64_t b, uint64_t one) { return fma2(a, one, b); }
+
+// The Adam / AdamW update of eight coordinates from their gradients (raw, as
+// pairs): the operations of adam_apply, two coordinates at a time.  Divisions and
+// square roots are the correctly rounded ones above where all of a warp's values
+// lie in [2^-80, 2^40], with any bias correction in their ranges, and else the
+// scalar ones.  m, v: in and out, as pairs.
+__device__ __forceinline__ void adam_eight(const Coef2& c, float lr, float wd, const uint64_t* g, float* th, uint64_t* m,
+                                           uint64_t* v) {
+    float low = 1.0f, high = 0.0f;  // the smallest and largest |m'|, v'
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint64_t x = mul2(mul2(g[j], c.inv), c.clip);
+        m[j] = add2_apart(mul2(c.b1, m[j]), mul2(c.c1, x), c.one);
+        v[j] = add2_apart(mul2(c.b2, v[j]), mul2(c.c2, mul2(x, x)), c.one);
+        float a, b, p, q;
+        split(m[j], a, b);
+        split(v[j], p, q);
+        low = fminf(fminf(low, fminf(fabsf(a), fabsf(b))), fminf(p, q));
+        high = fmaxf(fmaxf(high, fmaxf(fabsf(a), fabsf(b))), fmaxf(p, q));
+    }
+    if (__any_sync(0xffffffffu, !(low >= 0x1p-80f && high <= 0x1p40f))) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float a[2], p[2];
+            split(m[j / 2], a[0], a[1]);
+            split(v[j / 2], p[0], p[1]);
+            const float u = __fdiv_rn(__fdiv_rn(a[j & 1], c.bc1), __fadd_rn(__fsqrt_rn(__fdiv_rn(p[j & 1], c.bc2)), c.eps));
+            th[j] = __fsub_rn(th[j], __fmul_rn(lr, __fadd_rn(u, __fmul_rn(wd, th[j]))));
+        }
+        return;
+    }
+    const uint64_t eps = pair(c.eps, c.eps);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint64_t mh = div2_by_constant(m[j], c.bc1, c.rcp_bc1), vh = div2_by_constant(v[j], c.bc2, c.rcp_bc2);
+        float u0, u1;
+        split(div2(mh, add2(sqrt2(vh), eps)), u0, u1);
+        th[2 * j] = __fsub_rn(th[2 * j], __fmul_rn(lr, __fadd_rn(u0, __fmul_rn(wd, th[2 * j]))));
+        th[2 * j + 1] = __fsub_rn(th[2 * j + 1], __fmul_rn(lr, __fadd_rn(u1, __fmul_rn(wd, th[2 * j + 1]))));
+    }
+}
+
+// Where a chunk is: its tensor, its first element there and its length.
+struct Place {
+    int i;
+    int64_t at;
+    int rem;
+};
+template <typename Args>
+__device__ __forceinline__ Place place_of(const Args& p, uint32_t q, int from) {
+    const int i = tensor_of(p.first, p.count, q, from);
+    const int64_t at = (int64_t)(q - p.first[i]) * kChunk, left = p.t[i].n - at;
+    return Place{i, at, (int)(left < kChunk ? left : kChunk)};
+}
+
+// Threads of the step's blocks and blocks of an SM.  fp32 states, 1200 tensors of
+// 94 M elements in all, with the norm: 493 us so, 509 us with four blocks of 128
+// threads (two vectors each), 532 us with four of 256 (64 registers).  8-bit
+// states, 667 M elements: two blocks' shares to a thread (128 threads) was slower
+// by half, and so was copying the next block ahead into registers: the step is
+// bound by instructions, whose latencies take the 32 warps of four blocks.
+constexpr int kThreads32 = 256, kBlocks32 = 3, kThreads8 = 256, kBlocks8 = 4;
+
+// fp32 states have no blocks, so their chunks start at the tensor's first vector
+// boundary; the elements before it and after the last whole vector, at most
+// seven each, are taken one to a thread by the first chunk.
+__host__ __device__ __forceinline__ int64_t chunks_of(int64_t n, int peel) {
+    const int64_t body = n - (peel == kScattered ? 0 : peel);
+    return body > kChunk ? (body + kChunk - 1) / kChunk : 1;
+}
+
+// 28 bytes in and out for an element with a 16-bit gradient and copy, and some
+// 45 instructions.
+__global__ void __launch_bounds__(kThreads32, kBlocks32) tensors_adamw_kernel(const __grid_constant__ StepArgs32 p) {
+    constexpr int kPer = kChunk / 8 / kThreads32;  // vectors of a thread in a chunk
     __shared__ StepCoef s_coef;
     griddep_wait();
     griddep_launch_dependents();
     if (threadIdx.x == 0) step_coef(p, &s_coef);
     __syncthreads();
-    Coef c = s_coef.c;
-    const float clip = s_coef.clip;
+    const Coef2 c = coef2_of(s_coef, p.one);
     const uint32_t total = s_coef.skip ? 0u : p.first[p.count];
+    int i = 0;
     for (uint32_t q = blockIdx.x; q < total; q += gridDim.x) {
-        const int i = tensor_of(p.first, p.count, q);
+        i = tensor_of(p.first, p.count, q, i);
         const StepEntry& t = p.t[i];
-        const int64_t at = (int64_t)(q - p.first[i]) * kChunk;
-        const int rem = (int)(t.n - at < kChunk ? t.n - at : kChunk);
-        c.lr = t.lr;
-        c.wd = t.wd;
-        if (chunk_vector(t.peel, rem) && ZS_RANGE_OK(kSiteTensor, at + chunk_element(t.peel, 0), 8, t.n)) {
-            const int64_t e = at + chunk_element(t.peel, 0);
-            float g[8], th[8], m[8], v[8];
-            load_grad8(t.grad, t.grad_type, e, g);
-            Mem<8>::load_f(t.master + e, th);
-            Mem<8>::load_f(t.m + e, m);
-            Mem<8>::load_f(t.v + e, v);
+        const int64_t n = t.n;
+        const int peel = t.peel, type = t.grad_type;
+        const uint32_t chunk = q - p.first[i];
+        const float lr = t.lr, wd = t.wd;
+        auto one = [&](int64_t e) {
+            if (e >= n || !ZS_RANGE_OK(kSiteTensor, e, 1, n)) return;
+            float th = __ldcs(t.master + e), m = __ldcs(t.m + e), v = __ldcs(t.v + e);
+            Coef k = s_coef.c;
+            k.lr = lr;
+            k.wd = wd;
+            adam_apply<false>(k, __fmul_rn(__fmul_rn(load_one(t.grad, type, e), k.inv), s_coef.clip), th, m, v);
+            __stcs(t.master + e, th);
+            __stcs(t.m + e, m);
+            __stcs(t.v + e, v);
+            if (t.param != nullptr) store_one16(t.param, t.param_type, e, th);
+        };
+        if (peel == kScattered) {
+            for (int j = threadIdx.x; j < kChunk; j += kThreads32) one((int64_t)chunk * kChunk + j);
+            continue;
+        }
+        const int64_t e0 = peel + (int64_t)chunk * kChunk + 8 * threadIdx.x;
+        uint32_t w[kPer][8];
+        float th[kPer][8], m8[kPer][8], v8[kPer][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) adam_apply<false>(c, __fmul_rn(__fmul_rn(g[j], c.inv), clip), th[j], m[j], v[j]);
-            Mem<8>::store_f(t.master + e, th);
-            Mem<8>::store_f(t.m + e, m);
-            Mem<8>::store_f(t.v + e, v);
-            if (t.param != nullptr) store_param8(t.param, t.param_type, e, th);
-        } else {
+        for (int h = 0; h < kPer; ++h) {
+            const int64_t e = e0 + 8 * h * kThreads32;
+            if (e + 8 <= n && ZS_RANGE_OK(kSiteTensor, e, 8, n)) {
+                load_raw8(t.grad, type, e, w[h]);
+                Mem<8>::load_f(t.master + e, th[h]);
+                Mem<8>::load_f(t.m + e, m8[h]);
+                Mem<8>::load_f(t.v + e, v8[h]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = chunk_element(t.peel, j);
-                const int64_t e = at + k;
-                if (k >= rem || !ZS_RANGE_OK(kSiteTensor, e, 1, t.n)) continue;
-                float th = __ldcs(t.master + e), m = __ldcs(t.m + e), v = __ldcs(t.v + e);
-                const float g = load_one(t.grad, t.grad_type, e);
-                adam_apply<false>(c, __fmul_rn(__fmul_rn(g, c.inv), clip), th, m, v);
-                __stcs(t.master + e, th);
-                __stcs(t.m + e, m);
-                __stcs(t.v + e, v);
-                if (t.param != nullptr) store_one16(t.param, t.param_type, e, th);
+                for (int j = 0; j < 8; ++j) {  // not there: anything harmless
+                    w[h][j] = 0u;
+                    th[h][j] = 0.0f;
+                    m8[h][j] = v8[h][j] = 1.0f;
+                }
+            }
+        }
+        if (chunk == 0 && threadIdx.x < 16) {
+            const int64_t tail = n > peel ? n - (n - peel) % 8 : n;
+            const int64_t e = threadIdx.x < 8 ? (int64_t)threadIdx.x : tail + threadIdx.x - 8;
+            if (threadIdx.x >= 8 || e < peel) one(e);
+        }
+#pragma unroll
+        for (int h = 0; h < kPer; ++h) {
+            uint64_t g[4], m[4], v[4];
+            widen_raw(w[h], type, g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[j] = pair(m8[h][2 * j], m8[h][2 * j + 1]);
+                v[j] = pair(v8[h][2 * j], v8[h][2 * j + 1]);
+            }
+            adam_eight(c, lr, wd, g, th[h], m, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                split(m[j], m8[h][2 * j], m8[h][2 * j + 1]);
+                split(v[j], v8[h][2 * j], v8[h][2 * j + 1]);
+            }
+            const int64_t e = e0 + 8 * h * kThreads32;
+            if (e + 8 <= n && ZS_RANGE_OK(kSiteTensor, e, 8, n)) {
+                Mem<8>::store_f(t.master + e, th[h]);
+                Mem<8>::store_f(t.m + e, m8[h]);
+                Mem<8>::store_f(t.v + e, v8[h]);
+                if (t.param != nullptr) store_param8(t.param, t.param_type, e, th[h]);
             }
         }
     }
     if (p.finish && threadIdx.x == 0) arrive_and_finish(p.ctrl, gridDim.x, p.hp.beta1, p.hp.beta2);
 }
 
-// Sum-free block maximum of two non-negative floats by their bit patterns.
-__device__ __forceinline__ void block_max2(float& a, float& b, uint32_t (&slots)[2][kThreads / 32]) {
-    const uint32_t wa = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
-    const uint32_t wb = __reduce_max_sync(0xffffffffu, __float_as_uint(b));
-    __syncthreads();  // the last chunk's maxima have been read
-    if ((threadIdx.x & 31) == 0) {
-        slots[0][threadIdx.x >> 5] = wa;
-        slots[1][threadIdx.x >> 5] = wb;
+// The nearest-code search of adam8_math.cuh with a bucket's threshold and code
+// in one 8-byte entry, and without the octaves below each map's lowest
+// threshold (5e-7 and 5e-8).
+constexpr int kOctaves7 = 21, kOctaves8 = 25;
+constexpr int kLut7 = kOctaves7 * (1 << kMantBits) + 1, kLut8 = kOctaves8 * (1 << kMantBits) + 1;
+struct CodeTables {
+    uint2 lut7[kLut7], lut8[kLut8];  // {threshold, number of thresholds below the bucket}
+    float dec7[256], mag8[256], thr7[128], thr8[256];
+};
+template <int OCTAVES>
+__device__ __forceinline__ uint32_t lut_code(float a, const uint2* lut) {
+    constexpr uint32_t lowest = (uint32_t)(127 - OCTAVES) << 23;
+    a = fmaxf(a, __uint_as_float(lowest));  // (a NaN becomes the lowest: code 0)
+    const uint2 e = lut[(__float_as_uint(a) - lowest) >> kBucketShift];
+    return e.y + (a > __uint_as_float(e.x) ? 1u : 0u);
+}
+// From the thresholds: thr[k] lies in bucket b_k, and the buckets above b_(k-1)
+// up to b_k have k thresholds below them.  One k to a thread; the buckets below
+// the lowest threshold and above the highest are the first's and the last's.
+template <int OCTAVES, int COUNT, int SIZE>
+__device__ __forceinline__ void build_lut(const float (&thr)[COUNT], uint2 (&lut)[SIZE]) {
+    constexpr uint32_t lowest = (uint32_t)(127 - OCTAVES) << 23;
+    auto bucket = [&](int k) { return (int)((__float_as_uint(thr[k]) - lowest) >> kBucketShift); };
+    for (int k = threadIdx.x; k < COUNT; k += blockDim.x) {
+        const int from = k == 0 ? 0 : bucket(k - 1) + 1, to = k == COUNT - 1 ? SIZE - 1 : bucket(k);
+        for (int b = from; b <= to; ++b) lut[b] = make_uint2(__float_as_uint(thr[k]), (uint32_t)k);
     }
-    __syncthreads();
-    uint32_t ma = 0u, mb = 0u;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        ma = max(ma, slots[0][w]);
-        mb = max(mb, slots[1][w]);
-    }
-    a = __uint_as_float(ma);
-    b = __uint_as_float(mb);
 }
 
-__global__ void __launch_bounds__(kThreads) tensors_adamw8_kernel(const __grid_constant__ StepArgs8 p) {
-    __shared__ StepCoef s_coef;
-    __shared__ Maps s_maps;
-    __shared__ uint32_t s_max[2][kThreads / 32];
-    {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(&p.maps);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(&s_maps);
-        for (int i = threadIdx.x; i < (int)(sizeof(Maps) / 4); i += kThreads) dst[i] = src[i];
+// A thread's shares of a chunk with 8-bit states, as they lie in memory.
+template <int kPerThread>
+struct Shares8 {
+    uint32_t g[kPerThread][8];
+    float th[kPerThread][8];
+    uint2 cm[kPerThread], cv[kPerThread];
+    float ms, vs;
+};
+template <int kPerThread>
+__device__ __forceinline__ void load_shares8(const StepEntry8& t, const Place& at, Shares8<kPerThread>& s) {
+    constexpr int kStepThreads = kShares / kPerThread;
+    const int64_t block = at.at / kChunk;
+    const int peel = t.peel, type = t.grad_type;
+    const void* grad = (const char*)t.grad + at.at * (type == ZS_F32 ? 4 : 2);
+    const float* master = t.master + at.at;
+    const uint8_t *mc = t.m_codes() + at.at, *vc = t.v_codes() + at.at;
+    [[maybe_unused]] const int64_t left = t.n - at.at;
+    const bool scale_ok = ZS_RANGE_OK(kSiteTensorScale, block, 1, (t.n + kChunk - 1) / kChunk);
+    s.ms = scale_ok ? __ldcs(t.m_scale + block) : 0.0f;
+    s.vs = scale_ok ? __ldcs(t.v_scale + block) : 0.0f;
+#pragma unroll
+    for (int h = 0; h < kPerThread; ++h) {
+        const int v = threadIdx.x + h * kStepThreads, e = share_element(peel, v, 0);
+        if (share_is_vector(peel, v, at.rem) && ZS_RANGE_OK(kSiteTensor, e, 8, left)) {
+            load_raw8(grad, type, e, s.g[h]);
+            Mem<8>::load_f(master + e, s.th[h]);
+            s.cm[h] = __ldcs(reinterpret_cast<const uint2*>(mc + e));
+            s.cv[h] = __ldcs(reinterpret_cast<const uint2*>(vc + e));
+        } else {
+            // (elements that are not there: code 0, gradient 0; their m' = v' = 0
+            // changes no block maximum)
+            float g[8];
+            uint32_t cm[8], cv[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = share_element(peel, v, j);
+                const bool have = k < at.rem && ZS_RANGE_OK(kSiteTensor, k, 1, left);
+                g[j] = have ? load_one(grad, type, k) : 0.0f;
+                s.th[h][j] = have ? __ldcs(master + k) : 0.0f;
+                cm[j] = have ? mc[k] : 0u;
+                cv[j] = have ? vc[k] : 0u;
+            }
+            raw_of(g, type, s.g[h]);
+            s.cm[h] = make_uint2(cm[0] | cm[1] << 8 | cm[2] << 16 | cm[3] << 24, cm[4] | cm[5] << 8 | cm[6] << 16 | cm[7] << 24);
+            s.cv[h] = make_uint2(cv[0] | cv[1] << 8 | cv[2] << 16 | cv[3] << 24, cv[4] | cv[5] << 8 | cv[6] << 16 | cv[7] << 24);
+        }
     }
+}
+
+// 8-bit states: 16 bytes in and out for an element with a 16-bit gradient and
+// copy, but some 80 instructions, which bound it; so pairs of elements share
+// instructions where they can.  A chunk is a block of states: its largest |m'|
+// and v' take one barrier (the slots alternate). 
+__global__ void __launch_bounds__(kThreads8, kBlocks8) tensors_adamw8_kernel(const __grid_constant__ StepArgs8 p) {
+    constexpr int kStepThreads = kThreads8, kPerThread = kShares / kStepThreads, kWarps = kStepThreads / 32;
+    extern __shared__ __align__(16) unsigned char s_dynamic[];
+    CodeTables& s_tab = *reinterpret_cast<CodeTables*>(s_dynamic);
+    __shared__ StepCoef s_coef;
+    __shared__ __align__(16) uint32_t s_max[2][2][kWarps];
+    static_assert(kWarps % 4 == 0, "the warps' maxima are read four at a time");
+    // the tables, from the kernel parameters; global memory only from here
+    for (int i = threadIdx.x; i < 256; i += kStepThreads) {
+        s_tab.dec7[i] = p.maps.dec7[i];
+        s_tab.mag8[i] = p.maps.mag8[i];
+        s_tab.thr8[i] = p.maps.thr8[i];
+        if (i < 128) s_tab.thr7[i] = p.maps.thr7[i];
+    }
+    __syncthreads();
+    build_lut<kOctaves7>(s_tab.thr7, s_tab.lut7);
+    build_lut<kOctaves8>(s_tab.thr8, s_tab.lut8);
     griddep_wait();
     griddep_launch_dependents();
     if (threadIdx.x == 0) step_coef(p, &s_coef);
     __syncthreads();
-    Coef c = s_coef.c;
-    const float clip = s_coef.clip;
+    const Coef2 c = coef2_of(s_coef, p.one);
     const uint32_t total = s_coef.skip ? 0u : p.first[p.count];
-    for (uint32_t q = blockIdx.x; q < total; q += gridDim.x) {
-        const int i = tensor_of(p.first, p.count, q);
-        const StepEntry8& t = p.t[i];
-        const int64_t block = q - p.first[i], at = block * kChunk;
-        const int rem = (int)(t.n - at < kChunk ? t.n - at : kChunk);
-        c.lr = t.lr;
-        c.wd = t.wd;
-        const bool scale_ok = ZS_RANGE_OK(kSiteTensorScale, block, 1, (t.n + kChunk - 1) / kChunk);
-        const float ms = scale_ok ? t.m_scale[block] : 0.0f, vs = scale_ok ? t.v_scale[block] : 0.0f;
-        float m[8], v[8], am = 0.0f, av = 0.0f;
-        const bool wide = chunk_vector(t.peel, rem) && ZS_RANGE_OK(kSiteTensor, at + chunk_element(t.peel, 0), 8, t.n);
-        if (wide) {
-            const int64_t e = at + chunk_element(t.peel, 0);
-            float g[8], th[8];
-            load_grad8(t.grad, t.grad_type, e, g);
-            Mem<8>::load_f(t.master + e, th);
-            const uint2 cm = __ldcs(reinterpret_cast<const uint2*>(t.m_codes() + e));
-            const uint2 cv = __ldcs(reinterpret_cast<const uint2*>(t.v_codes() + e));
+    int par = 0;
+    Place at{0, 0, 0};
+    if (blockIdx.x < total) at = place_of(p, blockIdx.x, 0);
+    for (uint32_t q = blockIdx.x; q < total; q += gridDim.x, par ^= 1) {
+        const StepEntry8& t = p.t[at.i];
+        const int64_t block = at.at / kChunk;
+        const int peel = t.peel, type = t.grad_type, rem = at.rem, param_type = t.param_type;
+        float* master = t.master + at.at;
+        uint8_t *mc = t.m_codes() + at.at, *vc = t.v_codes() + at.at;
+        uint16_t* param = t.param == nullptr ? nullptr : (uint16_t*)t.param + at.at;
+        float *m_scale = t.m_scale + block, *v_scale = t.v_scale + block;
+        const float lr = t.lr, wd = t.wd;
+        [[maybe_unused]] const int64_t left = t.n - at.at;
+        Shares8<kPerThread> s;
+        load_shares8<kPerThread>(t, at, s);
+        if (q + gridDim.x < total) at = place_of(p, q + gridDim.x, at.i);
+        uint64_t g[kPerThread][4], m[kPerThread][4], v2[kPerThread][4];
+        const uint64_t ms = pair(s.ms, s.ms), vs = pair(s.vs, s.vs);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                m[j] = __fmul_rn(s_maps.dec7[__byte_perm(j < 4 ? cm.x : cm.y, 0u, 0x4440u + (j & 3))], ms);
-                v[j] = __fmul_rn(s_maps.mag8[__byte_perm(j < 4 ? cv.x : cv.y, 0u, 0x4440u + (j & 3))], vs);
-                adam_apply<false>(c, __fmul_rn(__fmul_rn(g[j], c.inv), clip), th[j], m[j], v[j]);
-            }
-            Mem<8>::store_f(t.master + e, th);
-            if (t.param != nullptr) store_param8(t.param, t.param_type, e, th);
-        } else {
+        for (int h = 0; h < kPerThread; ++h) {
+            widen_raw(s.g[h], type, g[h]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = chunk_element(t.peel, j);
-                const int64_t e = at + k;
-                m[j] = v[j] = 0.0f;  // changes no block maximum
-                if (k >= rem || !ZS_RANGE_OK(kSiteTensor, e, 1, t.n)) continue;
-                m[j] = __fmul_rn(s_maps.dec7[t.m_codes()[e]], ms);
-                v[j] = __fmul_rn(s_maps.mag8[t.v_codes()[e]], vs);
-                float th = __ldcs(t.master + e);
-                const float g = load_one(t.grad, t.grad_type, e);
-                adam_apply<false>(c, __fmul_rn(__fmul_rn(g, c.inv), clip), th, m[j], v[j]);
-                __stcs(t.master + e, th);
-                if (t.param != nullptr) store_one16(t.param, t.param_type, e, th);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t wm = j < 2 ? s.cm[h].x : s.cm[h].y, wv = j < 2 ? s.cv[h].x : s.cv[h].y;
+                const int b = 2 * (j & 1);
+                m[h][j] = mul2(pair(s_tab.dec7[__byte_perm(wm, 0u, 0x4440u + b)], s_tab.dec7[__byte_perm(wm, 0u, 0x4441u + b)]), ms);
+                v2[h][j] = mul2(pair(s_tab.mag8[__byte_perm(wv, 0u, 0x4440u + b)], s_tab.mag8[__byte_perm(wv, 0u, 0x4441u + b)]), vs);
             }
         }
+        float am = 0.0f, av = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            am = fmaxf(am, fabsf(m[j]));
-            av = fmaxf(av, v[j]);
-        }
-        block_max2(am, av, s_max);
-        uint32_t cm[8], cv[8];
+        for (int h = 0; h < kPerThread; ++h) {
+            adam_eight(c, lr, wd, g[h], s.th[h], m[h], v2[h]);
+            const int v = threadIdx.x + h * kStepThreads, e = share_element(peel, v, 0);
+            if (share_is_vector(peel, v, rem) && ZS_RANGE_OK(kSiteTensor, e, 8, left)) {
+                Mem<8>::store_f(master + e, s.th[h]);
+                if (param != nullptr) store_param8(param, param_type, e, s.th[h]);
+            } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float xm = am > 0.0f ? __fdiv_rn(m[j], am) : 0.0f, xv = av > 0.0f ? __fdiv_rn(v[j], av) : 0.0f;
-            const uint32_t k = nearest_code(fabsf(xm), s_maps.thr7, s_maps.bucket7);
-            cm[j] = xm < 0.0f && k > 0u ? k | 0x80u : k;
-            cv[j] = nearest_code(xv, s_maps.thr8, s_maps.bucket8);
-        }
-        if (wide) {
-            const int64_t e = at + chunk_element(t.peel, 0);
-            auto four = [](const uint32_t* x) { return x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24; };
-            __stcs(reinterpret_cast<uint2*>(t.m_codes() + e), make_uint2(four(cm), four(cm + 4)));
-            __stcs(reinterpret_cast<uint2*>(t.v_codes() + e), make_uint2(four(cv), four(cv + 4)));
-        } else {
+                for (int j = 0; j < 8; ++j) {
+                    const int k = share_element(peel, v, j);
+                    if (k >= rem || !ZS_RANGE_OK(kSiteTensor, k, 1, left)) continue;
+                    __stcs(master + k, s.th[h][j]);
+                    if (param != nullptr) store_one16(param, param_type, k, s.th[h][j]);
+                }
+            }
+            // the block's largest |m'| and v', by their bit patterns
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = chunk_element(t.peel, j);
-                if (k >= rem || !ZS_RANGE_OK(kSiteTensor, at + k, 1, t.n)) continue;
-                t.m_codes()[at + k] = (uint8_t)cm[j];
-                t.v_codes()[at + k] = (uint8_t)cv[j];
+            for (int j = 0; j < 4; ++j) {
+                float a, b;
+                split(m[h][j], a, b);
+                am = fmaxf(am, fmaxf(fabsf(a), fabsf(b)));
+                split(v2[h][j], a, b);
+                av = fmaxf(av, fmaxf(a, b));
             }
         }
-        if (threadIdx.x == 0 && scale_ok) {
-            t.m_scale[block] = am;
-            t.v_scale[block] = av;
+        const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+        const uint32_t wv = __reduce_max_sync(0xffffffffu, __float_as_uint(av));
+        if ((threadIdx.x & 31) == 0) {
+            s_max[par][0][threadIdx.x >> 5] = wm;
+            s_max[par][1][threadIdx.x >> 5] = wv;
+        }
+        __syncthreads();  // one barrier per block: a parity's slots are not rewritten before every warp read them
+        uint32_t bm = 0u, bv = 0u;
+#pragma unroll
+        for (int w = 0; w < kWarps; w += 4) {
+            const uint4 a = *reinterpret_cast<const uint4*>(&s_max[par][0][w]), b = *reinterpret_cast<const uint4*>(&s_max[par][1][w]);
+            bm = max(bm, max(max(a.x, a.y), max(a.z, a.w)));
+            bv = max(bv, max(max(b.x, b.y), max(b.z, b.w)));
+        }
+        am = __uint_as_float(bm);
+        av = __uint_as_float(bv);
+        // codes of m' / am and v' / av, each quotient rounded once
+        const bool usual = scale_divisor_ok(am) && scale_divisor_ok(av);
+        float rm = 0.0f, rv = 0.0f;
+        if (usual) split(reciprocal2(pair(am, av)), rm, rv);
+#pragma unroll
+        for (int h = 0; h < kPerThread; ++h) {
+            uint32_t cm[8], cv[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x[2], y[2];
+                if (usual) {
+                    split(div2_by_constant(m[h][j], am, rm), x[0], x[1]);
+                    split(div2_by_constant(v2[h][j], av, rv), y[0], y[1]);
+                } else {
+                    split(m[h][j], x[0], x[1]);
+                    split(v2[h][j], y[0], y[1]);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        x[b] = am > 0.0f ? __fdiv_rn(x[b], am) : 0.0f;
+                        y[b] = av > 0.0f ? __fdiv_rn(y[b], av) : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t k = lut_code<kOctaves7>(fabsf(x[b]), s_tab.lut7);
+                    cm[2 * j + b] = x[b] < 0.0f && k > 0u ? k | 0x80u : k;
+                    cv[2 * j + b] = lut_code<kOctaves8>(y[b], s_tab.lut8);
+                }
+            }
+            const int v = threadIdx.x + h * kStepThreads, e = share_element(peel, v, 0);
+            if (share_is_vector(peel, v, rem) && ZS_RANGE_OK(kSiteTensor, e, 8, left)) {
+                auto four = [](const uint32_t* x) {
+                    return __byte_perm(__byte_perm(x[0], x[1], 0x0040u), __byte_perm(x[2], x[3], 0x0040u), 0x5410u);
+                };
+                __stcs(reinterpret_cast<uint2*>(mc + e), make_uint2(four(cm), four(cm + 4)));
+                __stcs(reinterpret_cast<uint2*>(vc + e), make_uint2(four(cv), four(cv + 4)));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int k = share_element(peel, v, j);
+                    if (k >= rem || !ZS_RANGE_OK(kSiteTensor, k, 1, left)) continue;
+                    mc[k] = (uint8_t)cm[j];
+                    vc[k] = (uint8_t)cv[j];
+                }
+            }
+        }
+        if (threadIdx.x == 0 && ZS_RANGE_OK(kSiteTensorScale, block, 1, (left + block * kChunk + kChunk - 1) / kChunk)) {
+            *m_scale = am;
+            *v_scale = av;
         }
     }
     if (p.finish && threadIdx.x == 0) arrive_and_finish(p.ctrl, gridDim.x, p.hp.beta1, p.hp.beta2);
@@ -397,33 +710,42 @@ __global__ void __launch_bounds__(kThreads) tensors_adamw8_kernel(const __grid_c
 
 // ------------------------------------------------------------- 8-bit values ---
 
+constexpr int kValueThreads = 256;
+
 struct ValueArgs {
     const uint8_t* codes;
     const float* scales;
     float* out;
     int64_t n;
-    int32_t wide;        // codes on 8-byte, out on 16-byte boundaries
+    int32_t wide;        // codes on 4-byte, out on 16-byte boundaries
     float map[256];
 };
 
-__global__ void __launch_bounds__(kThreads) adam8_values_kernel(const __grid_constant__ ValueArgs p) {
+__global__ void __launch_bounds__(kValueThreads) adam8_values_kernel(const __grid_constant__ ValueArgs p) {
     __shared__ float s_map[256];
     s_map[threadIdx.x] = p.map[threadIdx.x];
     griddep_wait();
     griddep_launch_dependents();
     __syncthreads();
-    const int64_t stride = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t nvec = p.wide ? p.n / 8 : 0;
-    for (int64_t i = first; i < nvec; i += stride) {
-        const uint2 c = __ldcs(reinterpret_cast<const uint2*>(p.codes + 8 * i));
-        const float s = __ldg(p.scales + 8 * i / ZS_ADAM8_BLOCK);
-        float x[8];
+    // a warp takes 512 codes: each lane 4, 128 apart, so that its stores are
+    // whole lines
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kValueThreads / 32), warp = ((int64_t)blockIdx.x * kValueThreads + threadIdx.x) / 32;
+    const int64_t whole = p.wide ? p.n / 512 : 0;
+    for (int64_t i = warp; i < whole; i += warps) {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(p.codes + 512 * i) + lane;
+        const float s = __ldg(p.scales + 512 * i / ZS_ADAM8_BLOCK);
+        uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = __fmul_rn(s_map[__byte_perm(j < 4 ? c.x : c.y, 0u, 0x4440u + (j & 3))], s);
-        Mem<8>::store_f(p.out + 8 * i, x);
+        for (int k = 0; k < 4; ++k) c[k] = __ldcs(from + 32 * k);
+        float4* to = reinterpret_cast<float4*>(p.out + 512 * i) + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            __stcs(to + 32 * k, make_float4(__fmul_rn(s_map[c[k] & 0xffu], s), __fmul_rn(s_map[c[k] >> 8 & 0xffu], s),
+                                            __fmul_rn(s_map[c[k] >> 16 & 0xffu], s), __fmul_rn(s_map[c[k] >> 24], s)));
     }
-    for (int64_t i = nvec * 8 + first; i < p.n; i += stride)
+    const int64_t stride = (int64_t)gridDim.x * kValueThreads;
+    for (int64_t i = whole * 512 + (int64_t)blockIdx.x * kValueThreads + threadIdx.x; i < p.n; i += stride)
         p.out[i] = __fmul_rn(s_map[p.codes[i]], __ldg(p.scales + i / ZS_ADAM8_BLOCK));
 }
 
@@ -459,7 +781,7 @@ int32_t check_grads(const zs_tensor* t, int32_t n) {
         if (t[i].n < 0 || t[i].n > (1ll << 40) || !known_type(t[i].grad_type) || t[i].reserved != 0) return ZS_ERR_ARG;
         if (t[i].n > 0 && t[i].grad == nullptr) return ZS_ERR_ARG;
         if (!zs::aligned_to(t[i].grad, t[i].grad_type == ZS_F32 ? 4 : 2)) return ZS_ERR_ALIGN;
-        chunks += (t[i].n + kChunk - 1) / kChunk;
+        chunks += t[i].n / kChunk + 1;
     }
     return chunks < (1ll << 31) ? ZS_OK : ZS_ERR_ARG;
 }
@@ -499,14 +821,14 @@ int common_peel(std::initializer_list<Buffer> bufs) {
 }
 int type_size(int32_t t) { return t == ZS_F32 ? 4 : 2; }
 
-int launch_blocks(const void* kernel, uint32_t chunks) {
-    return zs::persistent_blocks(kernel, kThreads, (int64_t)(chunks > 0 ? chunks : 1) * kThreads);
+int norm_grid(uint32_t chunks) {
+    return zs::persistent_blocks((const void*)tensors_sqnorm_kernel, kNormThreads, (int64_t)(chunks > 0 ? chunks : 1) * kNormThreads);
 }
 
 // The partial sums of one norm call share the scratch buffer: this many each.
 int norm_blocks(uint32_t chunks, int launches_left, int base) {
     const int fit = (kWorkParts - base) / launches_left;
-    const int blocks = launch_blocks((const void*)tensors_sqnorm_kernel, chunks);
+    const int blocks = norm_grid(chunks);
     return blocks < fit ? blocks : fit;
 }
 
@@ -534,7 +856,7 @@ void fill(StepEntry8* e, const zs_tensor& x, const zs_adam& hp) {
 // Launches the tensors of one kind of state, as many at a time as fit; the last
 // launch ends the step if `finish`.
 template <typename Args>
-int32_t launch_steps(void (*kernel)(Args), Args& a, int32_t state, const zs_tensor* t, int32_t n, const zs_adam& hp,
+int32_t launch_steps(void (*kernel)(Args), Args& a, int threads, int per_sm, int smem, int32_t state, const zs_tensor* t, int32_t n, const zs_adam& hp,
                      bool finish, cudaStream_t stream, const char* name) {
     constexpr int G = (int)(sizeof(a.t) / sizeof(a.t[0]));
     int32_t left = 0;
@@ -544,13 +866,13 @@ int32_t launch_steps(void (*kernel)(Args), Args& a, int32_t state, const zs_tens
     for (int32_t i = 0; i < n; ++i) {
         if (t[i].state != state || t[i].n == 0) continue;
         fill(&a.t[a.count], t[i], hp);
-        a.first[a.count + 1] = a.first[a.count] + (uint32_t)((t[i].n + kChunk - 1) / kChunk);
+        a.first[a.count + 1] = a.first[a.count] + (uint32_t)(state == ZS_STATE_U8 ? (t[i].n + kChunk - 1) / kChunk : chunks_of(t[i].n, a.t[a.count].peel));
         ++a.count;
         --left;
         if (a.count < G && left > 0) continue;
         a.finish = finish && left == 0;
-        const int32_t rc = launch_ex(kernel, launch_blocks((const void*)kernel, a.first[a.count]), kThreads, 0, true,
-                                     stream, a, name);
+        const int64_t full = (int64_t)per_sm * zs::device_sm_count(), chunks = a.first[a.count];
+        const int32_t rc = launch_ex(kernel, (int)(chunks < full ? chunks : full), threads, smem, true, stream, a, name);
         if (rc != ZS_OK) return rc;
         a.count = 0;
     }
@@ -583,13 +905,16 @@ ZS_API int32_t zero_tensors_sqnorm_async(const zs_tensor* tensors, int32_t n_ten
         a.first[0] = 0;
         for (a.count = 0; a.count < kNormGroup && i < n_tensors; ++i) {
             const zs_tensor& x = tensors[i];
-            a.t[a.count] = NormEntry{x.grad, x.n, x.grad_type, common_peel({{x.grad, type_size(x.grad_type)}})};
-            a.first[a.count + 1] = a.first[a.count] + (uint32_t)((x.n + kChunk - 1) / kChunk);
+            if (x.n == 0) continue;
+            a.t[a.count] = NormEntry{x.grad, x.n, x.grad_type};
+            const int size = type_size(x.grad_type);
+            const int64_t vectors = (x.n - norm_head(x.grad, size, x.n)) * size / 16;
+            a.first[a.count + 1] = a.first[a.count] + (uint32_t)(vectors > kNormChunk ? (vectors + kNormChunk - 1) / kNormChunk : 1);
             ++a.count;
         }
         a.finish = i == n_tensors;
         const int blocks = norm_blocks(a.first[a.count], launches, a.base);
-        const int32_t lrc = launch_ex(tensors_sqnorm_kernel, blocks, kThreads, 0, true, (cudaStream_t)stream, a,
+        const int32_t lrc = launch_ex(tensors_sqnorm_kernel, blocks, kNormThreads, 0, true, (cudaStream_t)stream, a,
                                       "tensors_sqnorm_kernel");
         if (lrc != ZS_OK) return lrc;
         a.base += blocks;
@@ -610,7 +935,7 @@ ZS_API int32_t zero_tensors_adamw_async(const zs_tensor* tensors, int32_t n_tens
     bool has[2] = {false, false};
     for (int32_t i = 0; i < n_tensors; ++i)
         if (tensors[i].n > 0) has[tensors[i].state] = true;
-    const StepShared shared{*hp, max_norm, sqnorm_dev, ctrl_dev, 0, 0};
+    const StepShared shared{*hp, max_norm, sqnorm_dev, ctrl_dev, 0, 0, 1.0f};
     cudaStream_t st = (cudaStream_t)stream;
     if (has[ZS_STATE_U8]) {
         static_assert(sizeof(StepArgs8) < 64 * 1024, "on the stack");
@@ -618,14 +943,18 @@ ZS_API int32_t zero_tensors_adamw_async(const zs_tensor* tensors, int32_t n_tens
         static_cast<StepShared&>(a) = shared;
         a.maps = host_maps().maps;
         if (!host_maps().ok) return zs::fail_with(ZS_ERR_CUDA, "zero_tensors_adamw_async: code tables");
-        rc = launch_steps(tensors_adamw8_kernel, a, ZS_STATE_U8, tensors, n_tensors, *hp, !has[ZS_STATE_F32], st,
+        constexpr int smem = (int)sizeof(CodeTables);
+        const cudaError_t err =
+            cudaFuncSetAttribute((const void*)tensors_adamw8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (err != cudaSuccess) return zs::cuda_fail(err, "tensors_adamw8_kernel");
+        rc = launch_steps(tensors_adamw8_kernel, a, kThreads8, kBlocks8, smem, ZS_STATE_U8, tensors, n_tensors, *hp, !has[ZS_STATE_F32], st,
                           "tensors_adamw8_kernel");
         if (rc != ZS_OK) return rc;
     }
     if (has[ZS_STATE_F32]) {
         StepArgs32 a;
         static_cast<StepShared&>(a) = shared;
-        return launch_steps(tensors_adamw_kernel, a, ZS_STATE_F32, tensors, n_tensors, *hp, true, st,
+        return launch_steps(tensors_adamw_kernel, a, kThreads32, kBlocks32, 0, ZS_STATE_F32, tensors, n_tensors, *hp, true, st,
                             "tensors_adamw_kernel");
     }
     if (has[ZS_STATE_U8]) return ZS_OK;
@@ -647,11 +976,11 @@ ZS_API int32_t zero_adam8_dequantize(const uint8_t* codes_dev, const float* scal
     a.scales = scales_dev;
     a.out = out_dev;
     a.n = n;
-    a.wide = zs::aligned_to(codes_dev, 8) && zs::aligned_to(out_dev, 16);
+    a.wide = zs::aligned_to(codes_dev, 4) && zs::aligned_to(out_dev, 16);
     const Maps& maps = host_maps().maps;
     std::memcpy(a.map, is_signed ? maps.dec7 : maps.mag8, sizeof(a.map));
-    const int blocks = zs::persistent_blocks((const void*)adam8_values_kernel, kThreads, a.wide ? n / 8 + 1 : n);
-    return launch_ex(adam8_values_kernel, blocks, kThreads, 0, true, (cudaStream_t)stream, a, "adam8_values_kernel");
+    const int blocks = zs::persistent_blocks((const void*)adam8_values_kernel, kValueThreads, a.wide ? n / 16 + 1 : n);
+    return launch_ex(adam8_values_kernel, blocks, kValueThreads, 0, true, (cudaStream_t)stream, a, "adam8_values_kernel");
 }
 
 }  // extern "C"
