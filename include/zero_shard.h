@@ -759,7 +759,7 @@ typedef struct zs_preference {
  *   SQUARED  loss = (h - 1 / (2 beta))^2
  *   totals = sum_pairs w { loss, [reward_chosen > reward_rejected], reward_chosen - reward_rejected }
  *   dlogp = d totals[0] / d logp;   reward = beta s
- *   logp       DEVICE fp32[n_tokens]
+ *   logp       DEVICE fp32[n_tokens], n_tokens <= 2^32
  *   ref_logp   DEVICE fp32[n_tokens], or NULL (0: reference-free)
  *   mask       DEVICE uint8[n_tokens], 0 = the token does not count (its
  *              values, whatever they are, are not used), or NULL (all count)

@@ -35,6 +35,7 @@
 
 #include <cfloat>
 #include <initializer_list>
+
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -452,8 +453,6 @@ __device__ __forceinline__ void zero_range(T* out, int64_t n, int threads) {
 
 // ------------------------------------------------------ copies and clusters ---
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 // Barriers in shared memory that count arrivals and copied bytes.
 __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
@@ -489,18 +488,6 @@ __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t b
                      smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(b)) : "memory");
 }
 
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Writes statistics at the same place of the shared memory of CTA `rank`, and
 // counts their 16 bytes at that CTA's barrier.
 __device__ __forceinline__ void store_to_peer(Stats* at, uint64_t* b, uint32_t rank, const Stats& st) {
@@ -542,7 +529,6 @@ struct RowArgs {
     Work* work;
 };
 
-constexpr int kMaxCluster = 8;
 // Computing threads of a block: kWide, or 128 where a row has few vectors; and
 // the blocks of an SM.  Two blocks of 256 + 64 threads at 96 registers: three of
 // 192 + 64 at 80 took 880 us and two of 384 + 64 at 72 took 732 us where these
@@ -1046,36 +1032,6 @@ int32_t with_type(int32_t type, F go) {
 
 // --------------------------------------------------------------- launch plan ---
 
-// How many clusters of a kernel run at once (cached: it does not change).
-int active_clusters(const void* kernel, int threads, int ctas, int smem) {
-    static std::mutex mu;
-    static std::map<std::tuple<const void*, int, int>, int> known;
-    const auto key = std::make_tuple(kernel, ctas, smem);
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        auto it = known.find(key);
-        if (it != known.end()) return it->second;
-    }
-    int n = 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ctas * zs::device_sm_count()));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        n = 1;
-    }
-    std::lock_guard<std::mutex> lock(mu);
-    known[key] = n;
-    return n;
-}
-
 struct Plan {
     int ctas, piece, buffers;  // CTAs of a cluster; vectors of a buffer; buffers
 };
@@ -1132,22 +1088,7 @@ int32_t launch_rows(RowArgs& a, cudaStream_t stream) {
     a.piece = pl.piece;
     a.buffers = pl.buffers;
     a.group = group;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * pl.ctas));
-    cfg.blockDim = dim3((unsigned)(NT + 64));
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)pl.ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, (const RowArgs)a);
-    if (err != cudaSuccess) return zs::cuda_fail(err, "rows_kernel");
-    return zs::check_launch("rows_kernel");
+    return launch_clusters(kernel, (int)clusters, pl.ctas, NT + 64, smem, stream, a, "rows_kernel");
 }
 
 // Blocks of 128 threads where a row has fewer vectors than 1024.

@@ -43,9 +43,90 @@ __device__ __forceinline__ double warp_sum(double x) {
     return x;
 }
 
+// A sum in two fp32 parts, hi + lo: what hi's rounding drops goes to lo exactly
+// (the TwoSum of Knuth).  GB300's fp64 rate is a small part of its fp32 rate.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float p) {
+        const float s = __fadd_rn(hi, p), bp = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bp)), __fsub_rn(p, bp)));
+        hi = s;
+    }
+};
+
 // The loss scale of a control block (1 without one).
 __device__ __forceinline__ float loss_scale_of(const zs_ctrl* c) {
     return c == nullptr ? 1.0f : __double2float_rn(*(const volatile double*)&c->loss_scale);
 }
 
 inline bool finite_double(double x) { return x == x && x <= 1e300 && x >= -1e300; }
+
+// --------------------------------------------------------------- clusters ---
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+constexpr int kMaxCluster = 8;
+
+// How many clusters of a kernel run at once (cached: it does not change).
+int active_clusters(const void* kernel, int threads, int ctas, int smem) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int>, int> known;
+    const auto key = std::make_tuple(kernel, ctas, smem);
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        auto it = known.find(key);
+        if (it != known.end()) return it->second;
+    }
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas * zs::device_sm_count()));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = 1;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    known[key] = n;
+    return n;
+}
+
+// Enqueues `clusters` clusters of `ctas` blocks with programmatic serialization.
+template <typename Args>
+int32_t launch_clusters(void (*kernel)(Args), int clusters, int ctas, int threads, int smem, cudaStream_t stream,
+                        const Args& args, const char* name) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * ctas));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args);
+    if (err != cudaSuccess) return zs::cuda_fail(err, name);
+    return zs::check_launch(name);
+}

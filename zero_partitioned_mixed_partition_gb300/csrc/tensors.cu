@@ -13,6 +13,10 @@
 #include <cmath>
 #include <cstring>
 
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "zs_internal.h"
 
 namespace {
@@ -155,17 +159,6 @@ __device__ __forceinline__ int tensor_of(const uint32_t* first, int count, uint3
     }
     return lo;
 }
-
-// A sum in two fp32 parts, hi + lo: what hi's rounding drops goes to lo exactly
-// (the TwoSum of Knuth).  GB300's fp64 rate is a small part of its fp32 rate.
-struct Sum2 {
-    float hi, lo;
-    __device__ __forceinline__ void add(float p) {
-        const float s = __fadd_rn(hi, p), bp = __fsub_rn(s, hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bp)), __fsub_rn(p, bp)));
-        hi = s;
-    }
-};
 
 // 2 or 4 bytes read for an element and some 4 instructions.  A chunk is 2048
 // vectors of one gradient, each thread's eight under way together; elements
