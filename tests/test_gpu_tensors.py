@@ -320,6 +320,29 @@ def test_eight_bit_extreme_scales(zs, cuda_device):
         _check_step(case, before, 1, 1.0, 1.0)
 
 
+@pytest.mark.parametrize("state", [32, 8])
+def test_weights_without_gradients_and_states(zs, cuda_device, state):
+    """Rows of zeros (m = v = g = 0) next to others: u = 0 there, and the weights
+    only decay."""
+    n = 20_000
+    case = _Case(zs, [n], state, torch.bfloat16, torch.bfloat16, 12)
+    zero = torch.arange(n, device="cuda") % 1000 < 700
+    zero[5000:5003] = True
+    for x in (case.grad, case.m, case.v):
+        x[:n][zero] = 0
+    before = [case.host(0)]
+    zs.zero_tensors_adamw_async(case.list, zs.adam(LR, BETA1, BETA2, EPS, WD), _ctrl(zs, 1.0))
+    _check_step(case, before, 1, 1.0, 1.0)
+    # v' of 0 with an m' that is not
+    case = _Case(zs, [n], state, torch.float32, None, 13)
+    case.grad[:n] = 1e-30
+    case.v[:n] = 0
+    before = [case.host(0)]
+    with np.errstate(all="ignore"):
+        zs.zero_tensors_adamw_async(case.list, zs.adam(LR, BETA1, BETA2, EPS, WD), _ctrl(zs, 1.0))
+        _check_step(case, before, 1, 1.0, 1.0)
+
+
 @pytest.mark.parametrize("n,shift", [(1, 0), (7, 0), (2048, 0), (5001, 0), (5001, 1), (1_000_003, 0)])
 @pytest.mark.parametrize("signed", [True, False])
 def test_values_of_8_bit_states(zs, cuda_device, n, shift, signed):

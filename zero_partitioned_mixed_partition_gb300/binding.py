@@ -672,6 +672,14 @@ def zero_qwz_dequantize(codes: torch.Tensor, scales: torch.Tensor, n: int, param
 _TYPES = {torch.float32: ZS_F32, torch.float16: ZS_F16, torch.bfloat16: ZS_BF16}
 
 
+def _stream_of(stream, t: torch.Tensor) -> Optional[int]:
+    """As _stream; None: the current stream of the tensor's device (read without
+    making a Stream object, which costs a small call a third of its time)."""
+    if stream is None and t.is_cuda:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return _stream(stream)
+
+
 def new_work(device="cuda") -> torch.Tensor:
     """Scratch of the calls that add up over a batch (cleared; one per stream)."""
     return torch.zeros(ZS_WORK_BYTES // 8, dtype=torch.int64, device=device)
@@ -730,7 +738,7 @@ def zero_token_logp_async(logits: torch.Tensor, labels: torch.Tensor, logp: torc
     rc = lib().zero_token_logp_async(ctypes.byref(x), _vector(labels, torch.int64, n, "labels"),
                                      _vector(logp, torch.float32, n, "logp"),
                                      _vector(entropy, torch.float32, n, "entropy"),
-                                     _vector(saved, torch.float32, 2 * n, "saved"), _stream(stream))
+                                     _vector(saved, torch.float32, 2 * n, "saved"), _stream_of(stream, logits))
     _check(rc, "zero_token_logp_async")
 
 
@@ -748,7 +756,7 @@ def zero_token_logp_grad_async(logits: torch.Tensor, labels: torch.Tensor, saved
                                           _vector(entropy, torch.float32, n, "entropy"),
                                           _vector(dentropy, torch.float32, n, "dentropy"),
                                           _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"), out, out_stride,
-                                          _stream(stream))
+                                          _stream_of(stream, logits))
     _check(rc, "zero_token_logp_grad_async")
 
 
@@ -781,7 +789,7 @@ def zero_policy_loss_async(logits: torch.Tensor, labels: torch.Tensor, old_logp:
                                       _vector(logp, f32, n, "logp"), _vector(entropy, f32, n, "entropy"),
                                       _vector(token_loss, f32, n, "token_loss"), out, out_stride,
                                       _vector(totals, f32, ZS_POLICY_TOTALS, "totals"), _work_ptr(work),
-                                      _stream(stream))
+                                      _stream_of(stream, logits))
     _check(rc, "zero_policy_loss_async")
 
 
@@ -817,7 +825,7 @@ def zero_preference_loss_async(logp: torch.Tensor, cu_seqlens: torch.Tensor, hp:
                                           _vector(reward, f32, 2 * pairs, "reward"),
                                           _vector(dlogp, f32, n, "dlogp"),
                                           _vector(totals, f32, ZS_PREFERENCE_TOTALS, "totals"), _work_ptr(work),
-                                          _stream(stream))
+                                          _stream_of(stream, logp))
     _check(rc, "zero_preference_loss_async")
 
 
@@ -878,7 +886,7 @@ def zero_tensors_sqnorm_async(tensors: TensorList, sqnorm_dev: torch.Tensor, wor
     non-finite test into the control block."""
     rc = lib().zero_tensors_sqnorm_async(tensors.array, len(tensors), _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"),
                                          _dev_ptr(sqnorm_dev, torch.float64, "sqnorm_dev"), _work_ptr(work),
-                                         _stream(stream))
+                                         _stream_of(stream, ctrl_dev))
     _check(rc, "zero_tensors_sqnorm_async")
 
 
@@ -888,7 +896,7 @@ def zero_tensors_adamw_async(tensors: TensorList, hp: Adam, ctrl_dev: torch.Tens
     sqnorm_dev; skipped on the device if the norm pass met a non-finite value."""
     rc = lib().zero_tensors_adamw_async(tensors.array, len(tensors), ctypes.byref(hp), float(max_norm),
                                         _dev_ptr(sqnorm_dev, torch.float64, "sqnorm_dev"),
-                                        _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"), _stream(stream))
+                                        _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"), _stream_of(stream, ctrl_dev))
     _check(rc, "zero_tensors_adamw_async")
 
 
@@ -898,7 +906,7 @@ def zero_adam8_dequantize(codes: torch.Tensor, scales: torch.Tensor, n: int, sig
     n = int(n)
     rc = lib().zero_adam8_dequantize(_vector(codes, torch.uint8, n, "codes"),
                                      _vector(scales, torch.float32, (n + ZS_ADAM8_BLOCK - 1) // ZS_ADAM8_BLOCK, "scales"),
-                                     n, 1 if signed else 0, _vector(out, torch.float32, n, "out"), _stream(stream))
+                                     n, 1 if signed else 0, _vector(out, torch.float32, n, "out"), _stream_of(stream, codes))
     _check(rc, "zero_adam8_dequantize")
 
 

@@ -326,8 +326,9 @@ __device__ __forceinline__ uint64_t add2_apart(uint64_t a, uint64_t b, uint64_t 
 // The Adam / AdamW update of eight coordinates from their gradients (raw, as
 // pairs): the operations of adam_apply, two coordinates at a time.  Divisions and
 // square roots are the correctly rounded ones above where all of a warp's values
-// lie in [2^-80, 2^40], with any bias correction in their ranges, and else the
-// scalar ones.  m, v: in and out, as pairs.
+// lie in [2^-80, 2^40], with any bias correction in their ranges, or all eight of
+// a thread's are 0 (weights that no gradient has reached), and else the scalar
+// ones.  m, v: in and out, as pairs.
 __device__ __forceinline__ void adam_eight(const Coef2& c, float lr, float wd, const uint64_t* g, float* th, uint64_t* m,
                                            uint64_t* v) {
     float low = 1.0f, high = 0.0f;  // the smallest and largest |m'|, v'
@@ -342,7 +343,7 @@ __device__ __forceinline__ void adam_eight(const Coef2& c, float lr, float wd, c
         low = fminf(fminf(low, fminf(fabsf(a), fabsf(b))), fminf(p, q));
         high = fmaxf(fmaxf(high, fmaxf(fabsf(a), fabsf(b))), fmaxf(p, q));
     }
-    if (__any_sync(0xffffffffu, !(low >= 0x1p-80f && high <= 0x1p40f))) {
+    if (__any_sync(0xffffffffu, !(low >= 0x1p-80f && high <= 0x1p40f) && high != 0.0f)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float a[2], p[2];
@@ -357,8 +358,9 @@ __device__ __forceinline__ void adam_eight(const Coef2& c, float lr, float wd, c
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint64_t mh = div2_by_constant(m[j], c.bc1, c.rcp_bc1), vh = div2_by_constant(v[j], c.bc2, c.rcp_bc2);
-        float u0, u1;
-        split(div2(mh, add2(sqrt2(vh), eps)), u0, u1);
+        float u0, u1, p, q;
+        split(vh, p, q);  // (a v' of 0 belongs to an m' of 0: any root will do)
+        split(div2(mh, add2(sqrt2(pair(fmaxf(p, 0x1p-80f), fmaxf(q, 0x1p-80f))), eps)), u0, u1);
         th[2 * j] = __fsub_rn(th[2 * j], __fmul_rn(lr, __fadd_rn(u0, __fmul_rn(wd, th[2 * j]))));
         th[2 * j + 1] = __fsub_rn(th[2 * j + 1], __fmul_rn(lr, __fadd_rn(u1, __fmul_rn(wd, th[2 * j + 1]))));
     }
@@ -494,7 +496,7 @@ template <int OCTAVES>
 __device__ __forceinline__ uint32_t lut_code(float a, const uint2* lut) {
     constexpr uint32_t lowest = (uint32_t)(127 - OCTAVES) << 23;
     a = fmaxf(a, __uint_as_float(lowest));  // (a NaN becomes the lowest: code 0)
-    const uint2 e = lut[(__float_as_uint(a) - lowest) >> kBucketShift];
+    const uint2 e = lut[(int)(__float_as_uint(a) >> kBucketShift) - (int)(lowest >> kBucketShift)];
     return e.y + (a > __uint_as_float(e.x) ? 1u : 0u);
 }
 // From the thresholds: thr[k] lies in bucket b_k, and the buckets above b_(k-1)
