@@ -536,15 +536,17 @@ struct RowArgs {
 // the registers more than the warps.
 constexpr int kWide = 256;
 constexpr int per_sm_of(int threads) { return threads == 128 ? 4 : 2; }
-constexpr int kList = 256;  // live rows that a cluster takes at a time
+constexpr int kList = 256;     // live rows that a cluster takes at a time
+constexpr int kMaxGroup = 48;  // clusters of a group
 
+// (All loads at once: none waits for another's test.)
 template <int MODE>
 __device__ __forceinline__ bool row_is_live(const RowArgs& p, int64_t r) {
     const int64_t y = p.labels[r];
-    bool live = y >= 0 && y < p.vocab;
-    if (MODE == kLogpGrad) live = live && p.saved[2 * r + 1] != -INFINITY;
-    if (MODE >= kPolicyLoss && p.weights != nullptr) live = live && p.weights[r] != 0.0f;
-    return live;
+    float w = 1.0f, lns = 0.0f;
+    if (MODE == kLogpGrad) lns = p.saved[2 * r + 1];
+    if (MODE >= kPolicyLoss && p.weights != nullptr) w = p.weights[r];
+    return (y >= 0) & (y < p.vocab) & (w != 0.0f) & (lns != -INFINITY);
 }
 
 // What the computing warps need of a row, per buffer.
@@ -579,9 +581,12 @@ __device__ __forceinline__ void deal_rows(const RowArgs& p, int64_t j0, int32_t 
     __shared__ int32_t s_scan[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t run = (batch + NT - 1) / NT, first = min(tid * run, batch), last = min(first + run, batch);
-    int32_t count = 0;
+    static_assert(kList * kMaxGroup <= 64 * NT, "a thread's rows have a bit each");
+    uint64_t alive = 0;
 #pragma unroll 4
-    for (int32_t j = first; j < last; ++j) count += row_is_live<MODE>(p, (j0 + j) * groups + group_first) ? 1 : 0;
+    for (int32_t j = first; j < last; ++j)
+        alive |= (uint64_t)(row_is_live<MODE>(p, (j0 + j) * groups + group_first) ? 1 : 0) << (j - first);
+    const int32_t count = __popcll(alive);
     int32_t upto = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -602,7 +607,7 @@ __device__ __forceinline__ void deal_rows(const RowArgs& p, int64_t j0, int32_t 
     const int32_t live_skip = (int32_t)((mine - live_before % p.group + p.group) % p.group);
     const int32_t dead_skip = (int32_t)((mine - dead_before % p.group + p.group) % p.group);
     for (int32_t j = first; j < last; ++j) {
-        const bool live = row_is_live<MODE>(p, (j0 + j) * groups + group_first);
+        const bool live = alive >> (j - first) & 1;
         const int32_t off = live ? before - live_skip : j - before - dead_skip;
         if (off >= 0 && off % p.group == 0) (live ? lists.live : lists.dead)[off / p.group] = j;
         before += live ? 1 : 0;
@@ -696,6 +701,13 @@ __global__ void __launch_bounds__(NT + 64, per_sm_of(NT)) rows_kernel(const __gr
                 int32_t first = 0;
                 do {
                     mbar_wait<true>(&s_empty[buf], phase ^ 1u);
+                    const int32_t count = min(p.piece, n - first);
+                    const bool ok = count > 0 && ZS_RANGE_OK(kSiteLogits, head + (int64_t)(v0 + first) * N, (int64_t)count * N, p.vocab);
+                    // the copy first: the row's label and edges may still be on
+                    // their way (the barrier's phase ends with the arrival below)
+                    if (lane == 0 && ok)
+                        copy_bulk(s_buffers + (int64_t)buf * p.piece, row + head + (int64_t)(v0 + first) * N,
+                                  (uint32_t)count * 16u, &s_full[buf]);
                     RowInfo& to = s_info[buf];
                     if (lane == 0) {
                         to.row = r;
@@ -711,14 +723,7 @@ __global__ void __launch_bounds__(NT + 64, per_sm_of(NT)) rows_kernel(const __gr
                         to.edge[lane] = edge;
                     }
                     __syncwarp();
-                    if (lane == 0) {
-                        const int32_t count = min(p.piece, n - first);
-                        const bool ok = ZS_RANGE_OK(kSiteLogits, head + (int64_t)(v0 + first) * N, (int64_t)count * N, p.vocab);
-                        mbar_expect(&s_full[buf], ok ? (uint32_t)count * 16u : 0u);
-                        if (ok && count > 0)
-                            copy_bulk(s_buffers + (int64_t)buf * p.piece, row + head + (int64_t)(v0 + first) * N,
-                                      (uint32_t)count * 16u, &s_full[buf]);
-                    }
+                    if (lane == 0) mbar_expect(&s_full[buf], ok ? (uint32_t)count * 16u : 0u);
                     advance();
                     first += p.piece;
                 } while (first < n);
@@ -1077,9 +1082,9 @@ int32_t launch_rows(RowArgs& a, cudaStream_t stream) {
     int group = 1;
     if (a.rows <= clusters) {
         clusters = a.rows > 0 ? a.rows : 1;
-    } else if (clusters >= 48) {
+    } else if (clusters >= kMaxGroup) {
         group = 32;
-        for (int g = 24; g <= 48; ++g)
+        for (int g = 24; g <= kMaxGroup; ++g)
             if (clusters % g < clusters % group) group = g;
         clusters -= clusters % group;
     } else {

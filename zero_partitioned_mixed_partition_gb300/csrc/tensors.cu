@@ -500,15 +500,16 @@ __device__ __forceinline__ uint32_t lut_code(float a, const uint2* lut) {
     return e.y + (a > __uint_as_float(e.x) ? 1u : 0u);
 }
 // From the thresholds: thr[k] lies in bucket b_k, and the buckets above b_(k-1)
-// up to b_k have k thresholds below them.  One k to a thread; the buckets below
-// the lowest threshold and above the highest are the first's and the last's.
+// up to b_k have k thresholds below them.  A warp fills one k's at a time (some
+// have hundreds; one to a thread took 25 us); the buckets below the lowest
+// threshold and above the highest are the first's and the last's.
 template <int OCTAVES, int COUNT, int SIZE>
 __device__ __forceinline__ void build_lut(const float (&thr)[COUNT], uint2 (&lut)[SIZE]) {
     constexpr uint32_t lowest = (uint32_t)(127 - OCTAVES) << 23;
     auto bucket = [&](int k) { return (int)((__float_as_uint(thr[k]) - lowest) >> kBucketShift); };
-    for (int k = threadIdx.x; k < COUNT; k += blockDim.x) {
+    for (int k = threadIdx.x / 32; k < COUNT; k += blockDim.x / 32) {
         const int from = k == 0 ? 0 : bucket(k - 1) + 1, to = k == COUNT - 1 ? SIZE - 1 : bucket(k);
-        for (int b = from; b <= to; ++b) lut[b] = make_uint2(__float_as_uint(thr[k]), (uint32_t)k);
+        for (int b = from + (int)(threadIdx.x & 31); b <= to; b += 32) lut[b] = make_uint2(__float_as_uint(thr[k]), (uint32_t)k);
     }
 }
 
