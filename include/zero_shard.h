@@ -53,7 +53,7 @@ extern "C" {
 #define ZS_ERR_ARG (-1)     /* invalid argument; nothing was enqueued */
 #define ZS_ERR_ALIGN (-2)   /* a pointer is not aligned to its element type */
 #define ZS_ERR_CUDA (-3)    /* a CUDA call failed; see zero_last_error() */
-#define ZS_ERR_TIMEOUT (-4) /* reserved: no kernel of this library polls a flag */
+#define ZS_ERR_TIMEOUT (-4) /* reserved: returned by no call */
 
 /* Largest data-parallel degree (number of gradient contributions). */
 #define ZS_MAX_ND 1024
@@ -664,7 +664,9 @@ typedef struct zs_logits {
  *            saved may be NULL.
  * A logit of -inf has probability 0.  A row of nothing but -inf has no
  * distribution: logp = -inf, entropy = 0.  A NaN or +inf in a row gives NaN.
- * One pass over the logits, stream-ordered, one launch.
+ * One pass over the logits, stream-ordered, one launch.  (The waits of the logits
+ * kernels for their own copies are bounded; one that ran out, after a second or
+ * so, would show as NaN in the outputs.)
  * Source: the softmax cross-entropy of a language model; no counterpart in the pages. */
 ZS_API int32_t zero_token_logp_async(const zs_logits* x, const int64_t* labels, float* logp, float* entropy,
                                      float* saved, void* stream);

@@ -505,3 +505,63 @@ def test_preference_without_pairs_and_offsets_outside(zs, cuda_device):
     zs.zero_preference_loss_async(x, cu, zs.preference(0.5), loss, reward, totals, work, dlogp=d)
     assert reward.tolist() == [-2.0, -2.0] and abs(loss.item() - math.log(2)) <= 4 * U
     assert d[:4].eq(d[0]).all() and d[4:].eq(-d[0]).all()
+
+
+# ----------------------------------------------------- together with a step ---
+
+def test_losses_and_step_in_a_graph(zs, cuda_device):
+    """Scoring, both losses, their gradients, the norm and the step replayed from
+    a CUDA graph give what the calls give."""
+    rows, vocab = 48, 3001
+    x, y, old, ref, adv, _ = _policy_inputs(rows, vocab, torch.bfloat16, 21)
+    f = lambda *n: torch.zeros(*n, device="cuda")
+    logp, saved, totals, pair, reward, pref, dlogp = f(rows), f(rows, 2), f(5), f(2), f(4), f(3), f(rows)
+    d1, d2 = torch.empty_like(x), torch.empty_like(x)
+    cu = torch.tensor([0, 10, 25, 40, rows], device="cuda")
+    work, ctrl, sq = zs.new_work(), zs.new_ctrl(), zs.new_sqnorm()
+    zs.zero_ctrl_init(ctrl, 4.0)
+    master, m, v = f(rows, vocab), f(rows, vocab), f(rows, vocab)
+    lst = zs.TensorList([zs.TensorView(d1, master, m, v)])
+
+    def calls():
+        zs.zero_token_logp_async(x, y, logp, saved=saved)
+        zs.zero_preference_loss_async(logp, cu, zs.preference(0.1), pair, reward, pref, work, ref_logp=ref, dlogp=dlogp)
+        zs.zero_token_logp_grad_async(x, y, saved, dlogp, d2, ctrl_dev=ctrl)
+        zs.zero_policy_loss_async(x, y, old, adv, None, zs.policy(), totals, work, ref_logp=ref, logp=logp, dlogits=d1,
+                                  ctrl_dev=ctrl)
+        zs.zero_tensors_sqnorm_async(lst, sq, work, ctrl)
+        zs.zero_tensors_adamw_async(lst, zs.adam(1e-3), ctrl, max_norm=1.0, sqnorm_dev=sq)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        calls()
+    s.synchronize()
+    want = [t.clone() for t in (logp, pref, dlogp, d1, d2, totals, sq, master, m, v)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for t in (master, m, v, d1, d2, logp, dlogp):
+        t.zero_()
+    zs.zero_ctrl_init(ctrl, 4.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, (logp, pref, dlogp, d1, d2, totals, sq, master, m, v)):
+        assert torch.equal(a, b)
+    assert zs.read_ctrl(ctrl)["step"] == 1
+
+
+def test_gradient_that_overflows_its_type_skips_the_step(zs, cuda_device):
+    rows, vocab = 8, 500
+    x, y, old, ref, adv, _ = _policy_inputs(rows, vocab, torch.float16, 22)
+    out, logp, totals, work = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(5, device="cuda"), zs.new_work()
+    ctrl, sq = zs.new_ctrl(), zs.new_sqnorm()
+    zs.zero_ctrl_init(ctrl, 2.0 ** 24)
+    zs.zero_policy_loss_async(x, y, old, adv, None, zs.policy(), totals, work, logp=logp, dlogits=out, ctrl_dev=ctrl)
+    assert torch.isinf(out).any() and totals.isfinite().all()
+    f = lambda: torch.zeros(rows, vocab, device="cuda")
+    master, m, v = f(), f(), f()
+    lst = zs.TensorList([zs.TensorView(out, master, m, v)])
+    zs.zero_tensors_sqnorm_async(lst, sq, work, ctrl)
+    zs.zero_tensors_adamw_async(lst, zs.adam(1e-3), ctrl, max_norm=1.0, sqnorm_dev=sq)
+    c = zs.read_ctrl(ctrl)
+    assert (c["skipped"], c["step"], c["loss_scale"]) == (1, 0, 2.0 ** 23) and (master == 0).all() and (m == 0).all()

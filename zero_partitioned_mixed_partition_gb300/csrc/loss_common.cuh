@@ -104,8 +104,11 @@ int active_clusters(const void* kernel, int threads, int ctas, int smem) {
         cudaGetLastError();
         n = 1;
     }
-    std::lock_guard<std::mutex> lock(mu);
-    known[key] = n;
+    try {
+        std::lock_guard<std::mutex> lock(mu);
+        known[key] = n;
+    } catch (...) {  // no memory to remember it: found again at the next call
+    }
     return n;
 }
 
