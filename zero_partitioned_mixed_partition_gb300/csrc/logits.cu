@@ -18,17 +18,20 @@
 // distributed shared memory and turns them into the row's outputs and gradient
 // coefficients; no barrier of the block is on the way.  The second pass finds the
 // row in L2: so few rows are under way at once that they fit there (plan_rows).
-// Keeping the slices in shared memory between the passes was built first and
-// was slower: it took clusters of six CTAs where this takes two, so that most
-// of a row's time went into its fixed costs.
+// Forms that kept the slices in shared memory between the passes were built
+// first; the best of them took 910 us in the first case below, with clusters of
+// six CTAs.
 //
 // Measured on one GB300 (6787 GB/s copied): policy loss and gradient, 8192 x
 // 131072 bf16, a tenth of the rows left out, with entropy: 685 us, 5.95 TB/s of
 // the bytes that have to move; 4096 x 32000 bf16, 30 % left out, no entropy:
 // 87 us, 5.1 TB/s; log-probabilities, 8192 x 50257 bf16, a quarter left out:
-// 98 us, 6.3 TB/s.  What bounds the first: instruction issue in the two passes
-// (about 90 instructions for 8 logits) next to the copies; the second: a row's
-// turn from statistics to gradient, some 1.5 us in 8.
+// 98 us, 6.3 TB/s.  Nothing is full in the first: 87 % of the copy rate, and 2.2 of 4
+// issue slots a cycle (on 1024 rows; 134 instructions for 8 logits, 87 of them in
+// the two passes' loops).  In the second a CTA takes its rows one at a time, so the
+// turn from statistics to gradient stands open in each (an estimated 1.5 us of
+// 8), and its 2867 live rows are 9.4 rounds of 304; letting the next row's first
+// pass go in between was tried: 94 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -1048,8 +1051,8 @@ constexpr int buffer_bytes(int per_sm) { return 228 * 1024 / per_sm - 1024 - 5 *
 // 725 us for the case above.)
 constexpr int kPiece = 1440;
 // Bytes of rows that may be under way at once where they are read twice.  (For
-// the case above: clusters of two and 40 MB of rows 685 us, of one and 80 MB
-// 887 us, of four and 20 MB 784 us.)
+// the case above: clusters of two and 40 MB of rows 685 to 689 us, of one and
+// 80 MB 887 us, of four and 20 MB 784 us.)
 constexpr int64_t kRowsInL2 = 45ll << 20;
 
 // The second pass should find its row in L2 (129 MB, which the gradient passes
