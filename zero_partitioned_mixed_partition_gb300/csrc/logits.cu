@@ -170,15 +170,18 @@ __device__ __forceinline__ uint4 at_least(const uint4& r, uint32_t t) {
 // Statistics of a part of a row, in units of log2: s = sum 2^a, u = sum 2^a a
 // with a = x k - c, k = it log2 e, and c = top k rounded once, the same c for
 // the whole part; so a is rounded once from its exact value (one fused
-// multiply-add) and c's own rounding cancels.  top is not the largest logit but
-// one that the largest exceeds by at most kSlack in those units: a sum is
-// scaled to a new top only where a vector exceeds that, which after the first
-// vectors hardly happens, and 2^kSlack times any vocabulary is far from fp32's
-// range.  Where c would be 2^100 or more, a is (x - top) k instead.  top starts
-// at the lowest finite float, so that a row of nothing but -inf keeps s = 0 and
-// no difference of infinities is formed.
+// multiply-add) and c's own rounding is the same factor in every term.  top is
+// not the largest logit but one that the largest exceeds by at most kSlack in
+// those units: a sum is scaled to a new top only where a vector exceeds that,
+// which after the first vectors hardly happens.  c's rounding moves a by up to
+// half a unit of its last place, so this form serves where |c| < 2^24 (half a
+// unit is 1/2 there, and an a of kSlack + 1/2 times any vocabulary is far from
+// fp32's range); it would leave the range from 2^31 on.  For larger c, a vocabulary
+// masked with -1e9 or below, a is (x - top) k instead.  top starts at the lowest
+// finite float, so that a row of nothing but -inf keeps s = 0 and no difference of
+// infinities is formed.
 constexpr float kSlack = 20.0f;
-constexpr float kLargeC = 0x1p100f;
+constexpr float kLargeC = 0x1p24f;
 // A logit this far below top, in the same units, has 2^a = 0 (ex2 flushes to 0
 // below -126).  Where 2^a a is summed, such logits are raised to it (16-bit
 // types, two by one instruction), or a to kLowest: 0 times -inf would be NaN.
@@ -190,10 +193,18 @@ struct __align__(16) Stats {
     float x_label;  // the row's label's logit, carried along
 };
 
-// (a - b) k for two tops, as the difference of their c.
+// What is left of c's rounding: c - top k, exactly (0 in the slow form).
+__device__ __forceinline__ float c_residue(float top, float k) {
+    const float c = __fmul_rn(top, k);
+    return fabsf(c) < kLargeC ? -fmaf(top, k, -c) : 0.0f;
+}
+
+// How far the sums at top a lie above those at top b: the difference of their c,
+// where a slow one counts as top k.
 __device__ __forceinline__ float top_gap(float a, float b, float k) {
     const float ca = __fmul_rn(a, k), cb = __fmul_rn(b, k);
-    return fmaxf(fabsf(ca) < kLargeC && fabsf(cb) < kLargeC ? ca - cb : (a - b) * k, kLowest);
+    if (fabsf(ca) < kLargeC && fabsf(cb) < kLargeC) return fmaxf(ca - cb, kLowest);
+    return fmaxf((a - b) * k + (c_residue(a, k) - c_residue(b, k)), kLowest);
 }
 
 // How a vector's exponentials are formed, by the row's top: kSlow where c
@@ -332,12 +343,6 @@ __device__ __forceinline__ Stats join_warp(Stats st, float k) {
         if (ENT) st.u += __shfl_xor_sync(0xffffffffu, st.u, o);
     }
     return st;
-}
-
-// What is left of c's rounding: c - top k, exactly (0 in the slow form).
-__device__ __forceinline__ float c_residue(float top, float k) {
-    const float c = __fmul_rn(top, k);
-    return fabsf(c) < kLargeC ? -fmaf(top, k, -c) : 0.0f;
 }
 
 // ---------------------------------------------------------------- gradient ---
