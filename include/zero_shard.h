@@ -759,6 +759,10 @@ typedef struct zs_preference {
  *   SIGMOID  loss = -(1 - ls) ln sigma(z) - ls ln sigma(-z)
  *   HINGE    loss = max(0, 1 - z)
  *   SQUARED  loss = (h - 1 / (2 beta))^2
+ * An unmasked token of -inf (a label that zero_token_logp_async found impossible)
+ * gives an infinite score, and the loss and gradient are the formulas' there: with
+ * it in the rejected answer SIGMOID without smoothing and HINGE are 0.  Infinities
+ * of both signs in a sequence, or the same one in both of a pair, give NaN.
  *   totals = sum_pairs w { loss, [reward_chosen > reward_rejected], reward_chosen - reward_rejected }
  *   dlogp = d totals[0] / d logp;   reward = beta s
  *   logp       DEVICE fp32[n_tokens], n_tokens <= 2^32

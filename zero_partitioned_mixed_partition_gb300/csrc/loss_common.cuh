@@ -45,8 +45,13 @@ __device__ __forceinline__ double warp_sum(double x) {
 
 // A sum in two fp32 parts, hi + lo: what hi's rounding drops goes to lo exactly
 // (the TwoSum of Knuth).  GB300's fp64 rate is a small part of its fp32 rate.
+// Once hi is infinite or NaN it is the sum, and lo, a difference of infinities,
+// is not read.
 struct Sum2 {
     float hi, lo;
+    __device__ __forceinline__ double value() const {
+        return fabsf(hi) <= 3.402823466e38f ? (double)hi + (double)lo : (double)hi;
+    }
     __device__ __forceinline__ void add(float p) {
         const float s = __fadd_rn(hi, p), bp = __fsub_rn(s, hi);
         lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, bp)), __fsub_rn(p, bp)));

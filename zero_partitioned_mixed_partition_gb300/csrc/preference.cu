@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kPairThreads, kPairBlocks) preference_loss_ker
                 keep.add(hi);
                 keep.lo = __fadd_rn(keep.lo, lo);
             }
-            if ((lane & 15) == 0) s_sum[warp][lane >> 4] = (double)keep.hi + (double)keep.lo;
+            if ((lane & 15) == 0) s_sum[warp][lane >> 4] = keep.value();
             if (p.average) {
                 const int32_t k0 = __reduce_add_sync(0xffffffffu, count0), k1 = __reduce_add_sync(0xffffffffu, count1);
                 if (lane == 0) {
@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kPairThreads, kPairBlocks) preference_loss_ker
             if (w != 0.0f) {
                 const float h = score[0] - score[1], z = p.beta * h - p.margin;
                 if (p.kind == ZS_PREFERENCE_SIGMOID) {
-                    loss = (1.0f - p.smooth) * softplus(-z) + p.smooth * softplus(z);
+                    loss = (1.0f - p.smooth) * softplus(-z);
+                    if (p.smooth != 0.0f) loss += p.smooth * softplus(z);  // (0 times an infinite one has no value)
                     dh = p.beta * (p.smooth / (1.0f + expf(-z)) - (1.0f - p.smooth) / (1.0f + expf(z)));
                 } else if (p.kind == ZS_PREFERENCE_HINGE) {
                     loss = z < 1.0f ? 1.0f - z : (z != z ? z : 0.0f);
