@@ -1,0 +1,95 @@
+"""The AdamW step over a list of tensors where its states are NaN or infinite.
+The definition in fp32, one rounding per operation (numpy), gives what must come
+out; a NaN may carry any bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_tensors as base
+from test_gpu_tensors import BETA1, BETA2, BLOCK, EPS, F, LR, WD, _Case, _ctrl, _decode
+
+pytestmark = pytest.mark.gpu
+
+N = 6 * BLOCK + 77
+
+
+def _definition(b, state, inv, eps=EPS, beta2=BETA2):
+    """m', v' and the weights after the first step, in fp32."""
+    c = lambda x: F(x)
+    with np.errstate(all="ignore"):
+        m = _decode(b["m"], b["ms"], True) if state == 8 else b["m"]
+        v = _decode(b["v"], b["vs"], False) if state == 8 else b["v"]
+        g = b["g"] * c(inv)
+        m = c(BETA1) * m + c(1.0 - BETA1) * g
+        v = c(beta2) * v + c(1.0 - beta2) * (g * g)
+        u = (m / c(1.0 - BETA1)) / (np.sqrt(v / c(1.0 - beta2)) + c(eps))
+        return b["th"] - c(LR) * (u + c(WD) * b["th"]), m, v
+
+
+def _same(got, want, what):
+    bad = (got.view(np.uint32) != want.view(np.uint32)) & ~(np.isnan(got) & np.isnan(want))
+    assert not bad.any(), (what, int(bad.sum()), np.flatnonzero(bad)[:8], got[bad][:4], want[bad][:4])
+
+
+def _step_and_check(zs, case, eps=EPS, beta2=BETA2, codes=False):
+    before = case.host(0)
+    zs.zero_tensors_adamw_async(case.list, zs.adam(LR, BETA1, beta2, eps, WD), _ctrl(zs, 1.0))
+    th, m, v = _definition(before, case.state, 1.0, eps, beta2)
+    got = case.host(0)
+    _same(got["th"], th, "weights")
+    if case.state == 32:
+        _same(got["m"], m, "m")
+        _same(got["v"], v, "v")
+    elif codes:
+        for name, x, signed in (("m", m, True), ("v", v, False)):
+            code, scale = base._encode(x, signed)
+            assert np.array_equal(got[name], code) and np.array_equal(got[name + "s"], scale), name
+    return th
+
+
+@pytest.mark.parametrize("lead", [0, 3])
+@pytest.mark.parametrize("where", [0, 5, 300, N - 1])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("which", ["m", "v", "both"])
+def test_nan_and_infinite_moments(zs, cuda_device, which, bad, where, lead):
+    for quiet in (False, True):                # among usual values, and among zeros
+        case = _Case(zs, [N], 32, torch.float32, None, 3, lead=lead)
+        if quiet:
+            for x in (case.grad, case.m, case.v):
+                x[case.at[0]:case.at[0] + N] = 0
+        if which != "v":
+            case.m[case.at[0] + where] = bad
+        if which != "m":
+            case.v[case.at[0] + where] = bad
+        th = _step_and_check(zs, case)
+        assert np.isnan(th).sum() == (0 if (which, bad) == ("v", math.inf) or (which, bad) == ("m", math.inf) else 1)
+
+
+@pytest.mark.parametrize("lead", [0, 5])
+@pytest.mark.parametrize("scale", ["ms", "vs"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_nan_and_infinite_scales_of_8_bit_states(zs, cuda_device, bad, scale, lead):
+    case = _Case(zs, [N], 8, torch.bfloat16, None, 4, lead=lead)
+    case.v[case.at[0] + 2 * BLOCK + 9] = 0     # 0 * inf
+    case.m[case.at[0] + 2 * BLOCK + 9] = 0
+    getattr(case, scale)[0][2] = bad
+    th = _step_and_check(zs, case)
+    assert np.isnan(th[2 * BLOCK + 9])
+
+
+def test_a_huge_gradient_without_the_norm_pass(zs, cuda_device):
+    """One gradient above 2^64: v' is infinite, and in the next step the states
+    that are 0 decode to NaN, which the weights show."""
+    case = _Case(zs, [N], 8, torch.float32, None, 5)
+    case.grad[:N] = 0.0
+    case.m[:N], case.v[:N] = 0, 0
+    case.grad[BLOCK + 1] = 2.0 ** 65
+    hp, ctrl = zs.adam(LR, BETA1, BETA2, EPS, WD), _ctrl(zs, 1.0)
+    zs.zero_tensors_adamw_async(case.list, hp, ctrl)
+    assert math.isinf(case.vs[0][1].item()) and case.master[:N].isfinite().all()
+    case.grad[:N] = 0.01
+    zs.zero_tensors_adamw_async(case.list, hp, ctrl)
+    th = case.master[:N]
+    assert th[BLOCK:2 * BLOCK].isnan().all() and th[:BLOCK].isfinite().all() and th[2 * BLOCK:].isfinite().all()

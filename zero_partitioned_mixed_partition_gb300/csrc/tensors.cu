@@ -324,12 +324,20 @@ __device__ __forceinline__ Coef2 coef2_of(const StepCoef& s, float one) {
 // unit of the last place off.
 __device__ __forceinline__ uint64_t add2_apart(uint64_t a, uint64_t b, uint64_t one) { return fma2(a, one, b); }
 
+// The larger of two, NaN if one is (fmaxf passes over a NaN).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // The Adam / AdamW update of eight coordinates from their gradients (raw, as
 // pairs): the operations of adam_apply, two coordinates at a time.  Divisions and
 // square roots are the correctly rounded ones above where all of a warp's values
 // lie in [2^-80, 2^40], with any bias correction in their ranges, or all eight of
 // a thread's are 0 (weights that no gradient has reached), and else the scalar
-// ones.  m, v: in and out, as pairs.
+// ones.  The tests pass over a NaN, which comes out of either as a NaN.  m, v: in
+// and out, as pairs.
 __device__ __forceinline__ void adam_eight(const Coef2& c, float lr, float wd, const uint64_t* g, float* th, uint64_t* m,
                                            uint64_t* v) {
     float low = 1.0f, high = 0.0f;  // the smallest and largest |m'|, v'
@@ -361,7 +369,7 @@ __device__ __forceinline__ void adam_eight(const Coef2& c, float lr, float wd, c
         const uint64_t mh = div2_by_constant(m[j], c.bc1, c.rcp_bc1), vh = div2_by_constant(v[j], c.bc2, c.rcp_bc2);
         float u0, u1, p, q;
         split(vh, p, q);  // (a v' of 0 belongs to an m' of 0: any root will do)
-        split(div2(mh, add2(sqrt2(pair(fmaxf(p, 0x1p-80f), fmaxf(q, 0x1p-80f))), eps)), u0, u1);
+        split(div2(mh, add2(sqrt2(pair(max_nan(p, 0x1p-80f), max_nan(q, 0x1p-80f))), eps)), u0, u1);
         th[2 * j] = __fsub_rn(th[2 * j], __fmul_rn(lr, __fadd_rn(u0, __fmul_rn(wd, th[2 * j]))));
         th[2 * j + 1] = __fsub_rn(th[2 * j + 1], __fmul_rn(lr, __fadd_rn(u1, __fmul_rn(wd, th[2 * j + 1]))));
     }
