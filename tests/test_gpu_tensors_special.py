@@ -1,5 +1,5 @@
-"""The AdamW step over a list of tensors where its states are NaN or infinite.
-The definition in fp32, one rounding per operation (numpy), gives what must come
+"""The AdamW step over a list of tensors where its states are NaN or infinite,
+or its eps is 0.  The definition in fp32, one rounding per operation (numpy), gives what must come
 out; a NaN may carry any bits."""
 import math
 
@@ -93,3 +93,18 @@ def test_a_huge_gradient_without_the_norm_pass(zs, cuda_device):
     zs.zero_tensors_adamw_async(case.list, hp, ctrl)
     th = case.master[:N]
     assert th[BLOCK:2 * BLOCK].isnan().all() and th[:BLOCK].isfinite().all() and th[2 * BLOCK:].isfinite().all()
+
+
+@pytest.mark.parametrize("state", [32, 8])
+@pytest.mark.parametrize("lead", [0, 1, 7])
+@pytest.mark.parametrize("eps", [0.0, 1e-60, 1e-30])
+def test_eps_of_zero(zs, cuda_device, state, lead, eps):
+    """Weights without gradient and states among others: 0 / 0 where eps is 0 in
+    fp32, as one element at a time, whatever its neighbours are."""
+    case = _Case(zs, [N], state, torch.float32, None, 6, lead=lead)
+    at = case.at[0]
+    for a, b in ((0, 3), (40, 45), (1024, 4096), (N - 5, N)):
+        for x in (case.grad, case.m, case.v):
+            x[at + a:at + b] = 0
+    th = _step_and_check(zs, case, eps=eps, codes=True)
+    assert np.isnan(th).any() == (F(eps) == 0)
