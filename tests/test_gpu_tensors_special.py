@@ -1,6 +1,7 @@
 """The AdamW step over a list of tensors where its states are NaN or infinite,
-or its eps is 0.  The definition in fp32, one rounding per operation (numpy), gives what must come
-out; a NaN may carry any bits."""
+its eps is 0 or huge, or its beta2 next to 1.  The definition in fp32, one
+rounding per operation (numpy), gives what must come out; a NaN may carry any
+bits."""
 import math
 
 import numpy as np
@@ -108,3 +109,28 @@ def test_eps_of_zero(zs, cuda_device, state, lead, eps):
             x[at + a:at + b] = 0
     th = _step_and_check(zs, case, eps=eps, codes=True)
     assert np.isnan(th).any() == (F(eps) == 0)
+
+
+@pytest.mark.parametrize("state", [32, 8])
+@pytest.mark.parametrize("lead", [0, 7])
+@pytest.mark.parametrize("eps", [1e10, 1e25, 1e38, 1e39, 1e300])
+def test_eps_of_any_size(zs, cuda_device, state, lead, eps):
+    """From 1e39 on it is infinite in fp32, and u is 0."""
+    case = _Case(zs, [N], state, torch.float32, None, 6, lead=lead)
+    for x in (case.grad, case.m, case.v):
+        x[case.at[0] + 1024:case.at[0] + 4096] = 0
+    assert np.isfinite(_step_and_check(zs, case, eps=eps, codes=True)).all()
+
+
+@pytest.mark.parametrize("state", [32, 8])
+@pytest.mark.parametrize("beta2", [1 - 2.0 ** -20, 1 - 2.0 ** -40, 1 - 2.0 ** -53])
+def test_beta2_next_to_one(zs, cuda_device, state, beta2):
+    """The bias correction of the first step is down to 2^-53."""
+    case = _Case(zs, [N], state, torch.float32, None, 7)
+    case.grad[:BLOCK] *= 1e4
+    case.grad[BLOCK:2 * BLOCK] *= 1e-15
+    if state == 32:
+        case.v[:BLOCK] *= 1e15
+        case.m[BLOCK:2 * BLOCK] *= 1e-20
+        case.v[BLOCK:2 * BLOCK] = 1e12
+    _step_and_check(zs, case, beta2=beta2, codes=True)

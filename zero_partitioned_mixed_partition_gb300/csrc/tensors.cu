@@ -311,12 +311,16 @@ __device__ __forceinline__ void step_coef(const StepShared& p, StepCoef* s) {
 struct Coef2 {
     uint64_t b1, c1, b2, c2, inv, clip, one;
     float bc1, bc2, rcp_bc1, rcp_bc2, eps;
-    float high;  // where adam_eight's largest value starts: 0 lets a group of zeros pass
+    // where adam_eight's smallest and largest value start: a low below 2^-80 sends
+    // every group to the scalar operations, a high above 0 groups of zeros
+    float low, high;
 };
 __device__ __forceinline__ Coef2 coef2_of(const StepCoef& s, float one) {
+    // (with these a root's argument is at most 2^80 and its sum with eps 2^41)
+    const bool fast = s.c.eps <= 0x1p40f && s.c.bc1 >= 0x1p-40f && s.c.bc2 >= 0x1p-40f;
     return Coef2{pair(s.c.b1, s.c.b1), pair(s.c.c1, s.c.c1), pair(s.c.b2, s.c.b2), pair(s.c.c2, s.c.c2),
                  pair(s.c.inv, s.c.inv), pair(s.clip, s.clip), pair(one, one), s.c.bc1, s.c.bc2, __frcp_rn(s.c.bc1),
-                 __frcp_rn(s.c.bc2), s.c.eps, s.c.eps > 0.0f ? 0.0f : 0x1p-80f};
+                 __frcp_rn(s.c.bc2), s.c.eps, fast ? 1.0f : 0.0f, fast && s.c.eps > 0.0f ? 0.0f : 0x1p-80f};
 }
 
 // a + b for products of pairs that have been rounded: as a 1 + b, with a 1 that
@@ -335,13 +339,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // The Adam / AdamW update of eight coordinates from their gradients (raw, as
 // pairs): the operations of adam_apply, two coordinates at a time.  Divisions and
 // square roots are the correctly rounded ones above where all of a warp's values
-// lie in [2^-80, 2^40], with any bias correction in their ranges, or all eight of
-// a thread's are 0 (weights that no gradient has reached; with eps = 0 they have
-// no quotient, and the scalar ones say so), and else the scalar ones.  The tests pass over a NaN, which comes out of either as a NaN.  m, v: in
-// and out, as pairs.
+// lie in [2^-80, 2^40] and eps and the bias corrections keep what follows in those
+// operations' ranges, or all eight of a thread's are 0 (weights that no gradient
+// has reached; with eps = 0 they have no quotient, and the scalar operations say
+// so), and else the scalar ones.  The tests pass over a NaN, which comes out of
+// either as a NaN.  m, v: in and out, as pairs.
 __device__ __forceinline__ void adam_eight(const Coef2& c, float lr, float wd, const uint64_t* g, float* th, uint64_t* m,
                                            uint64_t* v) {
-    float low = 1.0f, high = c.high;  // the smallest and largest |m'|, v'
+    float low = c.low, high = c.high;  // the smallest and largest |m'|, v'
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint64_t x = mul2(mul2(g[j], c.inv), c.clip);
