@@ -829,9 +829,10 @@ typedef struct zs_tensor {
 /* *sqnorm_dev (DEVICE fp64) = the sum of g^2 over every tensor, g = grad / L
  * rounded to fp32 and L the loss scale of *ctrl_dev; squares and sums of eight
  * of them are fp32, the sums of those fp64 or as exact, in a fixed order.  A
- * gradient that is not finite, or of magnitude 2^62 or more after unscaling
- * (from 2^60 on it may be), sets ctrl->overflow, so that the step that follows is
- * skipped.  Only grad, grad_type and n of each tensor are used.
+ * gradient that is not finite, or of magnitude 2^62 or more after unscaling, sets
+ * ctrl->overflow, so that the step that follows is skipped; smaller ones do, from
+ * 2^60 or with very many of them from 2^54 on, where a partial sum of squares
+ * passes fp32's range.  Only grad, grad_type and n of each tensor are used.
  * The partial sums of up to some hundred tensors share a launch.
  * Source: "DeepSpeed ZeRO Stages", sec. 2.1, Fact 1 (clipping); the non-finite test: the dynamic
  *   loss-scale rule. */

@@ -1,7 +1,7 @@
 """The AdamW step over a list of tensors where its states are NaN or infinite,
-its eps is 0 or huge, or its beta2 next to 1.  The definition in fp32, one
-rounding per operation (numpy), gives what must come out; a NaN may carry any
-bits."""
+its eps is 0 or huge, its beta2 next to 1, or the sum of its gradients' squares
+passes fp32's range.  The definition in fp32, one rounding per operation
+(numpy), gives what must come out; a NaN may carry any bits."""
 import math
 
 import numpy as np
@@ -134,3 +134,22 @@ def test_beta2_next_to_one(zs, cuda_device, state, beta2):
         case.m[BLOCK:2 * BLOCK] *= 1e-20
         case.v[BLOCK:2 * BLOCK] = 1e12
     _step_and_check(zs, case, beta2=beta2, codes=True)
+
+
+def test_squares_that_overflow_a_sum(zs, cuda_device):
+    """Gradients just below the size that is refused one by one, 2^62: their sum
+    passes the largest fp32.  Such a step may be skipped; it may not be taken
+    unclipped."""
+    n = 48_000_000
+    grad = torch.full((n,), 2.0 ** 61 * 0.99, device="cuda")
+    master, m, v = (torch.zeros(n, device="cuda") for _ in range(3))
+    lst, ctrl, sq = zs.TensorList([zs.TensorView(grad, master, m, v)]), _ctrl(zs, 1.0), zs.new_sqnorm()
+    zs.zero_tensors_sqnorm_async(lst, sq, zs.new_work(), ctrl)
+    zs.zero_tensors_adamw_async(lst, zs.adam(LR), ctrl, max_norm=1.0, sqnorm_dev=sq)
+    c = zs.read_ctrl(ctrl)
+    if c["skipped"] == 0:
+        # clipped to a norm of 1: m = (1 - beta1) / sqrt(n) everywhere
+        assert abs(sq.item() / (n * grad[0].item() ** 2) - 1) < 1e-6
+        assert abs(m[0].item() * math.sqrt(n) / 0.1 - 1) < 1e-5
+    else:
+        assert (m == 0).all() and c["step"] == 0

@@ -223,6 +223,8 @@ __global__ void __launch_bounds__(kNormThreads) tensors_sqnorm_kernel(const __gr
             add(part);
         }
     }
+    // (sixteen parts just below the test's bound already pass the largest fp32)
+    bad |= !(fabsf(sum.hi) < INFINITY);
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(&p.ctrl->overflow, 1);
     auto block_sum = [&](double x) {  // in the first thread; the order is fixed
         x = warp_sum(x);
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kNormThreads) tensors_sqnorm_kernel(const __gr
             for (int w = 0; w < kWarps; ++w) x += s_part[w];
         return x;
     };
-    const double block = block_sum((double)sum.hi + (double)sum.lo);
+    const double block = block_sum(sum.value());
     if (threadIdx.x == 0) p.work->part[p.base + blockIdx.x] = block;
     if (!p.finish || !last_to_arrive(p.work, gridDim.x)) return;
     double all = 0.0;
