@@ -93,20 +93,21 @@ __global__ void __launch_bounds__(kPairThreads, kPairBlocks) preference_loss_ker
     griddep_wait();
     griddep_launch_dependents();
     if (ctas > 1) cluster_wait();
-    const int32_t cluster = (int32_t)blockIdx.x / ctas, clusters = (int32_t)gridDim.x / ctas;
+    const uint32_t cluster = blockIdx.x / (uint32_t)ctas, clusters = gridDim.x / (uint32_t)ctas;
+    const uint32_t n_pairs = (uint32_t)p.n_pairs;  // (up to 2^31 - 1: one cluster further still has 32 bits)
     const int32_t me = rank * kPairThreads + tid, step = ctas * kPairThreads;
     double sum[ZS_PREFERENCE_TOTALS] = {};  // of the cluster's first thread
     int par = 0;
     int64_t next_cu[3] = {0, 0, 0};
     float next_w = 0.0f;
-    auto fetch = [&](int32_t i) {  // a pair's offsets and weight, one pair ahead
-        if (i >= p.n_pairs) return;
+    auto fetch = [&](uint32_t i) {  // a pair's offsets and weight, one pair ahead
+        if (i >= n_pairs) return;
 #pragma unroll
         for (int k = 0; k < 3; ++k) next_cu[k] = p.cu[2 * (int64_t)i + k];
         next_w = p.weights != nullptr ? p.weights[i] : p.uniform_weight;
     };
     fetch(cluster);
-    for (int32_t i = cluster; i < p.n_pairs; i += clusters) {
+    for (uint32_t i = cluster; i < n_pairs; i += clusters) {
         const float w = next_w;
         const Range r0 = range_of(p, next_cu[0], next_cu[1]), r1 = range_of(p, next_cu[1], next_cu[2]);
         fetch(i + clusters);
@@ -320,10 +321,10 @@ __global__ void __launch_bounds__(kPairThreads, kPairBlocks) preference_loss_ker
     if (rank != 0) return;
     if (tid == 0)
         for (int q = 0; q < ZS_PREFERENCE_TOTALS; ++q) p.work->part[cluster * ZS_PREFERENCE_TOTALS + q] = sum[q];
-    if (!last_to_arrive(p.work, (uint32_t)clusters)) return;
+    if (!last_to_arrive(p.work, clusters)) return;
     if (warp < ZS_PREFERENCE_TOTALS) {
         double t = 0.0;
-        for (int32_t b = lane; b < clusters; b += 32) t += *(volatile double*)&p.work->part[b * ZS_PREFERENCE_TOTALS + warp];
+        for (uint32_t b = lane; b < clusters; b += 32) t += *(volatile double*)&p.work->part[b * ZS_PREFERENCE_TOTALS + warp];
         t = warp_sum(t);
         if (lane == 0) s_total[warp] = t;
     }
