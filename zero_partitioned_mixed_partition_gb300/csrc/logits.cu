@@ -39,10 +39,7 @@
 #include <cfloat>
 #include <initializer_list>
 
-#include <map>
-#include <mutex>
-#include <tuple>
-
+#include "cluster_counts.h"
 #include "zs_internal.h"
 
 namespace {
@@ -1084,7 +1081,9 @@ int32_t launch_rows(RowArgs& a, cudaStream_t stream) {
     const cudaError_t ready =
         cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, buffer_bytes(1));
     if (ready != cudaSuccess) return zs::cuda_fail(ready, "rows_kernel");
-    int64_t clusters = active_clusters((const void*)kernel, NT + 64, pl.ctas, smem);
+    cudaError_t err = cudaSuccess;
+    int64_t clusters = active_clusters((const void*)kernel, NT + 64, pl.ctas, smem, &err);
+    if (clusters < 1) return zs::cuda_fail(err, "rows_kernel");
     if (clusters > kWorkParts / ZS_POLICY_TOTALS) clusters = kWorkParts / ZS_POLICY_TOTALS;
     // groups of about 32 clusters, of one size; some clusters may be left out
     int group = 1;

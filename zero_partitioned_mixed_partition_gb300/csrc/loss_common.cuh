@@ -1,7 +1,7 @@
 // loss_common.cuh -- device and host code shared by the loss kernels
 // (logits.cu, preference.cu) and the tensor-list kernels (tensors.cu).
 // Included inside an anonymous namespace after step_common.cuh and
-// step_end.cuh.
+// step_end.cuh; cluster_counts.h before it, outside.
 #pragma once
 
 #include "packed.cuh"
@@ -84,37 +84,31 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 constexpr int kMaxCluster = 8;
 
-// How many clusters of a kernel run at once (cached: it does not change).
-int active_clusters(const void* kernel, int threads, int ctas, int smem) {
-    static std::mutex mu;
-    static std::map<std::tuple<const void*, int, int>, int> known;
-    const auto key = std::make_tuple(kernel, ctas, smem);
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        auto it = known.find(key);
-        if (it != known.end()) return it->second;
-    }
-    int n = 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ctas * zs::device_sm_count()));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+// How many clusters of a kernel run at once on the current device; 0 and *err
+// set if that could not be found.
+int active_clusters(const void* kernel, int threads, int ctas, int smem, cudaError_t* err) {
+    static zs::ClusterCounts counts;
+    int device = 0;
+    *err = cudaGetDevice(&device);
+    if (*err != cudaSuccess) return 0;
+    return counts.get(device, kernel, ctas, smem, [&] {
+        int n = 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(ctas * zs::device_sm_count()));
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        *err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (*err == cudaSuccess && n < 1) *err = cudaErrorInvalidConfiguration;
+        if (*err == cudaSuccess) return n;
         cudaGetLastError();
-        n = 1;
-    }
-    try {
-        std::lock_guard<std::mutex> lock(mu);
-        known[key] = n;
-    } catch (...) {  // no memory to remember it: found again at the next call
-    }
-    return n;
+        return 0;
+    });
 }
 
 // Enqueues `clusters` clusters of `ctas` blocks with programmatic serialization.

@@ -9,10 +9,7 @@
 
 #include <cuda_fp16.h>
 
-#include <map>
-#include <mutex>
-#include <tuple>
-
+#include "cluster_counts.h"
 #include "zs_internal.h"
 
 namespace {
@@ -369,7 +366,9 @@ ZS_API int32_t zero_preference_loss_async(const float* logp, const float* ref_lo
     int ctas = 1;
     const int64_t mean = n_pairs > 0 ? n_tokens / n_pairs : 0;
     while (ctas < kMaxCluster && 2ll * ctas * n_pairs <= full && mean > (int64_t)ctas * kPairThreads * 4) ctas *= 2;
-    int clusters = active_clusters((const void*)preference_loss_kernel, kPairThreads, ctas, 0);
+    cudaError_t err = cudaSuccess;
+    int clusters = active_clusters((const void*)preference_loss_kernel, kPairThreads, ctas, 0, &err);
+    if (clusters < 1) return zs::cuda_fail(err, "preference_loss_kernel");
     if (clusters > n_pairs) clusters = n_pairs > 0 ? n_pairs : 1;
     return launch_clusters(preference_loss_kernel, clusters, ctas, kPairThreads, 0, (cudaStream_t)stream, a,
                            "preference_loss_kernel");

@@ -13,10 +13,7 @@
 #include <cmath>
 #include <cstring>
 
-#include <map>
-#include <mutex>
-#include <tuple>
-
+#include "cluster_counts.h"
 #include "zs_internal.h"
 
 namespace {
