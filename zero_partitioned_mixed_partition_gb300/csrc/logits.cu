@@ -197,11 +197,10 @@ __device__ __forceinline__ float c_residue(float top, float k) {
 }
 
 // How far the sums at top a lie above those at top b: the difference of their c,
-// where a slow one counts as top k.
+// where a slow one counts as top k.  (One expression for all: a branch for two fast
+// ones took 695 us where this takes 688, in the first case above.)
 __device__ __forceinline__ float top_gap(float a, float b, float k) {
-    const float ca = __fmul_rn(a, k), cb = __fmul_rn(b, k);
-    if (fabsf(ca) < kLargeC && fabsf(cb) < kLargeC) return fmaxf(ca - cb, kLowest);
-    return fmaxf((a - b) * k + (c_residue(a, k) - c_residue(b, k)), kLowest);
+    return fmaxf(fmaf(a - b, k, c_residue(a, k) - c_residue(b, k)), kLowest);
 }
 
 // How a vector's exponentials are formed, by the row's top: kSlow where c
