@@ -664,9 +664,10 @@ typedef struct zs_logits {
  *            saved may be NULL.
  * A logit of -inf has probability 0.  A row of nothing but -inf has no
  * distribution: logp = -inf, entropy = 0.  A NaN or +inf in a row gives NaN.
- * One pass over the logits, stream-ordered, one launch.  (The waits of the logits
- * kernels for their own copies are bounded; one that ran out, after a second or
- * so, would show as NaN in the outputs.)
+ * One pass over the logits, stream-ordered, one launch.  The waits of the logits
+ * kernels for their own copies and warps are bounded.  If one ran out, after a
+ * second or so, the kernel would end and leave NaN in every output of the rows
+ * that were dealt to the same blocks, and in the totals.
  * Source: the softmax cross-entropy of a language model; no counterpart in the pages. */
 ZS_API int32_t zero_token_logp_async(const zs_logits* x, const int64_t* labels, float* logp, float* entropy,
                                      float* saved, void* stream);
@@ -889,6 +890,14 @@ ZS_API int64_t zero_kernel_launches(void);
  * ZS_ERR_CUDA if the record cannot be read.
  * Source: no counterpart in the pages (a property of this library). */
 ZS_API int32_t zero_debug_checks(uint64_t* first_fault);
+
+/* Debug build: sets how many tries, 0 to 2^20 (the ordinary build's number), the
+ * waits of the logits kernels make for their own copies and warps before they
+ * give up, and returns 1.  With few tries waits run out that would have been met,
+ * which shows what a call does then (see zero_token_logp_async).  Synchronises
+ * the device.  The ordinary build changes nothing and returns 0.
+ * Source: no counterpart in the pages (a property of this library). */
+ZS_API int32_t zero_debug_wait_limit(int32_t tries);
 
 #ifdef __cplusplus
 }

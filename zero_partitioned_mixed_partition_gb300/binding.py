@@ -147,6 +147,7 @@ _SIGNATURES = {
     "zero_last_error": (ctypes.c_char_p, []),
     "zero_kernel_launches": (_I64, []),
     "zero_debug_checks": (_I32, [_P]),
+    "zero_debug_wait_limit": (_I32, [_I32]),
 }
 EXPORTED = tuple(_SIGNATURES)
 

@@ -80,6 +80,11 @@ ZS_API int32_t zero_debug_checks(uint64_t* first_fault) {
 #endif
 }
 
+ZS_API int32_t zero_debug_wait_limit(int32_t tries) {
+    if (tries < 0 || tries > 1 << 20) return ZS_ERR_ARG;
+    return zs::set_wait_limit(tries);
+}
+
 // Model-state bytes per device ("DeepSpeed ZeRO Stages", sec. 1.2 and 3):
 // three categories -- fp16 parameters (2 Psi), fp16 gradients (2 Psi) and
 // optimizer states (K Psi) -- and the stages partition them cumulatively,
