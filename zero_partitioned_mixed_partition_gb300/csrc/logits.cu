@@ -899,16 +899,26 @@ __global__ void __launch_bounds__(NT + 64, per_sm_of(NT)) rows_kernel(const __gr
         }
 
         // ---- the computing warps
-        // the buffer is free again, if every lane had it (false: not)
+        // The buffer is free again, if its waits were met; false: the warp stops.  With
+        // a gradient the warp agrees on that at every buffer.  Without one it agrees at a
+        // row's start and end, in between a lane whose wait ran out works on whatever is
+        // there, and the first lane, if it is that one, sets nothing free (scoring 8192 x
+        // 50257 bf16: 99.0 us so, 100.0 with every buffer; the policy loss is better with
+        // every buffer, 86.3 us for 86.7 in the second case above).
         auto release = [&](bool ok) {
-            if (!all_lanes(ok)) return false;
-            if (lane == 0) mbar_arrive(&s_empty[buf]);
+            if (GRAD) {
+                if (!all_lanes(ok)) return false;
+            } else {
+                __syncwarp();
+            }
+            if (lane == 0 && ok) mbar_arrive(&s_empty[buf]);
             advance();
             return true;
         };
         // first pass over the next row: its parts of the statistics (false: a wait ran out)
         auto first_pass = [&]() {
             bool ok = mbar_wait(&s_full[buf], phase, &s_failed);
+            if (!GRAD && !all_lanes(ok)) return false;
             const int32_t n = ok ? s_info[buf].n : 0;
             const int32_t edge_at = tid < 16 ? s_info[buf].edge_at[tid] : -1;
             const float x_edge = tid < 16 ? s_info[buf].edge[tid] : 0.0f;
@@ -930,7 +940,7 @@ __global__ void __launch_bounds__(NT + 64, per_sm_of(NT)) rows_kernel(const __gr
                 if (!release(ok)) return false;
                 first += p.piece;
                 if (first >= n) break;
-                ok = mbar_wait(&s_full[buf], phase, &s_failed);
+                ok = mbar_wait(&s_full[buf], phase, &s_failed) && (GRAD || ok);
             }
             if (edge_at >= 0) add_value<T, ENT>(run, x_edge, k);
             Stats st{run.top, 0.0f, 0.0f, 0.0f};
@@ -943,7 +953,7 @@ __global__ void __launch_bounds__(NT + 64, per_sm_of(NT)) rows_kernel(const __gr
             }
             st = join_warp<ENT>(st, k);
             // the parts of two rows before have been read
-            if (!GRAD && !all_lanes(mbar_wait(&s_done[par], par_phase ^ 1u, &s_failed))) return false;
+            if (!GRAD && !all_lanes(mbar_wait(&s_done[par], par_phase ^ 1u, &s_failed) && ok)) return false;
             if (lane == 0) {
                 s_warp[par][warp] = st;
                 mbar_arrive(&s_parts[par]);
@@ -1195,7 +1205,15 @@ int32_t launch_rows(RowArgs& a, cudaStream_t stream) {
     return launch_clusters(kernel, (int)clusters, pl.ctas, NT + 64, smem, stream, a, "rows_kernel");
 }
 
-// Blocks of 128 threads where a row has fewer vectors than 1024.
+// Blocks of 128 threads, four to an SM, where a row has fewer vectors than 1024:
+// more rows are under way and a thread has more of each.  Measured with both, us of
+// scoring, its gradient, and the policy loss with its gradient:
+//                     128 threads      256 threads
+//   8192 x 1000 bf16  20   19   41     31   29   64
+//   8192 x 8000 bf16  33   52   65     40   48   85
+//   8192 x 24000 bf16 69  136  145     74  134  158
+//   600 x 3001 bf16   8.2  8.6 14.4    7.4  8.2 13.3
+// (Some hundred rows are better off with 256, by up to a tenth.)
 template <typename T, int MODE, bool ENT>
 int32_t launch_sized(RowArgs& a, cudaStream_t stream) {
     if (a.vocab * (int64_t)sizeof(T) / 16 < 1024) return launch_rows<T, MODE, ENT, 128>(a, stream);
