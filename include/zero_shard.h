@@ -641,7 +641,7 @@ ZS_API int32_t zero_qwz_dequantize(const int8_t* codes_dev, const float* scales_
  *   row_stride   elements from one row to the next, >= vocab; any value is
  *                allowed, rows need not start on vector boundaries
  *   type         ZS_F32, ZS_F16 or ZS_BF16; reserved must be 0
- *   inv_temperature  it > 0: the distribution of a row is softmax(x it) */
+ *   inv_temperature  it in [1e-6, 1e6]: the distribution of a row is softmax(x it) */
 typedef struct zs_logits {
     const void* data;
     int64_t rows;
@@ -662,6 +662,9 @@ typedef struct zs_logits {
  *            is ignored: its logits are not read and its outputs are 0.
  *   logp, entropy, saved   DEVICE fp32 [rows], [rows], [2 rows]; entropy and
  *            saved may be NULL.
+ * Accuracy: the sum is held at a logit of the row up to 20 units of log2 below the
+ * largest, so ln S is off by some units of the last place of a number up to 14 +
+ * ln S (5e-7 where a token is almost certain), besides the exponentials' own.
  * A logit of -inf has probability 0.  A row of nothing but -inf has no
  * distribution: logp = -inf, entropy = 0.  A NaN or +inf in a row gives NaN.
  * One pass over the logits, stream-ordered, one launch.  The waits of the logits
@@ -791,6 +794,17 @@ ZS_API int32_t zero_preference_loss_async(const float* logp, const float* ref_lo
 /* (adapters, replicated or unpartitioned parameters, bf16 models).          */
 /* ------------------------------------------------------------------------ */
 
+/* A step over a list is a step of its own: like every step call,
+ * zero_tensors_adamw_async ends it in the control block (t and the powers of
+ * beta, cur, the overflow flag).  One step cannot hold a list and flat shards.
+ * With one control block t would advance twice and cur flip twice, and the call
+ * that comes first would use up the overflow flag; with two, a step skipped in
+ * one would be taken in the other, and their gradients would be clipped apart.
+ * All of a model's weights go into one list, or into shards.
+ * Both calls take 1 to ZS_MAX_TENSORS tensors; n of any of them may be 0, and a
+ * list of nothing but empty tensors still ends its step.  (Without any tensor
+ * they return ZS_ERR_ARG.) */
+
 /* Kinds of optimizer state. */
 #define ZS_STATE_F32 0
 #define ZS_STATE_U8 1
@@ -882,7 +896,7 @@ ZS_API int64_t zero_kernel_launches(void);
  * ZS_CHECKED=1 give libzeroshard_checked.so, whose kernels test every element
  * range they are about to touch against the extent the call was given (the
  * shard's n, or its qwZ block count); a failed test records the first failure
- * -- (site << 48) | first element, site 1-9 naming the kernel and access --
+ * -- (site << 48) | first element, site 1-17 naming the kernel and access --
  * and skips the access instead of trapping.  This call synchronises the
  * device, writes that record (0: none) to *first_fault, clears it, and
  * returns 1 in the checked build; the ordinary build has no checks and

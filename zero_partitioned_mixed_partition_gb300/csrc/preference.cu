@@ -20,8 +20,9 @@ namespace {
 
 [[maybe_unused]] constexpr uint32_t kSitePair = 17;
 
-// (4096 pairs, 8.2 M tokens: 96 threads and 10 blocks took 36 us, 64 and 16 took
-// 43, 256 and 4 took 47, where these take 34 with the same dealing of pairs.)
+// (4096 pairs, 8.2 M tokens, in a build that dealt pairs in runs of equal tokens:
+// these took 34 us, 96 threads and 10 blocks 36, 64 and 16 43, 256 and 4 47.  Dealt
+// by number, as here, these take 35 and 64 and 16 took 48.)
 constexpr int kPairThreads = 128, kPairWarps = kPairThreads / 32, kPairBlocks = 8;  // blocks of an SM
 constexpr int kBatch = 4;  // fours that a thread loads together
 
@@ -75,9 +76,9 @@ __device__ __forceinline__ Range range_of(const PairArgs& p, int64_t u, int64_t 
 // thread a few fours, so what a pair costs whatever its length (the sums' joining,
 // the loss) is kept to four warps.
 // Measured: 4096 pairs, 8.2 M tokens, 35 us, 3.0 TB/s of the bytes that have to
-// move (147 us in the first form, token by token).  It fills neither memory (44 %)
+// move (147 us in the first form, token by token).  It fills neither memory (45 %)
 // nor issue (2.1 of 4 slots); waiting at the barriers around a pair's serial part is
-// its most frequent stall.
+// its most frequent stall, and pairs are dealt by number, whatever their lengths.
 __global__ void __launch_bounds__(kPairThreads, kPairBlocks) preference_loss_kernel(const __grid_constant__ PairArgs p) {
     __shared__ double s_sum[kPairWarps][2];
     __shared__ int64_t s_count[kPairWarps][2];
