@@ -713,7 +713,8 @@ typedef struct zs_policy {
  *   pg    = max(-A r, -A clip(r, 1 - clip_low, 1 + clip_high))
  *           and, with dual_clip c > 0 and A < 0, at most -A c
  *   kl    = exp(ref_logp - logp) - (ref_logp - logp) - 1      (0 without ref_logp)
- *   loss  = pg + kl_coef kl - entropy_coef entropy
+ *   loss  = pg + kl_coef kl - entropy_coef entropy     (a term of coefficient 0 is
+ *           left out, even if it is infinite)
  * and over the rows, w the row's weight:
  *   totals = sum_rows w { loss, pg, kl, entropy, [the gradient of pg is cut off] }
  *   dlogits = L d totals[0] / d logits   (L the loss scale of *ctrl_dev; NULL: 1)

@@ -856,10 +856,11 @@ __global__ void __launch_bounds__(NT + 64, per_sm_of(NT)) rows_kernel(const __gr
                         float kl = 0.0f, dlogp = cut ? 0.0f : free_pg;
                         if (p.ref_logp != nullptr) {
                             const float gap = ref_logp - logp, rise = expm1f(gap);
-                            kl = rise - gap;
-                            dlogp -= p.kl * rise;
+                            kl = rise == INFINITY ? rise : rise - gap;
+                            if (p.kl != 0.0f) dlogp -= p.kl * rise;  // (0 times an infinite one has no value)
                         }
-                        loss = pg + p.kl * kl;
+                        loss = pg;
+                        if (p.kl != 0.0f) loss += p.kl * kl;
                         if (ENT) loss -= p.ent_coef * ent;
                         if (rank == 0 && lane == 0) {
                             sum[0] += (double)w * loss;
