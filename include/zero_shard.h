@@ -710,7 +710,7 @@ typedef struct zs_policy {
  * with respect to the logits, and its statistics, in one launch that reads the
  * logits from memory once.  Per row, with logp and entropy as in zero_token_logp_async:
  *   r     = exp(logp - old_logp)
- *   pg    = max(-A r, -A clip(r, 1 - clip_low, 1 + clip_high))
+ *   pg    = max(-A r, -A clip(r, 1 - clip_low, 1 + clip_high)), 0 where A is
  *           and, with dual_clip c > 0 and A < 0, at most -A c
  *   kl    = exp(ref_logp - logp) - (ref_logp - logp) - 1      (0 without ref_logp)
  *   loss  = pg + kl_coef kl - entropy_coef entropy     (a term of coefficient 0 is

@@ -53,3 +53,21 @@ def test_kl_with_a_coefficient(zs, cuda_device, kl):
     e = _err(V)
     tol = (2 * e + 320 * U) * 4 * ((plain.abs() + kl / ROWS * (p + hot))) + HALF_UNIT[torch.float32] * 4 * (plain + more).abs() + TINY[torch.float32]
     _close(out, plain + more, tol, "dlogits")
+
+
+@pytest.mark.parametrize("dual", [0.0, 3.0])
+def test_a_ratio_past_fp32(zs, cuda_device, dual):
+    """logp - old_logp of 100: exp passes fp32.  With A = 0 the loss and its
+    gradient are 0; with A > 0 the clipped bound holds; with A < 0 the loss is
+    past fp32 too, or capped."""
+    x, y, _, _, _, _ = _policy_inputs(ROWS, V, torch.float32, 5)
+    logp64 = torch.log_softmax(x.double(), 1).gather(1, y[:, None])[:, 0]
+    old = (logp64 - 100.0).float()
+    adv = torch.tensor([0.0, 1.0, -1.0, -0.0, 0.5, 0.0], device="cuda")
+    old[5] = -INF
+    logp, loss, totals, out = _run(zs, x, y, old, adv, {"dual_clip": dual}, None)
+    want = [0.0, -1.2, 3.0 if dual else INF, 0.0, -0.6, 0.0]
+    for i, w in enumerate(want):
+        assert loss[i].item() == w or abs(loss[i].item() - w) <= 4 * U * abs(w), i
+    still = [0, 1, 3, 4, 5] + ([2] if dual else [])
+    assert (out[still] == 0).all()

@@ -845,7 +845,8 @@ __global__ void __launch_bounds__(NT + 64, per_sm_of(NT)) rows_kernel(const __gr
                     if (POLICY && some) {
                         const float ratio = expf(logp - old_logp);
                         const float held = fminf(fmaxf(ratio, p.lo), p.hi);
-                        const float free_pg = -adv * ratio, held_pg = -adv * held;
+                        // (no advantage, no loss, although the ratio may have passed fp32)
+                        const float free_pg = adv == 0.0f ? 0.0f : -adv * ratio, held_pg = -adv * held;
                         bool cut = free_pg < held_pg;
                         float pg = cut ? held_pg : free_pg;
                         if (p.dual > 0.0f && adv < 0.0f && pg > -adv * p.dual) {
