@@ -23,10 +23,10 @@
 // six CTAs.
 //
 // Measured on one GB300 (6787 GB/s copied): policy loss and gradient, 8192 x
-// 131072 bf16, a tenth of the rows left out, with entropy: 686 us, 5.95 TB/s of
+// 131072 bf16, a tenth of the rows left out, with entropy: 683 us, 5.97 TB/s of
 // the bytes that have to move; 4096 x 32000 bf16, 30 % left out, no entropy:
-// 87 us, 5.2 TB/s; log-probabilities, 8192 x 50257 bf16, a quarter left out:
-// 100 us, 6.2 TB/s.  Nothing is full in the first: 88 % of the copy rate, and 2.2 of 4
+// 87 us, 5.1 TB/s; log-probabilities, 8192 x 50257 bf16, a quarter left out:
+// 99 us, 6.2 TB/s.  Nothing is full in the first: 88 % of the copy rate, and 2.2 of 4
 // issue slots a cycle (on 1024 rows; 130 instructions for 8 logits, 87 of them in
 // the two passes' loops).  In the second a CTA takes its rows one at a time, so the
 // turn from statistics to gradient stands open in each (an estimated 1.5 us of
