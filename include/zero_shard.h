@@ -791,6 +791,189 @@ ZS_API int32_t zero_preference_loss_async(const float* logp, const float* ref_lo
                                           float* dlogp, float* totals, void* work_dev, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The two ends of a language model: token log-probabilities straight from    */
+/* hidden states and the vocabulary matrix (the logits are never kept), layer */
+/* norm, and the embedding lookup, each with its gradient.                    */
+/* ------------------------------------------------------------------------ */
+
+/* A language model's head: the logits x_ij = sum_k hidden[i][k] weight[j][k] of
+ * `rows` tokens over a vocabulary of `vocab` entries, formed piece by piece.
+ *   hidden   DEVICE [rows][width], hidden_stride >= width elements from row to row
+ *   weight   DEVICE [vocab][width], weight_stride >= width
+ *   rows     0 to 2^24; vocab 1 to 2^24; width 8 to 65536
+ *   type     ZS_F16 or ZS_BF16, of both (products are exact in fp32, and summed
+ *            there; a model's computing copies have these types); reserved: 0
+ *   inv_temperature  it in [1e-6, 1e6]: a row's distribution is softmax(x it)
+ * width and the strides are multiples of 8, the matrices (and the outputs
+ * dhidden, dweight) start on 16-byte boundaries: the tensor cores' operands come
+ * in boxes of whole 16-byte units.  The stride of a single row is not used. */
+typedef struct zs_head {
+    const void* hidden;
+    const void* weight;
+    int64_t rows;
+    int64_t vocab;
+    int64_t width;
+    int64_t hidden_stride;
+    int64_t weight_stride;
+    int32_t type;
+    int32_t reserved;
+    double inv_temperature;
+} zs_head;
+
+/* Bytes of scratch that the head's calls need for these sizes: gradient 0 for
+ * zero_head_logp_async, 1 for zero_head_logp_grad_async.  The gradient call forms
+ * the gradient of the logits for `piece` entries of the vocabulary at a time
+ * (rounded up to a multiple of 256; 0: as many as fit 1 GiB); it takes the largest
+ * piece that the buffer it is given holds.  Returns ZS_ERR_ARG for sizes out of
+ * range.  No CUDA call.
+ * Source: no counterpart in the pages. */
+ZS_API int64_t zero_head_work_bytes(int64_t rows, int64_t width, int64_t vocab, int64_t piece, int32_t gradient);
+
+/* Log-probability of each row's label, as zero_token_logp_async has it from the
+ * logits: with t_i a logit near the row's largest, logp_i = (x_iy - t_i) it -
+ * ln sum_j exp((x_ij - t_i) it), all in fp32 from fp32 logits.
+ *   labels   DEVICE int64[rows]; a row whose label is outside [0, vocab) is
+ *            ignored: its hidden state is not used, its outputs are 0
+ *   logp     DEVICE fp32[rows]
+ *   saved    DEVICE fp32[2 rows] or NULL: t_i, ln sum_j exp((x_ij - t_i) it)
+ *   work_dev DEVICE scratch on a 128-byte boundary, work_bytes >=
+ *            zero_head_work_bytes(rows, width, vocab, 0, 0) of it.  It holds nothing
+ *            between calls; calls that may run at the same time need one each.
+ * A logit of -inf has probability 0; a row of nothing but -inf has logp = -inf.
+ * A NaN or +inf among a row's logits gives NaN.  The waits of the product
+ * kernels for their own copies are bounded, as those of the logits kernels are;
+ * one that ran out would leave NaN in the outputs it concerns.
+ * Stream-ordered.  Source: the softmax cross-entropy of a language model; no
+ * counterpart in the pages. */
+ZS_API int32_t zero_head_logp_async(const zs_head* h, const int64_t* labels, float* logp, float* saved,
+                                    void* work_dev, int64_t work_bytes, void* stream);
+
+/* Gradient of sum_rows dlogp logp with respect to the hidden states and the
+ * vocabulary matrix, times the loss scale L of *ctrl_dev (NULL: 1).  With
+ * p_ij = exp((x_ij - t_i) it - saved[2 i + 1]):
+ *   d_ij = L it dlogp_i (1[j = label_i] - p_ij)
+ *   dhidden_i = sum_j d_ij weight_j,   dweight_j = sum_i d_ij hidden_i
+ * The logits are formed anew.  p and d are fp32; d is rounded to the matrices'
+ * type for the two products (scaled by a power of 2 so that the largest dlogp
+ * lies at the top of fp16's range), whose sums are fp32, rounded once more at the
+ * end.  Every sum has a fixed order.
+ *   saved    DEVICE fp32[2 rows] of zero_head_logp_async (or of
+ *            zero_token_logp_async from the same logits)
+ *   dlogp    DEVICE fp32[rows].  Rows with dlogp = 0 are left out, as ignored
+ *            ones are: dhidden 0, nothing added to dweight.
+ *   dhidden  DEVICE [rows][width], dhidden_stride >= width, or NULL
+ *   dweight  DEVICE [vocab][width], dweight_stride >= width, or NULL; every row
+ *            is written.  One of the two at least.  They may not overlap the inputs
+ *            or each other.
+ *   work_dev, work_bytes   as above; at least zero_head_work_bytes(rows, width, vocab, 256, 1)
+ * Source: derivative of zero_head_logp_async; loss scale: the dynamic loss-scale rule. */
+ZS_API int32_t zero_head_logp_grad_async(const zs_head* h, const int64_t* labels, const float* saved,
+                                         const float* dlogp, const zs_ctrl* ctrl_dev, void* dhidden,
+                                         int64_t dhidden_stride, void* dweight, int64_t dweight_stride,
+                                         void* work_dev, int64_t work_bytes, void* stream);
+
+/* Layer norm over rows of `width` elements.
+ *   x        DEVICE [rows][width], x_stride >= width elements from row to row
+ *   gamma, beta   DEVICE [width] of param_type, or NULL (1 and 0)
+ *   rows     0 to 2^31 - 1; width 1 to 2^24
+ *   type, param_type   ZS_F32, ZS_F16 or ZS_BF16
+ *   eps      finite, >= 0
+ * Any alignment to the element; 16-byte boundaries of every row allow vectors. */
+typedef struct zs_norm {
+    const void* x;
+    const void* gamma;
+    const void* beta;
+    int64_t rows;
+    int64_t width;
+    int64_t x_stride;
+    int32_t type;
+    int32_t param_type;
+    double eps;
+} zs_norm;
+
+/* y = (x - mean) rstd gamma + beta with mean = sum x / width and rstd =
+ * 1 / sqrt(sum (x - mean)^2 / width + eps), all in fp32 (the squares are of
+ * differences from the mean), y rounded once to `type`.
+ *   y        DEVICE [rows][width], y_stride >= width; may be x (same stride)
+ *   saved    DEVICE fp32[2 rows] or NULL: mean, rstd
+ * A row with a NaN or an infinity gives NaN.  A constant row with eps = 0 has
+ * rstd = +inf and gives NaN.
+ * Source: layer normalization (Ba, Kiros, Hinton); the pages' models have it
+ * ("ln 2 x 768"), no step of the pages computes it. */
+ZS_API int32_t zero_layer_norm_async(const zs_norm* n, void* y, int64_t y_stride, float* saved, void* stream);
+
+/* Bytes of scratch of zero_layer_norm_grad_async (ZS_ERR_ARG for sizes out of
+ * range).  The same on every device.  No CUDA call.
+ * Source: no counterpart in the pages. */
+ZS_API int64_t zero_layer_norm_work_bytes(int64_t rows, int64_t width);
+
+/* Gradient of zero_layer_norm_async: with xh = (x - mean) rstd and a = dy gamma
+ *   dx = rstd (a - mean_k(a) - xh mean_k(a xh))
+ *   dgamma = sum_rows dy xh,   dbeta = sum_rows dy
+ * in fp32, each rounded once (dx to type, the others to param_type); the sums over
+ * rows have a fixed order.
+ *   dy       DEVICE [rows][width] of `type`, dy_stride >= width
+ *   saved    DEVICE fp32[2 rows] of the forward call; n->beta and n->eps are not used
+ *   dx       DEVICE [rows][width], dx_stride >= width, or NULL; may be dy or x
+ *            (same stride)
+ *   dgamma, dbeta   DEVICE [width] of param_type, or NULL; written, not added to
+ *   work_dev DEVICE scratch on a 16-byte boundary, work_bytes >=
+ *            zero_layer_norm_work_bytes(rows, width); NULL where dgamma and dbeta are
+ * With rows = 0 dgamma and dbeta become 0.
+ * Source: derivative of zero_layer_norm_async. */
+ZS_API int32_t zero_layer_norm_grad_async(const zs_norm* n, const void* dy, int64_t dy_stride, const float* saved,
+                                          void* dx, int64_t dx_stride, void* dgamma, void* dbeta, void* work_dev,
+                                          int64_t work_bytes, void* stream);
+
+/* An embedding lookup.
+ *   table    DEVICE [vocab][width], table_stride >= width elements from row to row
+ *   ids      DEVICE int64[tokens]; an id outside [0, vocab) gives a row of zeros
+ *            and no gradient
+ *   tokens   0 to 2^28; vocab 1 to 2^30; width 1 to 2^24
+ *   type     ZS_F32, ZS_F16 or ZS_BF16; reserved 0
+ *   scale    finite, rounded to fp32
+ * Any alignment to the element; 16-byte boundaries of every row allow vectors. */
+typedef struct zs_embed {
+    const void* table;
+    const int64_t* ids;
+    int64_t tokens;
+    int64_t vocab;
+    int64_t width;
+    int64_t table_stride;
+    int32_t type;
+    int32_t reserved;
+    double scale;
+} zs_embed;
+
+/* out_i = table[ids_i] scale, one fp32 product rounded once to `type` (none with
+ * scale 1).
+ *   out      DEVICE [tokens][width], out_stride >= width; may not overlap the table
+ * Source: the embedding of a language model; no counterpart in the pages. */
+ZS_API int32_t zero_embed_async(const zs_embed* e, void* out, int64_t out_stride, void* stream);
+
+/* Bytes of scratch of zero_embed_grad_async (ZS_ERR_ARG for sizes out of range).
+ * No CUDA call.
+ * Source: no counterpart in the pages. */
+ZS_API int64_t zero_embed_work_bytes(int64_t tokens, int64_t width);
+
+/* Gradient of the table: dtable_v = [dtable_v +] scale sum over the tokens i of
+ * id v of dout_i, summed in fp32 in a fixed order over the tokens sorted by id, rounded
+ * once to dtable_type.
+ *   e        e->table is not used (may be NULL); e->type is dout's
+ *   dout     DEVICE [tokens][width], dout_stride >= width
+ *   dtable   DEVICE [vocab][width] of dtable_type (e->type or ZS_F32),
+ *            dtable_stride >= width
+ *   accumulate  0: every row is written (zeros where no token has the id); 1: rows
+ *            of ids that occur are added to, the others are left as they are
+ *            (a table tied to the head adds to zero_head_logp_grad_async's dweight)
+ *   work_dev DEVICE scratch on a 16-byte boundary, work_bytes >=
+ *            zero_embed_work_bytes(tokens, width); holds nothing between calls
+ * Source: derivative of zero_embed_async. */
+ZS_API int32_t zero_embed_grad_async(const zs_embed* e, const void* dout, int64_t dout_stride, void* dtable,
+                                     int64_t dtable_stride, int32_t dtable_type, int32_t accumulate, void* work_dev,
+                                     int64_t work_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* AdamW over a list of tensors: weights that are not one flat fp16 shard     */
 /* (adapters, replicated or unpartitioned parameters, bf16 models).          */
 /* ------------------------------------------------------------------------ */

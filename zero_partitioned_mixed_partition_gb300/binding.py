@@ -97,6 +97,22 @@ class Tensor(ctypes.Structure):
                 ("state", _I32), ("reserved", _I32)]
 
 
+class Head(ctypes.Structure):
+    _fields_ = [("hidden", _P), ("weight", _P), ("rows", _I64), ("vocab", _I64), ("width", _I64),
+                ("hidden_stride", _I64), ("weight_stride", _I64), ("type", _I32), ("reserved", _I32),
+                ("inv_temperature", _F64)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("x", _P), ("gamma", _P), ("beta", _P), ("rows", _I64), ("width", _I64), ("x_stride", _I64),
+                ("type", _I32), ("param_type", _I32), ("eps", _F64)]
+
+
+class Embed(ctypes.Structure):
+    _fields_ = [("table", _P), ("ids", _P), ("tokens", _I64), ("vocab", _I64), ("width", _I64),
+                ("table_stride", _I64), ("type", _I32), ("reserved", _I32), ("scale", _F64)]
+
+
 class Ctrl(ctypes.Structure):
     _fields_ = [("loss_scale", _F64), ("beta1_pow", _F64), ("beta2_pow", _F64), ("step", _I64),
                 ("skipped", _I64), ("cur", _I32), ("overflow", _I32), ("last_overflow", _I32),
@@ -140,6 +156,15 @@ _SIGNATURES = {
     "zero_token_logp_grad_async": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
     "zero_policy_loss_async": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P]),
     "zero_preference_loss_async": (_I32, [_P, _P, _P, _I64, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "zero_head_work_bytes": (_I64, [_I64, _I64, _I64, _I64, _I32]),
+    "zero_head_logp_async": (_I32, [_P, _P, _P, _P, _P, _I64, _P]),
+    "zero_head_logp_grad_async": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "zero_layer_norm_async": (_I32, [_P, _P, _I64, _P, _P]),
+    "zero_layer_norm_work_bytes": (_I64, [_I64, _I64]),
+    "zero_layer_norm_grad_async": (_I32, [_P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _P]),
+    "zero_embed_async": (_I32, [_P, _P, _I64, _P]),
+    "zero_embed_work_bytes": (_I64, [_I64, _I64]),
+    "zero_embed_grad_async": (_I32, [_P, _P, _I64, _P, _I64, _I32, _I32, _P, _I64, _P]),
     "zero_tensors_sqnorm_async": (_I32, [_P, _I32, _P, _P, _P, _P]),
     "zero_tensors_adamw_async": (_I32, [_P, _I32, _P, _F64, _P, _P, _P]),
     "zero_adam8_dequantize": (_I32, [_P, _P, _I64, _I32, _P, _P]),
@@ -828,6 +853,158 @@ def zero_preference_loss_async(logp: torch.Tensor, cu_seqlens: torch.Tensor, hp:
                                           _vector(totals, f32, ZS_PREFERENCE_TOTALS, "totals"), _work_ptr(work),
                                           _stream_of(stream, logp))
     _check(rc, "zero_preference_loss_async")
+
+
+# ------------------------------------------------- head, norm and embedding ---
+
+def _work_bytes(nbytes: int, what: str, device) -> torch.Tensor:
+    """Scratch of a call (uninitialised; calls that may run at once need one each)."""
+    if nbytes < 0:
+        raise ZeroShardError(nbytes, what, "")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _scratch(work: Optional[torch.Tensor]):
+    """Pointer and size of a call's scratch."""
+    return (None, 0) if work is None else (_dev_ptr(work, torch.uint8, "work"), work.numel())
+
+
+def _same_matrix(t: torch.Tensor, like: torch.Tensor, what: str):
+    """Pointer and row stride of a matrix of the type and shape of another."""
+    ptr = _matrix(t, what)
+    if t.dtype != like.dtype or t.shape != like.shape:
+        raise TypeError(f"{what}: expected {tuple(like.shape)} of {like.dtype}, got {tuple(t.shape)} of {t.dtype}")
+    return ptr, _row_stride(t)
+
+
+def new_head_work(rows: int, width: int, vocab: int, gradient: bool = True, piece: int = 0, device="cuda") -> torch.Tensor:
+    """Scratch of the head's calls; gradient: of zero_head_logp_grad_async, which
+    then takes ``piece`` entries of the vocabulary at a time (0: the library's choice)."""
+    return _work_bytes(int(lib().zero_head_work_bytes(int(rows), int(width), int(vocab), int(piece), 1 if gradient else 0)),
+                       "zero_head_work_bytes", device)
+
+
+def _head(hidden: torch.Tensor, weight: torch.Tensor, inv_temperature: float) -> Head:
+    h, w = _matrix(hidden, "hidden"), _matrix(weight, "weight")
+    if hidden.dtype != weight.dtype or hidden.dtype == torch.float32:
+        raise TypeError(f"hidden, weight: expected both float16 or both bfloat16, got {hidden.dtype}, {weight.dtype}")
+    if hidden.shape[1] != weight.shape[1]:
+        raise ValueError(f"hidden is {hidden.shape[1]} wide, weight {weight.shape[1]}")
+    return Head(h, w, hidden.shape[0], weight.shape[0], hidden.shape[1], _row_stride(hidden), _row_stride(weight),
+                _TYPES[hidden.dtype], 0, float(inv_temperature))
+
+
+def zero_head_logp_async(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, logp: torch.Tensor,
+                         work: torch.Tensor, saved: Optional[torch.Tensor] = None, inv_temperature: float = 1.0,
+                         stream=None):
+    """Log-probability of each row's label under softmax(hidden weight^T *
+    inv_temperature), without the logits; ``saved`` ([rows, 2] fp32) is what the
+    gradient needs.  ``work``: new_head_work(..., gradient=False) or larger."""
+    h = _head(hidden, weight, inv_temperature)
+    n = h.rows
+    rc = lib().zero_head_logp_async(ctypes.byref(h), _vector(labels, torch.int64, n, "labels"),
+                                    _vector(logp, torch.float32, n, "logp"),
+                                    _vector(saved, torch.float32, 2 * n, "saved"), *_scratch(work),
+                                    _stream_of(stream, hidden))
+    _check(rc, "zero_head_logp_async")
+
+
+def zero_head_logp_grad_async(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, saved: torch.Tensor,
+                              dlogp: torch.Tensor, dhidden: Optional[torch.Tensor], dweight: Optional[torch.Tensor],
+                              work: torch.Tensor, inv_temperature: float = 1.0,
+                              ctrl_dev: Optional[torch.Tensor] = None, stream=None):
+    """Loss-scaled gradients of the hidden states and the vocabulary matrix
+    (either may be None)."""
+    h = _head(hidden, weight, inv_temperature)
+    n = h.rows
+    dh, dh_stride = (None, 0) if dhidden is None else _same_matrix(dhidden, hidden, "dhidden")
+    dw, dw_stride = (None, 0) if dweight is None else _same_matrix(dweight, weight, "dweight")
+    rc = lib().zero_head_logp_grad_async(ctypes.byref(h), _vector(labels, torch.int64, n, "labels"),
+                                         _vector(saved, torch.float32, 2 * n, "saved"),
+                                         _vector(dlogp, torch.float32, n, "dlogp"),
+                                         _dev_ptr(ctrl_dev, torch.int64, "ctrl_dev"), dh, dh_stride, dw, dw_stride,
+                                         *_scratch(work), _stream_of(stream, hidden))
+    _check(rc, "zero_head_logp_grad_async")
+
+
+def _norm(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], like, eps: float) -> Norm:
+    """The C description; gamma, beta and what ``like`` holds share one type."""
+    ptr, width, kind = _matrix(x, "x"), x.shape[1], None
+    for t, what in ((gamma, "gamma"), (beta, "beta"), *like):
+        if t is None:
+            continue
+        if t.dtype not in _TYPES or kind not in (None, t.dtype):
+            raise TypeError(f"{what}: expected float32, float16 or bfloat16, the same for all of the norm's vectors")
+        if t.numel() != width:
+            raise ValueError(f"{what}: {t.numel()} elements, rows have {width}")
+        kind = t.dtype
+    part = lambda t, what: None if t is None else _dev_ptr(t, t.dtype, what)
+    return Norm(ptr, part(gamma, "gamma"), part(beta, "beta"), x.shape[0], width, _row_stride(x), _TYPES[x.dtype],
+                ZS_F32 if kind is None else _TYPES[kind], float(eps))
+
+
+def zero_layer_norm_async(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], y: torch.Tensor,
+                          saved: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None):
+    """Layer norm of the rows of ``x`` into ``y`` (which may be ``x``); ``saved``
+    ([rows, 2] fp32: mean, 1 / deviation) is what the gradient needs."""
+    n = _norm(x, gamma, beta, (), eps)
+    out, stride = _same_matrix(y, x, "y")
+    rc = lib().zero_layer_norm_async(ctypes.byref(n), out, stride, _vector(saved, torch.float32, 2 * n.rows, "saved"),
+                                     _stream_of(stream, x))
+    _check(rc, "zero_layer_norm_async")
+
+
+def new_layer_norm_work(rows: int, width: int, device="cuda") -> torch.Tensor:
+    """Scratch of zero_layer_norm_grad_async."""
+    return _work_bytes(int(lib().zero_layer_norm_work_bytes(int(rows), int(width))), "zero_layer_norm_work_bytes", device)
+
+
+def zero_layer_norm_grad_async(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor], saved: torch.Tensor,
+                               dx: Optional[torch.Tensor], dgamma: Optional[torch.Tensor], dbeta: Optional[torch.Tensor],
+                               work: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of the norm's input (``dx`` may be ``dy`` or ``x``), weight and
+    bias; any of the three may be None."""
+    n = _norm(x, gamma, None, ((dgamma, "dgamma"), (dbeta, "dbeta")), 0.0)
+    dy_ptr, dy_stride = _same_matrix(dy, x, "dy")
+    dx_ptr, dx_stride = (None, 0) if dx is None else _same_matrix(dx, x, "dx")
+    part = lambda t, what: None if t is None else _dev_ptr(t, t.dtype, what)
+    rc = lib().zero_layer_norm_grad_async(ctypes.byref(n), dy_ptr, dy_stride,
+                                          _vector(saved, torch.float32, 2 * n.rows, "saved"), dx_ptr, dx_stride,
+                                          part(dgamma, "dgamma"), part(dbeta, "dbeta"), *_scratch(work),
+                                          _stream_of(stream, x))
+    _check(rc, "zero_layer_norm_grad_async")
+
+
+def zero_embed_async(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0, stream=None):
+    """Rows of ``table`` at ``ids`` (any shape; out of range: zeros) times ``scale``."""
+    ptr, out_ptr = _matrix(table, "table"), _matrix(out, "out")
+    if out.dtype != table.dtype or tuple(out.shape) != (ids.numel(), table.shape[1]):
+        raise TypeError("out: expected one row of the table's type and width for each id")
+    e = Embed(ptr, _dev_ptr(ids, torch.int64, "ids"), ids.numel(), table.shape[0], table.shape[1], _row_stride(table),
+              _TYPES[table.dtype], 0, float(scale))
+    _check(lib().zero_embed_async(ctypes.byref(e), out_ptr, _row_stride(out), _stream_of(stream, table)), "zero_embed_async")
+
+
+def new_embed_work(tokens: int, width: int, device="cuda") -> torch.Tensor:
+    """Scratch of zero_embed_grad_async."""
+    return _work_bytes(int(lib().zero_embed_work_bytes(int(tokens), int(width))), "zero_embed_work_bytes", device)
+
+
+def zero_embed_grad_async(ids: torch.Tensor, dout: torch.Tensor, dtable: torch.Tensor, work: torch.Tensor,
+                          scale: float = 1.0, accumulate: bool = False, stream=None):
+    """Gradient of the table from that of the looked-up rows; ``accumulate`` adds to
+    the rows of ``dtable`` whose ids occur and leaves the others as they are."""
+    ptr, grad = _matrix(dout, "dout"), _matrix(dtable, "dtable")
+    if dout.shape[0] != ids.numel() or dout.shape[1] != dtable.shape[1]:
+        raise TypeError("dout: expected one row of the table's width for each id")
+    if dtable.dtype not in (dout.dtype, torch.float32):
+        raise TypeError(f"dtable: expected {dout.dtype} or float32, got {dtable.dtype}")
+    e = Embed(None, _dev_ptr(ids, torch.int64, "ids"), ids.numel(), dtable.shape[0], dtable.shape[1], 0,
+              _TYPES[dout.dtype], 0, float(scale))
+    rc = lib().zero_embed_grad_async(ctypes.byref(e), ptr, _row_stride(dout), grad, _row_stride(dtable),
+                                     _TYPES[dtable.dtype], 1 if accumulate else 0, *_scratch(work),
+                                     _stream_of(stream, dout))
+    _check(rc, "zero_embed_grad_async")
 
 
 # --------------------------------------------------------- lists of tensors ---

@@ -23,7 +23,7 @@ CHECKED_BUILD_DIR = os.path.join(PKG, "_build_checked")
 CHECKED_LIB_PATH = os.path.join(PKG, "libzeroshard_checked.so")
 
 SOURCES = ["shard_step.cu", "clip.cu", "sgd.cu", "adam8.cu", "layout.cu", "logits.cu", "preference.cu", "tensors.cu",
-           "cpu_step.cpp", "diag.cpp"]
+           "head.cu", "norm.cu", "embed.cu", "cpu_step.cpp", "diag.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -ffp-contract=off keeps host arithmetic (step coefficients, the CPU step) free
 # of fused multiply-adds, matching the device code's explicit _rn operations;

@@ -66,6 +66,9 @@ uint64_t take_fault_logits();
 int32_t set_wait_limit(int32_t tries);
 uint64_t take_fault_preference();
 uint64_t take_fault_tensors();
+uint64_t take_fault_head();
+uint64_t take_fault_norm();
+uint64_t take_fault_embed();
 // Enqueues the device-side commit / skip of a step over `shards`.
 int32_t launch_commit(const zs_shard* shards, int32_t n_shards, const zs_adam& hp, zs_ctrl* ctrl,
                       cudaStream_t stream);
