@@ -83,7 +83,8 @@ ZS_API int32_t zero_debug_checks(uint64_t* first_fault) {
 
 ZS_API int32_t zero_debug_wait_limit(int32_t tries) {
     if (tries < 0 || tries > 1 << 20) return ZS_ERR_ARG;
-    return zs::set_wait_limit(tries);
+    const int32_t rc = zs::set_wait_limit(tries);
+    return rc < 0 ? rc : zs::set_wait_limit_head(tries);
 }
 
 // Model-state bytes per device ("DeepSpeed ZeRO Stages", sec. 1.2 and 3):

@@ -6,11 +6,10 @@
 //   dH = d W,   dW = d^T H,         c_i = L it dlogp_i.
 // Rows that are left out (ignored labels, dlogp = 0) are taken out first: the
 // live rows' hidden states are copied together, so that prompts cost nothing.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
-
-#include <initializer_list>
 
 #include "cluster_counts.h"
 #include "zs_internal.h"
@@ -20,6 +19,8 @@ namespace {
 #include "step_common.cuh"
 #include "step_end.cuh"
 #include "loss_common.cuh"
+#include "mbar.cuh"
+#include "tensor_core.cuh"
 #include "elem.cuh"
 #include "launch.cuh"
 
@@ -28,6 +29,7 @@ constexpr float kLowestFloat = -3.402823466e38f;
 
 constexpr int64_t kTile = 256;  // rows, and entries of the vocabulary, that a block's sums cover
 constexpr int64_t kMaxRows = 1 << 24, kMaxVocab = 1 << 24, kMaxWidth = 1 << 16;
+constexpr int kMaxSplit = 16;               // parts of dH's sums
 constexpr int64_t kPieceBytes = 1ll << 30;  // of a piece's gradient, where the caller leaves the choice
 
 constexpr int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -49,7 +51,7 @@ struct __align__(16) Row {
 
 // The parts of the scratch buffer, as offsets from its start.
 struct Plan {
-    int64_t rows_pad, tiles, piece;
+    int64_t rows_pad, tiles, piece, sums_room;
     int64_t index, row, hidden, part, label_logit, d, total;
 };
 Plan plan_of(int64_t rows, int64_t width, int64_t vocab, int64_t piece, bool gradient) {
@@ -69,7 +71,11 @@ Plan plan_of(int64_t rows, int64_t width, int64_t vocab, int64_t piece, bool gra
         if (piece <= 0) piece = kPieceBytes / (2 * p.rows_pad);
         p.piece = piece < kTile ? kTile : round_up(piece, kTile);
         if (p.piece > p.tiles * kTile) p.piece = p.tiles * kTile;
-        p.part = take(4 * p.rows_pad * width);
+        // fp32 sums of dH, several of them where there are few tiles
+        const int64_t tiles = p.rows_pad / kTile * (round_up(width, kTile) / kTile);
+        const int64_t parts = round_up(160, tiles) / tiles;
+        p.sums_room = p.rows_pad * (parts < kMaxSplit ? parts : kMaxSplit);
+        p.part = take(4 * p.sums_room * width);
         p.d = take(2 * p.rows_pad * p.piece);
     } else {
         p.part = take(8 * p.rows_pad * p.tiles);
@@ -114,7 +120,7 @@ struct HeadArgs {
     void* part;
     float* label_logit;
     uint16_t* d;                 // [rows_pad][piece]
-    int64_t rows_pad, tiles, piece;
+    int64_t rows_pad, tiles, piece, sums_room;
 };
 
 __device__ __forceinline__ bool is_live(const HeadArgs& a, int64_t i) {
@@ -210,101 +216,384 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
+__device__ __forceinline__ float infinity() { return __int_as_float(0x7f800000); }
 
-// d of a live row's logit, scaled.
-__device__ __forceinline__ float d_of(const Row& row, float x, int32_t j, float k) {
-    const float p = exp2_approx((x - row.top) * k - row.log_sum * kLog2e);
-    return j == row.label ? row.coef * (1.0f - p) : -row.coef * p;
-}
-
-constexpr int kBlockRows = 16;
-
+// The three products, each a 256 x 256 tile (of sums) at a time:
+//   kLogits    H W^T: statistics of each row over the tile's entries
+//   kGrad      the same over one piece of the vocabulary: d
+//   kDHidden   d W over one piece
+//   kDWeight   d^T H: the piece's rows of dW
 enum { kLogits, kGrad, kDHidden, kDWeight };
 
-// A block makes kBlockRows x 256 sums, a thread those of one column.
-//   kLogits    rows of H and of W: statistics of each row over the block's columns
-//   kGrad      the same logits of one piece: d
-//   kDHidden   d of one piece times W: added to fp32 sums, or the output
-//   kDWeight   d^T H: rows of dW
-template <typename T, int MODE>
-__global__ void __launch_bounds__(256) head_product_kernel(const __grid_constant__ HeadArgs a, int64_t first, int64_t count,
-                                                           int last) {
-    __shared__ float s_a[kBlockRows][33];
-    __shared__ float s_x[kBlockRows][256];
-    griddep_wait();
-    const int32_t live = a.counts->live;
-    const int64_t m0 = (int64_t)blockIdx.x * kBlockRows, n0 = (int64_t)blockIdx.y * 256;
-    const int64_t n = n0 + threadIdx.x;
-    const T* hidden = (const T*)a.compact;
-    const T* weight = (const T*)a.weight + first * a.weight_stride;
-    const T* d = (const T*)a.d;
-    int64_t inner;
+constexpr int kStages = 6, kStep = 64;                      // stages of the ring, k in one of them
+constexpr int kHalfBytes = 128 * kStep * 2;                 // a CTA's half of an operand's stage
+constexpr int kBoxBytes = 64 * kStep * 2;                   // 64 m of 64 k, across k
+constexpr int kRing = kStages * 2 * kHalfBytes;
+constexpr int kProductThreads = 256, kProductShared = kRing + 1024;
+struct ProductArgs {
+    HeadArgs h;
+    int64_t first, count;  // the piece
+    int32_t last;          // its end is the vocabulary's
+};
+
+// The tiles of a product over the live rows, and how the long sum of kDHidden is
+// split among several sums joined afterwards.
+struct Tiles {
+    int32_t m_tiles, n_tiles, split, steps;  // steps of kStep in the whole sum
+};
+// The number of parts of dH's sums: with few tiles the CTA pairs would be idle.
+// Estimated in steps: rounds of tiles, each with a start and an end of some 12 steps,
+// and what the parts cost to write and read.
+__device__ int32_t split_of(int32_t tiles, int32_t steps, int32_t pairs, int32_t room) {
+    int32_t best = 1;
+    float least = 3.4e38f;
+    for (int32_t s = 1; s <= kMaxSplit && s <= room && s * 8 <= steps; ++s) {
+        const float rounds = (float)((tiles * s + pairs - 1) / pairs);
+        const float cost = rounds * ((float)((steps + s - 1) / s) + 12.0f) + (s > 1 ? 0.3f * (float)(tiles * s) : 0.0f);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+__device__ __forceinline__ int32_t tiles_of(int64_t n) { return (int32_t)((n + kTile - 1) / kTile); }
+__device__ __forceinline__ int32_t steps_of(int64_t n) { return (int32_t)((n + kStep - 1) / kStep); }
+
+template <int MODE>
+__device__ __forceinline__ Tiles work_of(const ProductArgs& p, int32_t live, int32_t pairs) {
+    Tiles w;
+    w.split = 1;
     if (MODE == kLogits || MODE == kGrad) {
-        if (m0 >= round_up(live, kTile)) return;
-        inner = a.width;
+        w.m_tiles = tiles_of(live);
+        w.n_tiles = tiles_of(p.count);
+        w.steps = steps_of(p.h.width);
     } else if (MODE == kDHidden) {
-        if (m0 >= live) return;
-        inner = count;
+        w.m_tiles = tiles_of(live);
+        w.n_tiles = tiles_of(p.h.width);
+        w.steps = steps_of(p.count);
+        // (the same for every piece: the first one's number of steps)
+        const int64_t whole = p.h.vocab < p.h.piece ? p.h.vocab : p.h.piece;
+        if (live > 0) w.split = split_of(w.m_tiles * w.n_tiles, steps_of(whole), pairs, (int32_t)(p.h.sums_room / (w.m_tiles * kTile)));
     } else {
-        inner = live;
+        w.m_tiles = tiles_of(p.count);
+        w.n_tiles = tiles_of(p.h.width);
+        w.steps = steps_of(live);
     }
-    float sum[kBlockRows] = {};
-    for (int64_t k0 = 0; k0 < inner; k0 += 32) {
-        for (int q = threadIdx.x; q < kBlockRows * 32; q += 256) {
-            const int m = MODE == kDWeight ? q % kBlockRows : q / 32, k = MODE == kDWeight ? q / kBlockRows : q % 32;
-            float x = 0.0f;
-            if (k0 + k < inner) {
-                if (MODE == kLogits || MODE == kGrad) x = to_float(hidden[(m0 + m) * a.width + k0 + k]);
-                if (MODE == kDHidden) x = to_float(d[(m0 + m) * a.piece + k0 + k]);
-                if (MODE == kDWeight) x = to_float(d[(k0 + k) * a.piece + m0 + m]);
+    return w;
+}
+
+// One tile of the pair, in the order in which they are taken.  Logits: groups of 16
+// tiles of rows go through the vocabulary together, so that a tile of W is read from
+// memory once for each group and the group's rows stay in L2.  The others: tiles of
+// the width run fastest (they share d), then rows.
+struct Tile {
+    int32_t m, n, part, from, to;  // from, to: steps
+};
+template <int MODE>
+__device__ __forceinline__ Tile tile_of(const Tiles& w, int32_t u) {
+    Tile t;
+    t.part = 0;
+    t.from = 0;
+    t.to = w.steps;
+    if (MODE == kLogits || MODE == kGrad) {
+        const int32_t group = 16 * w.n_tiles, g = u / group, first = g * 16, rest = u - g * group;
+        const int32_t high = w.m_tiles - first < 16 ? w.m_tiles - first : 16;
+        t.m = first + rest % high;
+        t.n = rest / high;
+    } else {
+        t.n = u % w.n_tiles;
+        const int32_t q = u / w.n_tiles;
+        t.m = q % w.m_tiles;
+        if (MODE == kDHidden) {
+            t.part = q / w.m_tiles;
+            t.from = (int32_t)((int64_t)w.steps * t.part / w.split);
+            t.to = (int32_t)((int64_t)w.steps * (t.part + 1) / w.split);
+        }
+    }
+    return t;
+}
+// Columns of B in a tile that a CTA holds: 64 where the width's last tile has no more
+// than 128.
+template <int MODE>
+__device__ __forceinline__ int32_t half_of(const ProductArgs& p, int32_t n) {
+    return (MODE == kDHidden || MODE == kDWeight) && p.h.width - (int64_t)n * kTile <= 128 ? 64 : 128;
+}
+
+struct Ring {
+    uint64_t full[kStages], empty[kStages];  // full: the first CTA's counts both CTAs' copies
+    uint64_t sums_full[2], sums_empty[2];    // sums_empty: the first CTA's counts both CTAs' warps
+    uint64_t done;
+    uint32_t sums;                           // address of the tensor memory
+    int32_t failed;                          // a wait ran out
+    int32_t issued;                          // steps whose copies were issued,
+    uint32_t bytes[kStages];                 // and what each CTA copied in the last ones
+};
+
+// A pair of CTAs (a cluster of two) takes tile after tile.  In each CTA one thread
+// copies its halves of A and B ahead into a ring of kStages stages; one thread of the
+// first CTA multiplies, 16 k at a time, into one of two sets of sums in tensor memory;
+// four warps turn the other set into the tile's outputs (a thread has a row of it).
+template <typename T, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+    head_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const __grid_constant__ ProductArgs p) {
+    constexpr bool kAlongA = MODE != kDWeight, kAlongB = MODE == kLogits || MODE == kGrad;  // operands along k
+    extern __shared__ uint8_t s_raw[];
+    __shared__ Ring ring;
+    uint8_t* const stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    const int32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const HeadArgs& a = p.h;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ring.full[s], 1);
+            mbar_init(&ring.empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ring.sums_full[s], 1);
+            mbar_init(&ring.sums_empty[s], 2 * 4);
+        }
+        mbar_init(&ring.done, 1);
+        ring.failed = 0;
+        ring.issued = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+    }
+    if (warp == 2) tensor_alloc(&ring.sums);
+    tensor_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    tensor_fence_after();
+    griddep_wait();
+    const uint32_t sums = ring.sums;
+    const int32_t live = a.counts->live;
+    const Tiles w = work_of<MODE>(p, live, pairs);
+    const int32_t units = w.m_tiles * w.n_tiles * w.split;
+
+    if (warp == 0 && lane == 0) {
+        // what earlier kernels wrote, seen by the copies
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        int32_t at = 0;
+        bool ok = true;
+        for (int32_t u = pair; u < units && ok; u += pairs) {
+            const Tile t = tile_of<MODE>(w, u);
+            const int32_t half = half_of<MODE>(p, t.n);
+            const uint32_t bytes = (uint32_t)(kHalfBytes + half * kStep * 2);
+            const int32_t m0 = t.m * (int32_t)kTile + (int32_t)rank * 128, n0 = t.n * (int32_t)kTile + (int32_t)rank * half;
+            for (int32_t k = t.from; k < t.to; ++k, ++at) {
+                const int s = at % kStages;
+                if (!mbar_wait(&ring.empty[s], (uint32_t)(at / kStages + 1) & 1u, &ring.failed)) {
+                    ok = false;
+                    break;
+                }
+                ring.bytes[s] = bytes;
+                ring.issued = at + 1;
+                if (rank == 0) mbar_expect(&ring.full[s], 2 * bytes);
+                const uint32_t full = peer_addr(&ring.full[s], 0);
+                uint8_t* const to_a = stage0 + s * 2 * kHalfBytes;
+                uint8_t* const to_b = to_a + kHalfBytes;
+                const int32_t x = k * kStep;
+                if (kAlongA) {
+                    copy_box(to_a, &map_a, x, m0, full);
+                } else {
+                    copy_box(to_a, &map_a, m0, x, full);
+                    copy_box(to_a + kBoxBytes, &map_a, m0 + 64, x, full);
+                }
+                if (kAlongB) {
+                    copy_box(to_b, &map_b, x, (int32_t)p.first + n0, full);
+                } else {
+                    const int32_t y = MODE == kDHidden ? (int32_t)p.first + x : x;
+                    copy_box(to_b, &map_b, n0, y, full);
+                    if (half == 128) copy_box(to_b + kBoxBytes, &map_b, n0 + 64, y, full);
+                }
             }
-            s_a[m][k] = x;
         }
-        __syncthreads();
-        const int lim = inner - k0 < 32 ? (int)(inner - k0) : 32;
-        for (int k = 0; k < lim; ++k) {
-            float y = 0.0f;
-            if (MODE == kLogits || MODE == kGrad) y = n < count ? to_float(weight[n * a.weight_stride + k0 + k]) : 0.0f;
-            if (MODE == kDHidden) y = n < a.width ? to_float(weight[(k0 + k) * a.weight_stride + n]) : 0.0f;
-            if (MODE == kDWeight) y = n < a.width ? to_float(hidden[(k0 + k) * a.width + n]) : 0.0f;
+        // (the last products' arrivals at this CTA's barriers, before it leaves)
+        for (int32_t i = at > kStages ? at - kStages : 0; i < at && ok; ++i)
+            ok = mbar_wait(&ring.empty[i % kStages], (uint32_t)(i / kStages) & 1u, &ring.failed);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        int32_t at = 0, turn = 0;
+        bool ok = true;
+        for (int32_t u = pair; u < units && ok; u += pairs) {
+            const Tile t = tile_of<MODE>(w, u);
+            if (t.from == t.to) continue;  // (nothing to add up: no turn of the sums)
+            const uint32_t kind = product_kind<T, kAlongA, kAlongB>(2u * (uint32_t)half_of<MODE>(p, t.n));
+            const int set = turn & 1;
+            ok = mbar_wait(&ring.sums_empty[set], (uint32_t)(turn / 2 + 1) & 1u, &ring.failed);
+            if (!ok) break;
+            tensor_fence_after();
+            for (int32_t k = t.from; k < t.to; ++k, ++at) {
+                const int s = at % kStages;
+                ok = mbar_wait(&ring.full[s], (uint32_t)(at / kStages) & 1u, &ring.failed);
+                if (!ok) break;
+                tensor_fence_after();
+                const uint8_t* const from = stage0 + s * 2 * kHalfBytes;
+                uint64_t da = operand<kAlongA>(from, kBoxBytes), db = operand<kAlongB>(from + kHalfBytes, kBoxBytes);
 #pragma unroll
-            for (int m = 0; m < kBlockRows; ++m) sum[m] = fmaf(s_a[m][k], y, sum[m]);
+                for (int q = 0; q < kStep / 16; ++q) {
+                    multiply(sums + (uint32_t)set * 256u, da, db, kind, k > t.from || q > 0);
+                    da += operand_step<kAlongA>();
+                    db += operand_step<kAlongB>();
+                }
+                arrive_after_products(&ring.empty[s]);
+            }
+            if (ok) arrive_after_products(&ring.sums_full[set]);
+            ++turn;
         }
-        __syncthreads();
-    }
-    const float k = a.it * kLog2e;
-    if (MODE == kLogits) {
-#pragma unroll
-        for (int m = 0; m < kBlockRows; ++m) s_x[m][threadIdx.x] = n < count ? sum[m] : -__int_as_float(0x7f800000);
-        __syncthreads();
-        if (threadIdx.x < kBlockRows) {
-            const int m = threadIdx.x;
+    } else if (warp >= 4) {
+        const int quarter = warp - 4;
+        bool ok = true;
+        int32_t turn = 0;
+        const float k2 = a.it * kLog2e;
+        for (int32_t u = pair; u < units; u += pairs) {
+            const Tile t = tile_of<MODE>(w, u);
+            const int set = turn & 1;
+            const bool any = t.from < t.to;
+            if (any) {
+                ok = ok && all_lanes(mbar_wait<true>(&ring.sums_full[set], (uint32_t)(turn / 2) & 1u, &ring.failed));
+                tensor_fence_after();
+            }
+            const uint32_t from = sums + (uint32_t)set * 256u + ((uint32_t)quarter * 32u << 16);
+            const int64_t r = (int64_t)t.m * kTile + rank * 128 + quarter * 32 + lane;  // the thread's row of the tile
+            const int64_t n0 = (int64_t)t.n * kTile;
+            const int32_t chunks = half_of<MODE>(p, t.n) * 2 / 32;
             float top = kLowestFloat, s = 0.0f;
-            for (int j = 0; j < 256; ++j) top = fmaxf(top, s_x[m][j]);
-            for (int j = 0; j < 256; ++j) s += exp2_approx((s_x[m][j] - top) * k);
-            const int32_t y = a.row[m0 + m].label;
-            if (y >= n0 && y < n0 + 256) a.label_logit[m0 + m] = s_x[m][y - n0];
-            ((float2*)a.part)[blockIdx.y * a.rows_pad + m0 + m] = make_float2(top, s);
-        }
-    }
-    for (int m = 0; m < kBlockRows; ++m) {
-        if (MODE == kGrad) {
-            const Row row = a.row[m0 + m];
-            const float v = n < count && row.coef != 0.0f ? d_of(row, sum[m], (int32_t)(first + n), k) : 0.0f;
-            ((T*)a.d)[(m0 + m) * a.piece + n] = from_float<T>(v);
-        }
-        if (MODE == kDHidden && n < a.width && m0 + m < live) {
-            float* acc = (float*)a.part + (m0 + m) * a.width + n;
-            const float v = first > 0 ? *acc + sum[m] : sum[m];
-            if (last) {
-                ((T*)a.dhidden)[a.index[m0 + m] * a.dhidden_stride + n] = from_float<T>(v * a.counts->unscale);
-            } else {
-                *acc = v;
+            Row row;
+            int32_t label = -1;  // its place in the tile
+            if (MODE == kLogits || MODE == kGrad) {
+                row = a.row[r];
+                label = row.label - (int32_t)(p.first + n0);
+            }
+            const float unscale = MODE == kDHidden || MODE == kDWeight ? a.counts->unscale : 0.0f;
+            const int32_t to_row = MODE == kDHidden && r < live ? a.index[r] : 0;
+#pragma unroll 1
+            for (int32_t c = 0; c < chunks; ++c) {
+                float v[32];
+                if (any && ok) {
+                    tensor_load(from + (uint32_t)c * 32u, v);
+                    tensor_load_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = ok ? 0.0f : quiet_nan();
+                }
+                const int64_t j0 = n0 + c * 32;  // the chunk's first column
+                if (MODE == kLogits) {
+                    if (label >> 5 == c) {
+                        float x = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x = (label & 31) == i ? v[i] : x;
+                        a.label_logit[r] = x;
+                    }
+                    if (j0 + 32 > p.count) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = j0 + i < p.count ? v[i] : -infinity();
+                    }
+                    float high = top;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) high = fmaxf(high, v[i]);
+                    float add[4] = {};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) add[i % 4] += exp2_approx((v[i] - high) * k2);
+                    s = s * exp2_approx((top - high) * k2) + ((add[0] + add[1]) + (add[2] + add[3]));
+                    top = high;
+                } else if (MODE == kGrad) {
+                    const float shift = row.log_sum * kLog2e, factor = -row.coef;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = factor * exp2_approx(fmaf(v[i] - row.top, k2, -shift));
+                    if (label >> 5 == c) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if ((label & 31) == i) v[i] += row.coef;
+                    }
+                    if (j0 + 32 > p.count) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = j0 + i < p.count ? v[i] : 0.0f;
+                    }
+                    uint4* out = reinterpret_cast<uint4*>(a.d + r * a.piece + j0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint4 x = make_uint4(narrow2<T>(v[8 * q], v[8 * q + 1]), narrow2<T>(v[8 * q + 2], v[8 * q + 3]),
+                                             narrow2<T>(v[8 * q + 4], v[8 * q + 5]), narrow2<T>(v[8 * q + 6], v[8 * q + 7]));
+                        // (rows that only fill the tile, whatever W holds)
+                        if (row.coef == 0.0f) x = make_uint4(0, 0, 0, 0);
+                        out[q] = x;
+                    }
+                } else {
+                    const bool sum_only = MODE == kDHidden && !(w.split == 1 && p.first == 0 && p.last);
+                    if (MODE == kDHidden ? r < live : r < p.count) {
+                        if (sum_only) {
+                            float* out = (float*)a.part + ((int64_t)t.part * w.m_tiles * kTile + r) * a.width + j0;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if (j0 + 8 * q >= a.width) break;
+                                float4* o = reinterpret_cast<float4*>(out + 8 * q);
+                                float4 x = make_float4(v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]);
+                                float4 y = make_float4(v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]);
+                                if (p.first > 0) {
+                                    const float4 f = o[0], g = o[1];
+                                    x = make_float4(x.x + f.x, x.y + f.y, x.z + f.z, x.w + f.w);
+                                    y = make_float4(y.x + g.x, y.y + g.y, y.z + g.z, y.w + g.w);
+                                }
+                                o[0] = x;
+                                o[1] = y;
+                            }
+                        } else {
+                            uint16_t* out = MODE == kDHidden ? a.dhidden + to_row * a.dhidden_stride + j0
+                                                             : a.dweight + (p.first + r) * a.dweight_stride + j0;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if (j0 + 8 * q >= a.width) break;
+                                uint32_t x[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    x[i] = narrow2<T>(v[8 * q + 2 * i] * unscale, v[8 * q + 2 * i + 1] * unscale);
+                                reinterpret_cast<uint4*>(out)[q] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                    }
+                }
+            }
+            if (MODE == kLogits) ((float2*)a.part)[(int64_t)t.n * a.rows_pad + r] = make_float2(top, s);
+            if (any) {
+                tensor_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(peer_addr(&ring.sums_empty[set], 0));
+                ++turn;
             }
         }
-        if (MODE == kDWeight && n < a.width && m0 + m < count)
-            ((T*)a.dweight)[(first + m0 + m) * a.dweight_stride + n] = from_float<T>(sum[m] * a.counts->unscale);
     }
+    __syncwarp();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    // Where a wait ran out, products and copies may be under way: neither CTA leaves
+    // before the products are done and the barriers of the last steps that either
+    // issued have counted their copies (of a step that one of the two did not reach,
+    // that one's are made up for).
+    if ((load_from_peer(&ring.failed, 0) | load_from_peer(&ring.failed, 1)) != 0 && rank == 0 && threadIdx.x == 32) {
+            signal_after_products(&ring.done);
+            drain(&ring.done, 0);
+            const int32_t mine = ring.issued, other = load_from_peer(&ring.issued, 1);
+            const int32_t most = mine > other ? mine : other;
+            for (int32_t i = most > kStages ? most - kStages : 0; i < most; ++i) {
+                const int s = i % kStages;
+                if (i >= mine) mbar_expect(&ring.full[s], (uint32_t)load_from_peer((const int32_t*)&ring.bytes[s], 1));
+                if (i >= other) mbar_give(&ring.full[s], ring.bytes[s]);
+                drain(&ring.full[s], (uint32_t)(i / kStages) & 1u);
+            }
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    tensor_fence_after();
+    if (warp == 2) tensor_free(sums);
 }
 
 // Joins the statistics of a row's tiles: a warp to a row.
@@ -334,7 +623,86 @@ __global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ 
     }
 }
 
+// Joins the parts of dH's sums: a block to a row.
+template <typename T>
+__global__ void __launch_bounds__(256) head_dhidden_kernel(const __grid_constant__ ProductArgs p, int32_t pairs) {
+    griddep_wait();
+    const HeadArgs& a = p.h;
+    const int32_t live = a.counts->live;
+    const Tiles w = work_of<kDHidden>(p, live, pairs);
+    if (w.split == 1 && p.first == 0) return;  // (one piece: the product wrote dH)
+    const float unscale = a.counts->unscale;
+    const int64_t part = (int64_t)w.m_tiles * kTile * a.width;
+    for (int64_t r = blockIdx.x; r < live; r += gridDim.x) {
+        const float* from = (const float*)a.part + r * a.width;
+        uint16_t* to = a.dhidden + (int64_t)a.index[r] * a.dhidden_stride;
+        for (int64_t k = 4 * threadIdx.x; k < a.width; k += 4 * blockDim.x) {
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int32_t q = 0; q < w.split; ++q) {
+                const float4 x = *reinterpret_cast<const float4*>(from + q * part + k);
+                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+            }
+            *reinterpret_cast<uint2*>(to + k) =
+                make_uint2(narrow2<T>(s.x * unscale, s.y * unscale), narrow2<T>(s.z * unscale, s.w * unscale));
+        }
+    }
+}
+
 // ------------------------------------------------------------------- launches ---
+
+// The tensor map of a matrix of 16-bit elements, `wide` of them to a row: boxes of 64
+// elements (a row of the swizzle) by `box_rows` rows.  Outside the matrix are zeros.
+int32_t make_map(CUtensorMap* map, int32_t type, const void* base, int64_t rows, int64_t wide, int64_t stride,
+                 uint32_t box_rows) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return (Encode)f;
+    }();
+    if (encode == nullptr) return zs::fail_with(ZS_ERR_CUDA, "cuTensorMapEncodeTiled: not found in the driver");
+    const cuuint64_t dims[2] = {(cuuint64_t)wide, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, box_rows}, one[2] = {1, 1};
+    const CUresult rc = encode(map, type == ZS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                               const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return rc == CUDA_SUCCESS ? ZS_OK : zs::fail_with(ZS_ERR_CUDA, "cuTensorMapEncodeTiled: refused a matrix of the head");
+}
+
+// Pairs of CTAs that run at once; 0: a CUDA error, reported.
+template <typename T, int MODE>
+int pairs_of() {
+    const void* kernel = (const void*)head_product_kernel<T, MODE>;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductShared);
+    const int pairs = err == cudaSuccess ? active_clusters(kernel, kProductThreads, 2, kProductShared, &err) : 0;
+    if (pairs < 1) zs::cuda_fail(err, "head_product_kernel");
+    return pairs;
+}
+template <typename T, int MODE>
+int32_t launch_product(const ProductArgs& p, const CUtensorMap& map_a, const CUtensorMap& map_b, int pairs,
+                       cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u * (unsigned)pairs);
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = kProductShared;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, head_product_kernel<T, MODE>, map_a, map_b, p);
+    if (err != cudaSuccess) return zs::cuda_fail(err, "head_product_kernel");
+    return zs::check_launch("head_product_kernel");
+}
 
 bool valid_stride(int64_t rows, int64_t width, int64_t stride) {
     return rows <= 1 || (stride >= width && stride <= 1ll << 40);
@@ -374,6 +742,7 @@ HeadArgs args_of(const zs_head* h, const Plan& p, void* work) {
     a.rows_pad = p.rows_pad;
     a.tiles = p.tiles;
     a.piece = p.piece;
+    a.sums_room = p.sums_room;
     return a;
 }
 
@@ -384,37 +753,55 @@ int32_t launch_rows(const HeadArgs& a, cudaStream_t stream) {
                   "head_gather_kernel", a);
 }
 
+template <typename T> constexpr int32_t type_of();
+template <> constexpr int32_t type_of<__half>() { return ZS_F16; }
+template <> constexpr int32_t type_of<__nv_bfloat16>() { return ZS_BF16; }
+
 template <typename T>
 int32_t launch_logp(const HeadArgs& a, cudaStream_t stream) {
+    CUtensorMap rows, entries;
+    ZS_TRY(make_map(&rows, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
+    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 128));
+    const int pairs = pairs_of<T, kLogits>();
+    if (pairs < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
-    ZS_TRY(launch(head_product_kernel<T, kLogits>, dim3((unsigned)(a.rows_pad / kBlockRows), (unsigned)a.tiles), 256, stream,
-                  "head_product_kernel", a, (int64_t)0, a.vocab, 0));
+    ZS_TRY((launch_product<T, kLogits>(ProductArgs{a, 0, a.vocab, 1}, rows, entries, pairs, stream)));
     return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 8) / 8)), 256, stream, "head_join_kernel", a);
 }
 
 template <typename T>
 int32_t launch_grad(const HeadArgs& a, cudaStream_t stream) {
+    // the operands of the three products: H, W and d, along k or across it
+    CUtensorMap rows, entries, d_rows, w_across, d_across, h_across;
+    ZS_TRY(make_map(&rows, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
+    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 128));
+    ZS_TRY(make_map(&d_rows, type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 128));
+    ZS_TRY(make_map(&w_across, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 64));
+    ZS_TRY(make_map(&d_across, type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 64));
+    ZS_TRY(make_map(&h_across, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 64));
+    const int pairs = pairs_of<T, kGrad>(), pairs_h = pairs_of<T, kDHidden>(), pairs_w = pairs_of<T, kDWeight>();
+    if (pairs < 1 || pairs_h < 1 || pairs_w < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
-    const unsigned wide = (unsigned)(round_up(a.width, 256) / 256), rows = (unsigned)(a.rows_pad / kBlockRows);
-    for (int64_t first = 0; first < a.vocab; first += a.piece) {
-        const int64_t count = a.vocab - first < a.piece ? a.vocab - first : a.piece;
-        const int last = first + count == a.vocab;
-        ZS_TRY(launch(head_product_kernel<T, kGrad>, dim3(rows, (unsigned)(round_up(count, 256) / 256)), 256, stream,
-                      "head_product_kernel", a, first, count, last));
-        if (a.dhidden != nullptr)
-            ZS_TRY(launch(head_product_kernel<T, kDHidden>, dim3(rows, wide), 256, stream, "head_product_kernel", a, first,
-                          count, last));
-        if (a.dweight != nullptr)
-            ZS_TRY(launch(head_product_kernel<T, kDWeight>, dim3((unsigned)(round_up(count, kBlockRows) / kBlockRows), wide),
-                          256, stream, "head_product_kernel", a, first, count, last));
+    ProductArgs p = {a, 0, 0, 0};
+    for (p.first = 0;; p.first += a.piece) {
+        p.last = p.first + a.piece >= a.vocab;
+        p.count = p.last ? a.vocab - p.first : a.piece;
+        ZS_TRY((launch_product<T, kGrad>(p, rows, entries, pairs, stream)));
+        if (a.dhidden != nullptr) ZS_TRY((launch_product<T, kDHidden>(p, d_rows, w_across, pairs_h, stream)));
+        if (a.dweight != nullptr) ZS_TRY((launch_product<T, kDWeight>(p, d_across, h_across, pairs_w, stream)));
+        if (p.last) break;
     }
-    return ZS_OK;
+    if (a.dhidden == nullptr) return ZS_OK;
+    const int64_t most = 8 * zs::device_sm_count();
+    return launch(head_dhidden_kernel<T>, dim3((unsigned)(a.rows_pad < most ? a.rows_pad : most)), 256, stream,
+                  "head_dhidden_kernel", p, (int32_t)pairs_h);
 }
 
 }  // namespace
 
 namespace zs {
 uint64_t take_fault_head() { return take_fault(); }
+int32_t set_wait_limit_head(int32_t tries) { return set_unit_wait_limit(tries); }
 }  // namespace zs
 
 extern "C" {

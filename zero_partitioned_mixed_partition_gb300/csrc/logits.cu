@@ -47,6 +47,7 @@ namespace {
 #include "step_common.cuh"
 #include "step_end.cuh"
 #include "loss_common.cuh"
+#include "mbar.cuh"
 
 [[maybe_unused]] constexpr uint32_t kSiteLogits = 12, kSiteDlogits = 13;
 
@@ -457,64 +458,6 @@ __device__ __forceinline__ void zero_range(T* out, int64_t n, int threads) {
 
 // ------------------------------------------------------ copies and clusters ---
 
-// Barriers in shared memory that count arrivals and copied bytes.
-__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
-    asm volatile("{\n\t.reg .b64 t;\n\tmbarrier.arrive.shared::cta.b64 t, [%0];\n\t}" ::"r"(smem_addr(b)) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
-    asm volatile("{\n\t.reg .b64 t;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(smem_addr(b)),
-                 "r"(bytes) : "memory");
-}
-// Whether the phase of the given parity is over; waits up to 2 us for it.
-__device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
-    uint32_t done = 0;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(smem_addr(b)), "r"(parity), "r"(2000u) : "memory");
-    return done != 0;
-}
-// The tries of a wait: a second or two.
-constexpr int kWaitLimit = 1 << 20;
-#if ZS_CHECKED
-__device__ int32_t g_wait_limit = kWaitLimit;  // zero_debug_wait_limit
-__device__ __forceinline__ int wait_limit() { return *(volatile int32_t*)&g_wait_limit; }
-#else
-__device__ __forceinline__ int wait_limit() { return kWaitLimit; }
-#endif
-template <bool RELAXED>
-__device__ __forceinline__ bool mbar_wait_on(uint64_t* b, uint32_t parity, int32_t* failed) {
-    const int limit = wait_limit();
-#pragma unroll 1
-    for (int i = 0; i < limit; ++i) {
-        if (mbar_try(b, parity)) return true;
-        if (*(volatile int32_t*)failed) return false;
-        if (RELAXED) __nanosleep(100);
-    }
-    *(volatile int32_t*)failed = 1;
-    return false;
-}
-// Waits for the phase, within the limit.  A wait that runs out sets *failed and
-// returns false; so do the block's other waits from then on, at once.  RELAXED: for
-// the warps that mostly wait; they leave the issue slots to the others.  (Most waits
-// are over at the first try; with that in the loop, 708 us for 684 in the first case
-// above.)
-template <bool RELAXED = false>
-__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, int32_t* failed) {
-#if ZS_CHECKED
-    if (wait_limit() == 0) return mbar_wait_on<RELAXED>(b, parity, failed);
-#endif
-    return mbar_try(b, parity) || mbar_wait_on<RELAXED>(b, parity, failed);
-}
-// Whether every lane of the warp may go on.
-__device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(0xffffffffu, ok); }
-// Waits, within the ordinary limit, until the barrier counts no copy in flight.
-__device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < kWaitLimit; ++i)
-        if (mbar_try(b, parity)) return;
-}
 // bytes (a multiple of 16, both addresses on 16-byte boundaries) from global
 // to shared memory, counted by the barrier.
 __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
@@ -1238,15 +1181,7 @@ int32_t launch(const zs_logits* x, RowArgs& a, bool ent, void* stream) {
 
 namespace zs {
 uint64_t take_fault_logits() { return take_fault(); }
-int32_t set_wait_limit(int32_t tries) {
-#if ZS_CHECKED
-    const cudaError_t err = cudaMemcpyToSymbol(g_wait_limit, &tries, sizeof(tries));
-    return err == cudaSuccess ? 1 : cuda_fail(err, "zero_debug_wait_limit");
-#else
-    (void)tries;
-    return 0;
-#endif
-}
+int32_t set_wait_limit(int32_t tries) { return set_unit_wait_limit(tries); }
 }  // namespace zs
 
 extern "C" {

@@ -61,9 +61,10 @@ uint64_t take_fault_clip();
 uint64_t take_fault_sgd();
 uint64_t take_fault_adam8();
 uint64_t take_fault_logits();
-// The debug build: how often the waits of the logits kernels try before they give
-// up (1: set; 0: not this build, ZS_ERR_CUDA).
+// The debug build: how often the waits of the logits kernels, and of the head's
+// products, try before they give up (1: set; 0: not this build, ZS_ERR_CUDA).
 int32_t set_wait_limit(int32_t tries);
+int32_t set_wait_limit_head(int32_t tries);
 uint64_t take_fault_preference();
 uint64_t take_fault_tensors();
 uint64_t take_fault_head();
