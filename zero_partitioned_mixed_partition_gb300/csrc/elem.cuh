@@ -30,8 +30,8 @@ template <> __device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t w) 
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// V values of a type, as one access of V * sizeof(T) bytes (V = 1: an element).
-template <typename T, int V> struct alignas(V * sizeof(T)) Pack {
+// V values of a type, as accesses of up to 16 bytes (V = 1: an element).
+template <typename T, int V> struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Pack {
     T v[V];
 };
 template <typename T, int V>

@@ -4,10 +4,12 @@
 #pragma once
 
 template <typename... P, typename... A>
-int32_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, const char* name, A... args) {
+int32_t launch_shared(void (*kernel)(P...), dim3 grid, int threads, size_t shared, cudaStream_t stream, const char* name,
+                      A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -17,6 +19,11 @@ int32_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
     if (err != cudaSuccess) return zs::cuda_fail(err, name);
     return zs::check_launch(name);
+}
+
+template <typename... P, typename... A>
+int32_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, const char* name, A... args) {
+    return launch_shared(kernel, grid, threads, 0, stream, name, args...);
 }
 
 #define ZS_TRY(call)                          \

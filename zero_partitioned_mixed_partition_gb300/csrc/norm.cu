@@ -12,6 +12,8 @@ namespace {
 #include "elem.cuh"
 #include "launch.cuh"
 
+[[maybe_unused]] constexpr uint32_t kSiteNormRow = 18;
+
 constexpr int64_t kMaxWidth = 1 << 24, kMaxGroups = 1024;
 
 struct NormArgs {
@@ -22,38 +24,287 @@ struct NormArgs {
     float* part;
     int64_t rows, width, x_stride, y_stride, dy_stride, dx_stride;
     float eps, inv_width;
+    int32_t param_type;
 };
 
-// Sum over the block, in every thread.
-__device__ float block_sum(float x) {
-    __shared__ float s[32];
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = x;
-    __syncthreads();
-    float t = 0.0f;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) t += s[w];
-    return t;
+// ------------------------------------------------------------- parameters ---
+
+// V values of gamma or beta from k on (`missing` without one).  Their type is a run-time
+// choice: one branch, the same for all threads, for a load from L1.
+template <int V>
+__device__ __forceinline__ void params_at(const void* p, int32_t type, int64_t k, float missing, float* out) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = missing;
+    } else if (type == ZS_F32) {
+        constexpr int N = V < 4 ? V : 4;
+#pragma unroll
+        for (int i = 0; i < V; i += N)
+            unpack<float, N>(*reinterpret_cast<const Pack<float, N>*>((const float*)p + k + i), out + i);
+    } else if (type == ZS_F16) {
+        unpack<__half, V>(*reinterpret_cast<const Pack<__half, V>*>((const __half*)p + k), out);
+    } else {
+        unpack<__nv_bfloat16, V>(*reinterpret_cast<const Pack<__nv_bfloat16, V>*>((const __nv_bfloat16*)p + k), out);
+    }
+}
+__device__ __forceinline__ void store_param(void* p, int32_t type, int64_t k, float x) {
+    if (type == ZS_F32)
+        ((float*)p)[k] = x;
+    else if (type == ZS_F16)
+        ((__half*)p)[k] = from_float<__half>(x);
+    else
+        ((__nv_bfloat16*)p)[k] = from_float<__nv_bfloat16>(x);
 }
 
-template <typename T, typename P>
-__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormArgs a) {
+// ------------------------------------------------------------------- teams ---
+
+// A team of 1 to 16 warps takes a row: C vectors of V elements to a thread, held in
+// registers from the first sum to the output, so that a row is read once and the
+// variance is of differences from the mean.  A block has threads / (32 warps) teams.
+constexpr int kThreads = 256, kMaxThreads = 512;
+
+struct Team {
+    int warps, number, teams, thread, threads;  // thread: of the team
+};
+__device__ __forceinline__ Team team_of(int warps) {
+    Team t;
+    t.warps = warps;
+    t.threads = 32 * warps;
+    t.number = threadIdx.x / t.threads;
+    t.teams = blockDim.x / t.threads;
+    t.thread = threadIdx.x % t.threads;
+    return t;
+}
+// The sums of x and y over the team, in every thread.  `turn` numbers the team's
+// calls: two places in turn, so that one barrier is enough (who writes a place again has
+// passed the barrier between, which its readers reach after reading).
+__device__ __forceinline__ float2 team_sum(const Team& t, uint32_t turn, float x, float y) {
+    __shared__ float2 s[2][kMaxThreads / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if (t.warps == 1) return make_float2(x, y);
+    float2* const place = s[turn & 1] + t.number * t.warps;
+    if (t.thread % 32 == 0) place[t.thread / 32] = make_float2(x, y);
+    asm volatile("bar.sync %0, %1;" ::"r"(t.number + 1), "r"(t.threads) : "memory");
+    x = y = 0.0f;
+    for (int w = 0; w < t.warps; ++w) {
+        x += place[w].x;
+        y += place[w].y;
+    }
+    return make_float2(x, y);
+}
+
+template <typename T, int V, int C>
+__global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
+    const Team t = team_of(warps);
+    const int32_t vectors = (int32_t)(a.width / V);
+    uint32_t turn = 0;
+    griddep_wait();
+    for (int64_t r = (int64_t)blockIdx.x * t.teams + t.number; r < a.rows; r += (int64_t)gridDim.x * t.teams) {
+        const Pack<T, V>* x = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
+        Pack<T, V>* y = reinterpret_cast<Pack<T, V>*>((T*)a.y + r * a.y_stride);
+        float v[C][V], s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int32_t q = t.thread + c * t.threads;
+            if (q < vectors) {
+                unpack<T, V>(x[q], v[c]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[c][i] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += v[c][i];
+        const float mean = team_sum(t, turn++, s, 0.0f).x * a.inv_width;
+        s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const bool in = t.thread + c * t.threads < vectors;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[c][i] -= mean;
+                s = in ? fmaf(v[c][i], v[c][i], s) : s;
+            }
+        }
+        const float rstd = 1.0f / sqrtf(team_sum(t, turn++, s, 0.0f).x * a.inv_width + a.eps);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int32_t q = t.thread + c * t.threads;
+            if (q >= vectors) break;
+            float g[V], b[V];
+            params_at<V>(a.gamma, a.param_type, (int64_t)q * V, 1.0f, g);
+            params_at<V>(a.beta, a.param_type, (int64_t)q * V, 0.0f, b);
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[i] = fmaf(v[c][i] * rstd, g[i], b[i]);
+            if (ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) y[q] = pack<T, V>(g);
+        }
+        if (t.thread == 0 && a.saved_out != nullptr) {
+            a.saved_out[2 * r] = mean;
+            a.saved_out[2 * r + 1] = rstd;
+        }
+    }
+}
+
+// The gradient in one pass over dy and x: a team keeps its columns' parts of dgamma and
+// dbeta in registers from row to row, and loads its next row before it sums up the
+// present one.  A block's teams add their parts up in shared memory, in their order; a
+// block leaves one row of parts.
+template <typename T, int V, int C, bool PARAMS>
+__global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
+    extern __shared__ float s_part[];  // [2][width], with several teams
+    const Team t = team_of(warps);
+    const int32_t vectors = (int32_t)(a.width / V);
+    const int64_t step = (int64_t)gridDim.x * t.teams;
+    uint32_t turn = 0;
+    griddep_wait();
+    float g[C][V], dg[C][V], db[C][V];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int32_t q = t.thread + c * t.threads;
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[c][i] = dg[c][i] = db[c][i] = 0.0f;
+        if (q < vectors) params_at<V>(a.gamma, a.param_type, (int64_t)q * V, 1.0f, g[c]);
+    }
+    Pack<T, V> x[C], dy[C];
+    float mean = 0.0f, rstd = 0.0f;
+    auto load = [&](int64_t r) {
+        const Pack<T, V>* px = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
+        const Pack<T, V>* pd = reinterpret_cast<const Pack<T, V>*>((const T*)a.dy + r * a.dy_stride);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int32_t q = t.thread + c * t.threads;
+            if (q < vectors) {
+                x[c] = px[q];
+                dy[c] = pd[q];
+            }
+        }
+        mean = a.saved[2 * r];
+        rstd = a.saved[2 * r + 1];
+    };
+    int64_t r = (int64_t)blockIdx.x * t.teams + t.number;
+    if (r < a.rows) load(r);
+    for (; r < a.rows; r += step) {
+        float xh[C][V], e[C][V], s = 0.0f, u = 0.0f;
+        const float scale = rstd;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (t.thread + c * t.threads < vectors) {
+                unpack<T, V>(x[c], xh[c]);
+                unpack<T, V>(dy[c], e[c]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) xh[c][i] = mean, e[c][i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                xh[c][i] = (xh[c][i] - mean) * rstd;
+                if (PARAMS) {
+                    dg[c][i] = fmaf(e[c][i], xh[c][i], dg[c][i]);
+                    db[c][i] += e[c][i];
+                }
+                e[c][i] *= g[c][i];
+                s += e[c][i];
+                u = fmaf(e[c][i], xh[c][i], u);
+            }
+        }
+        if (r + step < a.rows) load(r + step);
+        if (a.dx == nullptr) continue;
+        const float2 sums = team_sum(t, turn++, s, u);
+        const float m = sums.x * a.inv_width, n = sums.y * a.inv_width;
+        Pack<T, V>* dx = reinterpret_cast<Pack<T, V>*>((T*)a.dx + r * a.dx_stride);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int32_t q = t.thread + c * t.threads;
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[c][i] = scale * (e[c][i] - fmaf(xh[c][i], n, m));
+            if (q < vectors && ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) dx[q] = pack<T, V>(e[c]);
+        }
+    }
+    if (!PARAMS) return;
+    float* const out = a.part + 2 * (int64_t)blockIdx.x * a.width;
+    for (int n = 0; n < t.teams; ++n) {
+        if (n == t.number) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int32_t q = t.thread + c * t.threads;
+                if (q >= vectors) break;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int32_t k = q * V + i;
+                    float p = dg[c][i], b = db[c][i];
+                    if (n > 0) p += s_part[k], b += s_part[a.width + k];
+                    if (n + 1 < t.teams) {
+                        s_part[k] = p;
+                        s_part[a.width + k] = b;
+                    } else {
+                        out[k] = p;
+                        out[a.width + k] = b;
+                    }
+                }
+            }
+        }
+        if (t.teams > 1) __syncthreads();
+    }
+}
+
+// Adds up the blocks' parts: 32 columns to a block, 16 threads to a column.
+__global__ void __launch_bounds__(512) norm_param_kernel(const __grid_constant__ NormArgs a, int32_t groups) {
+    __shared__ float s[2][16][33];
+    const int column = threadIdx.x % 32, lane = threadIdx.x / 32;
+    const int64_t k = (int64_t)blockIdx.x * 32 + column;
+    griddep_wait();
+    float g = 0.0f, b = 0.0f;
+    if (k < a.width) {
+#pragma unroll 4
+        for (int32_t q = lane; q < groups; q += 16) {
+            g += a.part[2 * (int64_t)q * a.width + k];
+            b += a.part[(2 * (int64_t)q + 1) * a.width + k];
+        }
+    }
+    s[0][lane][column] = g;
+    s[1][lane][column] = b;
+    __syncthreads();
+    if (lane > 1 || k >= a.width) return;
+    float sum = 0.0f;
+    for (int q = 0; q < 16; ++q) sum += s[lane][q][column];
+    void* const out = lane == 0 ? a.dgamma : a.dbeta;
+    if (out != nullptr) store_param(out, a.param_type, k, sum);
+}
+
+// ----------------------------------------------------------------- long rows ---
+
+// Rows that a team's registers do not hold are read once for each sum, from L2 after
+// the first: a block to a row.
+template <typename T>
+__global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const __grid_constant__ NormArgs a) {
+    const Team t = team_of(kMaxThreads / 32);
+    uint32_t turn = 0;
     griddep_wait();
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T* x = (const T*)a.x + r * a.x_stride;
         T* y = (T*)a.y + r * a.y_stride;
         float s = 0.0f;
-        for (int64_t k = threadIdx.x; k < a.width; k += blockDim.x) s += to_float(x[k]);
-        const float mean = block_sum(s) * a.inv_width;
+#pragma unroll 4
+        for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) s += to_float(x[k]);
+        const float mean = team_sum(t, turn++, s, 0.0f).x * a.inv_width;
         s = 0.0f;
-        for (int64_t k = threadIdx.x; k < a.width; k += blockDim.x) {
+#pragma unroll 4
+        for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) {
             const float d = to_float(x[k]) - mean;
             s = fmaf(d, d, s);
         }
-        const float rstd = 1.0f / sqrtf(block_sum(s) * a.inv_width + a.eps);
-        for (int64_t k = threadIdx.x; k < a.width; k += blockDim.x) {
-            const float g = a.gamma != nullptr ? to_float(((const P*)a.gamma)[k]) : 1.0f;
-            const float b = a.beta != nullptr ? to_float(((const P*)a.beta)[k]) : 0.0f;
+        const float rstd = 1.0f / sqrtf(team_sum(t, turn++, s, 0.0f).x * a.inv_width + a.eps);
+#pragma unroll 4
+        for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) {
+            float g, b;
+            params_at<1>(a.gamma, a.param_type, k, 1.0f, &g);
+            params_at<1>(a.beta, a.param_type, k, 0.0f, &b);
             y[k] = from_float<T>(fmaf((to_float(x[k]) - mean) * rstd, g, b));
         }
         if (threadIdx.x == 0 && a.saved_out != nullptr) {
@@ -62,36 +313,40 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
         }
     }
 }
-
-template <typename T, typename P>
-__global__ void __launch_bounds__(256) norm_dx_kernel(const __grid_constant__ NormArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kMaxThreads) norm_long_dx_kernel(const __grid_constant__ NormArgs a) {
+    const Team t = team_of(kMaxThreads / 32);
+    uint32_t turn = 0;
     griddep_wait();
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *x = (const T*)a.x + r * a.x_stride, *dy = (const T*)a.dy + r * a.dy_stride;
         const float mean = a.saved[2 * r], rstd = a.saved[2 * r + 1];
-        float s = 0.0f, t = 0.0f;
-        for (int64_t k = threadIdx.x; k < a.width; k += blockDim.x) {
-            const float g = to_float(dy[k]) * (a.gamma != nullptr ? to_float(((const P*)a.gamma)[k]) : 1.0f);
+        float s = 0.0f, u = 0.0f, g;
+#pragma unroll 4
+        for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) {
+            params_at<1>(a.gamma, a.param_type, k, 1.0f, &g);
+            g *= to_float(dy[k]);
             s += g;
-            t = fmaf(g, (to_float(x[k]) - mean) * rstd, t);
+            u = fmaf(g, (to_float(x[k]) - mean) * rstd, u);
         }
-        s = block_sum(s) * a.inv_width;
-        t = block_sum(t) * a.inv_width;
-        for (int64_t k = threadIdx.x; k < a.width; k += blockDim.x) {
-            const float g = to_float(dy[k]) * (a.gamma != nullptr ? to_float(((const P*)a.gamma)[k]) : 1.0f);
+        const float2 sums = team_sum(t, turn++, s, u);
+        const float m = sums.x * a.inv_width, n = sums.y * a.inv_width;
+#pragma unroll 4
+        for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) {
+            params_at<1>(a.gamma, a.param_type, k, 1.0f, &g);
             const float xh = (to_float(x[k]) - mean) * rstd;
-            ((T*)a.dx)[r * a.dx_stride + k] = from_float<T>(rstd * (g - s - xh * t));
+            ((T*)a.dx)[r * a.dx_stride + k] = from_float<T>(rstd * (g * to_float(dy[k]) - fmaf(xh, n, m)));
         }
     }
 }
-
-// Sums over the rows of a group, a thread to a column; and over the groups.
+// Parts of dgamma and dbeta: a thread to a column, blocks of rows.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_part_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(256) norm_long_part_kernel(const __grid_constant__ NormArgs a) {
     griddep_wait();
     const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (k >= a.width) return;
     float g = 0.0f, b = 0.0f;
+#pragma unroll 4
     for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
         const float dy = to_float(((const T*)a.dy)[r * a.dy_stride + k]);
         g = fmaf(dy, (to_float(((const T*)a.x)[r * a.x_stride + k]) - a.saved[2 * r]) * a.saved[2 * r + 1], g);
@@ -100,25 +355,115 @@ __global__ void __launch_bounds__(256) norm_part_kernel(const __grid_constant__ 
     a.part[2 * (int64_t)blockIdx.y * a.width + k] = g;
     a.part[(2 * (int64_t)blockIdx.y + 1) * a.width + k] = b;
 }
-template <typename P>
-__global__ void __launch_bounds__(256) norm_param_kernel(const __grid_constant__ NormArgs a, int64_t groups) {
-    griddep_wait();
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= a.width) return;
-    float g = 0.0f, b = 0.0f;
-    for (int64_t q = 0; q < groups; ++q) {
-        g += a.part[2 * q * a.width + k];
-        b += a.part[(2 * q + 1) * a.width + k];
+
+// ------------------------------------------------------------------ launches ---
+
+int64_t groups_of(int64_t rows) { return rows < kMaxGroups ? (rows > 0 ? rows : 1) : kMaxGroups; }
+
+// How a row is dealt to a team: V elements to a vector, C vectors to a thread.  c = 0: the
+// row is too long.
+struct Shape {
+    int v, c, warps;
+};
+Shape shape_of(int64_t width, int v, int most) {
+    const int64_t vectors = width / v;
+    const int per_thread = v == 1 ? 16 : most / v;
+    for (int warps = 1; warps <= kMaxThreads / 32; warps *= 2) {
+        if (vectors > 32ll * warps * per_thread) continue;
+        const int c = (int)((vectors + 32 * warps - 1) / (32 * warps));
+        return {v, v == 1 ? (c <= 4 ? 4 : 16) : c, warps};
     }
-    if (a.dgamma != nullptr) ((P*)a.dgamma)[k] = from_float<P>(g);
-    if (a.dbeta != nullptr) ((P*)a.dbeta)[k] = from_float<P>(b);
+    return {v, 0, kMaxThreads / 32};
+}
+// Whether rows of these matrices (row strides in elements) and the parameters can be
+// accessed as 16-byte vectors.
+template <typename... M>
+bool vectors_fit(int64_t width, int64_t size, const void* gamma, const void* beta, M... matrices) {
+    const int64_t v = 16 / size;
+    if (width % v != 0 || !zs::aligned_to(gamma, 16) || !zs::aligned_to(beta, 16)) return false;
+    auto fits = [&](const void* p, int64_t stride) { return zs::aligned_to(p, 16) && stride % v == 0; };
+    return (fits(matrices.first, matrices.second) && ...);
+}
+struct Matrix {
+    const void* first;
+    int64_t second;
+};
+
+// Blocks of a grid that fill the device, and no more than there are rows for.
+template <typename K>
+unsigned grid_of(K kernel, int threads, size_t shared, int64_t blocks) {
+    int per_sm = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, shared) != cudaSuccess || per_sm < 1) {
+        cudaGetLastError();
+        per_sm = 1;
+    }
+    const int64_t most = (int64_t)per_sm * zs::device_sm_count();
+    return (unsigned)(blocks < most ? (blocks > 0 ? blocks : 1) : most);
 }
 
-int64_t groups_of(int64_t rows) { return rows < 64 ? (rows > 0 ? rows : 1) : 64; }
+template <typename T, int V, int C>
+int32_t launch_rows(const NormArgs& a, int warps, cudaStream_t stream) {
+    const int threads = warps > kThreads / 32 ? 32 * warps : kThreads, teams = threads / (32 * warps);
+    const unsigned grid = grid_of(norm_rows_kernel<T, V, C>, threads, 0, (a.rows + teams - 1) / teams);
+    return launch(norm_rows_kernel<T, V, C>, dim3(grid), threads, stream, "norm_rows_kernel", a, warps);
+}
+template <typename T>
+int32_t launch_forward(const NormArgs& a, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, a.beta, Matrix{a.x, a.x_stride}, Matrix{a.y, a.y_stride});
+    const Shape s = shape_of(a.width, wide ? V : 1, 4 * V);
+    if (s.c == 0) {
+        const unsigned grid = grid_of(norm_long_kernel<T>, kMaxThreads, 0, a.rows);
+        return launch(norm_long_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_kernel", a);
+    }
+    if (!wide) return s.c == 4 ? launch_rows<T, 1, 4>(a, s.warps, stream) : launch_rows<T, 1, 16>(a, s.warps, stream);
+    switch (s.c) {
+    case 1: return launch_rows<T, V, 1>(a, s.warps, stream);
+    case 2: return launch_rows<T, V, 2>(a, s.warps, stream);
+    case 3: return launch_rows<T, V, 3>(a, s.warps, stream);
+    default: return launch_rows<T, V, 4>(a, s.warps, stream);
+    }
+}
 
-unsigned blocks_for(int64_t rows) {
-    const int64_t most = 8 * zs::device_sm_count();
-    return (unsigned)(rows < most ? rows : most);
+int32_t launch_params(const NormArgs& a, int64_t groups, cudaStream_t stream) {
+    return launch(norm_param_kernel, dim3((unsigned)((a.width + 31) / 32)), 512, stream, "norm_param_kernel", a, (int32_t)groups);
+}
+template <typename T, int V, int C>
+int32_t launch_grad_rows(const NormArgs& a, int warps, cudaStream_t stream) {
+    const bool params = a.dgamma != nullptr || a.dbeta != nullptr;
+    const int threads = warps > kThreads / 32 ? 32 * warps : kThreads, teams = threads / (32 * warps);
+    const size_t shared = params && teams > 1 ? 8 * (size_t)a.width : 0;
+    auto go = [&](auto kernel) {
+        unsigned grid = grid_of(kernel, threads, shared, (a.rows + teams - 1) / teams);
+        if (grid > kMaxGroups) grid = kMaxGroups;
+        const int32_t rc = launch_shared(kernel, dim3(grid), threads, shared, stream, "norm_grad_kernel", a, warps);
+        return rc != ZS_OK || !params ? rc : launch_params(a, grid, stream);
+    };
+    return params ? go(norm_grad_kernel<T, V, C, true>) : go(norm_grad_kernel<T, V, C, false>);
+}
+template <typename T>
+int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    const bool params = a.dgamma != nullptr || a.dbeta != nullptr;
+    const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, nullptr, Matrix{a.x, a.x_stride}, Matrix{a.dy, a.dy_stride},
+                                  Matrix{a.dx, a.dx_stride});
+    const Shape s = shape_of(a.width, wide ? V : 1, 16);
+    if (s.c == 0) {
+        if (params) {
+            // (before dx, which may take dy's or x's place)
+            const int64_t groups = a.rows < 64 ? groups_of(a.rows) : 64;
+            ZS_TRY(launch(norm_long_part_kernel<T>, dim3((unsigned)((a.width + 255) / 256), (unsigned)groups), 256, stream,
+                          "norm_long_part_kernel", a));
+            ZS_TRY(launch_params(a, groups, stream));
+        }
+        if (a.dx == nullptr) return ZS_OK;
+        const unsigned grid = grid_of(norm_long_dx_kernel<T>, kMaxThreads, 0, a.rows);
+        return launch(norm_long_dx_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_dx_kernel", a);
+    }
+    if (!wide) return s.c == 4 ? launch_grad_rows<T, 1, 4>(a, s.warps, stream) : launch_grad_rows<T, 1, 16>(a, s.warps, stream);
+    if (s.c == 1) return launch_grad_rows<T, V, 1>(a, s.warps, stream);
+    if (V == 8 || s.c == 2) return launch_grad_rows<T, V, 2>(a, s.warps, stream);
+    return launch_grad_rows<T, V, 16 / V>(a, s.warps, stream);
 }
 
 bool valid_sizes(int64_t rows, int64_t width) {
@@ -142,25 +487,13 @@ NormArgs args_of(const zs_norm* n) {
     a.x = n->x;
     a.gamma = n->gamma;
     a.beta = n->beta;
+    a.param_type = n->param_type;
     a.rows = n->rows;
     a.width = n->width;
     a.x_stride = n->rows > 1 ? n->x_stride : n->width;
     a.eps = (float)n->eps;
     a.inv_width = (float)(1.0 / (double)n->width);
     return a;
-}
-
-template <typename T, typename P>
-int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
-    if (a.dgamma != nullptr || a.dbeta != nullptr) {
-        // (before dx, which may take dy's or x's place)
-        const int64_t groups = groups_of(a.rows);
-        const unsigned wide = (unsigned)((a.width + 255) / 256);
-        ZS_TRY(launch(norm_part_kernel<T>, dim3(wide, (unsigned)groups), 256, stream, "norm_part_kernel", a));
-        ZS_TRY(launch(norm_param_kernel<P>, dim3(wide), 256, stream, "norm_param_kernel", a, groups));
-    }
-    if (a.dx == nullptr || a.rows == 0) return ZS_OK;
-    return launch(norm_dx_kernel<T, P>, dim3(blocks_for(a.rows)), 256, stream, "norm_dx_kernel", a);
 }
 
 }  // namespace
@@ -181,18 +514,12 @@ ZS_API int32_t zero_layer_norm_async(const zs_norm* n, void* y, int64_t y_stride
     a.y = y;
     a.y_stride = n->rows > 1 ? y_stride : n->width;
     a.saved_out = saved;
-    return with_elem(n->type, [&](auto t) {
-        return with_elem(n->param_type, [&](auto p) {
-            return launch(norm_kernel<decltype(t), decltype(p)>, dim3(blocks_for(a.rows)), 256, (cudaStream_t)stream,
-                          "norm_kernel", a);
-        });
-    });
+    return with_elem(n->type, [&](auto t) { return launch_forward<decltype(t)>(a, (cudaStream_t)stream); });
 }
 
 ZS_API int64_t zero_layer_norm_work_bytes(int64_t rows, int64_t width) {
     if (!valid_sizes(rows, width)) return ZS_ERR_ARG;
-    const int64_t groups = rows < 1 ? 1 : rows < kMaxGroups ? rows : kMaxGroups;
-    return 8 * groups * ((width + 3) / 4 * 4);
+    return 8 * groups_of(rows) * ((width + 3) / 4 * 4);
 }
 
 ZS_API int32_t zero_layer_norm_grad_async(const zs_norm* n, const void* dy, int64_t dy_stride, const float* saved,
@@ -220,10 +547,7 @@ ZS_API int32_t zero_layer_norm_grad_async(const zs_norm* n, const void* dy, int6
     a.dgamma = dgamma;
     a.dbeta = dbeta;
     a.part = (float*)work_dev;
-    return with_elem(n->type, [&](auto t) {
-        return with_elem(n->param_type,
-                         [&](auto p) { return launch_grad<decltype(t), decltype(p)>(a, (cudaStream_t)stream); });
-    });
+    return with_elem(n->type, [&](auto t) { return launch_grad<decltype(t)>(a, (cudaStream_t)stream); });
 }
 
 }  // extern "C"
