@@ -1,16 +1,27 @@
 // embed.cu -- embedding lookup with scaling, and the gradient of its table.
+//
+//   out_i = E[id_i] scale,       dE[v] = scale sum_{i: id_i = v} dout_i
+//
+// The gradient sorts the tokens by id (stable, so that the order of a sum is that of
+// the tokens), takes the sorted list in chunks of equal length, however often an id
+// comes, sums each run of one id within a chunk in fp32, and joins the runs that go
+// across chunks.  No floating-point atomics; the same bits in every call.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "cluster_counts.h"
 #include "zs_internal.h"
 
 namespace {
 
 #include "step_common.cuh"
 #include "step_end.cuh"
+#include "loss_common.cuh"
 #include "elem.cuh"
 #include "launch.cuh"
+
+[[maybe_unused]] constexpr uint32_t kSiteEmbed = 19, kSiteSort = 20, kSiteTable = 21;
 
 constexpr int64_t kMaxTokens = 1 << 28, kMaxVocab = 1 << 30, kMaxWidth = 1 << 24;
 
@@ -26,52 +37,353 @@ struct EmbedArgs {
     void* dtable;
     int64_t dtable_stride;
     int32_t accumulate;
+    // the tokens sorted by id, and the list's second place (sort passes write the two
+    // in turn); ids outside the vocabulary count as `vocab` and come last
+    uint32_t *keys, *places, *other_keys, *other_places;
+    int32_t passes, bits;  // of the sort, and of a pass
+    float* part;           // sums of runs that go across chunks: two rows to a chunk
+    int32_t chunk;         // tokens of a chunk
 };
 
-template <typename T>
-__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedArgs a) {
+// ------------------------------------------------------------------- lookup ---
+
+constexpr int kThreads = 256;
+
+// A team of `warps` warps copies a row, four vectors to a thread at a time.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedArgs a, int32_t warps) {
+    const int threads = 32 * warps, teams = kThreads / threads, thread = threadIdx.x % threads;
+    const int64_t vectors = a.width / V;
     griddep_wait();
-    for (int64_t i = blockIdx.x; i < a.tokens; i += gridDim.x) {
+    for (int64_t i = (int64_t)blockIdx.x * teams + threadIdx.x / threads; i < a.tokens; i += (int64_t)gridDim.x * teams) {
         const int64_t v = a.ids[i];
         const bool inside = v >= 0 && v < a.vocab;
-        const T* row = (const T*)a.table + (inside ? v : 0) * a.table_stride;
-        T* out = (T*)a.out + i * a.out_stride;
-        for (int64_t k = threadIdx.x; k < a.width; k += blockDim.x)
-            out[k] = inside ? from_float<T>(to_float(row[k]) * a.scale) : from_float<T>(0.0f);
-    }
-}
-
-// A block to a row of the table: looks through the tokens in their order.
-template <typename T, typename G>
-__global__ void __launch_bounds__(256) embed_grad_kernel(const __grid_constant__ EmbedArgs a) {
-    griddep_wait();
-    for (int64_t v = blockIdx.x; v < a.vocab; v += gridDim.x) {
-        G* row = (G*)a.dtable + v * a.dtable_stride;
-        for (int64_t k0 = 0; k0 < a.width; k0 += 256) {
-            const int64_t k = k0 + threadIdx.x;
-            float s = 0.0f;
-            bool any = false;
-            for (int64_t from = 0; from < a.tokens; from += 256) {
-                const int64_t i = from + threadIdx.x;
-                const bool hit = i < a.tokens && a.ids[i] == v;
-                if (!__syncthreads_or(hit)) continue;
-                any = true;
-                for (int64_t j = from; j < from + 256 && j < a.tokens; ++j)
-                    if (a.ids[j] == v && k < a.width) s += to_float(((const T*)a.dout)[j * a.dout_stride + k]);
+        const Pack<T, V>* row = reinterpret_cast<const Pack<T, V>*>((const T*)a.table + (inside ? v : 0) * a.table_stride);
+        Pack<T, V>* out = reinterpret_cast<Pack<T, V>*>((T*)a.out + i * a.out_stride);
+        for (int64_t k0 = thread; k0 < vectors; k0 += 4 * threads) {
+            Pack<T, V> x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (k0 + q * threads < vectors && inside) x[q] = row[k0 + q * threads];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t k = k0 + q * threads;
+                if (k >= vectors || !ZS_RANGE_OK(kSiteEmbed, k * V, V, a.width)) break;
+                float f[V];
+                if (!inside) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) f[j] = 0.0f;
+                    x[q] = pack<T, V>(f);
+                } else if (a.scale != 1.0f) {
+                    unpack<T, V>(x[q], f);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) f[j] *= a.scale;
+                    x[q] = pack<T, V>(f);
+                }
+                out[k] = x[q];
             }
-            if (k >= a.width) continue;
-            s *= a.scale;
-            if (!a.accumulate)
-                row[k] = from_float<G>(s);
-            else if (any)
-                row[k] = from_float<G>(to_float(row[k]) + s);
         }
     }
 }
 
-unsigned blocks_for(int64_t rows) {
-    const int64_t most = 8 * zs::device_sm_count();
-    return (unsigned)(rows < most ? rows : most);
+// --------------------------------------------------------------------- sort ---
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCtas = 8, kMaxBits = 9, kBins = 1 << kMaxBits;
+constexpr int kSortShared = (kSortWarps * kBins + 2 * kBins) * 4;
+
+// Cluster 0 sorts: passes of `bits` bits of the id from the lowest up.  A warp has a
+// piece of the list, in order; in a pass it counts its digits, the counts turn into
+// places (warps below, CTAs below, smaller digits), and it puts its tokens there, equal
+// digits in their order.  The other clusters fill the table with zeros meanwhile.
+// A cluster of eight has its counts one distributed-shared-memory read apart, and its
+// barrier is the only one on the way.
+template <typename G, int V>
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ EmbedArgs a) {
+    extern __shared__ uint32_t s_sort[];
+    uint32_t(*const count)[kBins] = reinterpret_cast<uint32_t(*)[kBins]>(s_sort);  // of each warp
+    uint32_t* const total = s_sort + kSortWarps * kBins;                            // of this CTA
+    uint32_t* const base = total + kBins;
+    __shared__ uint32_t s_scan[kSortWarps];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    griddep_wait();
+    if (blockIdx.x >= kSortCtas) {
+        if (a.accumulate) return;
+        float zero[V] = {};
+        const Pack<G, V> z = pack<G, V>(zero);
+        const int64_t vectors = a.width / V, step = (int64_t)(gridDim.x - kSortCtas) * kSortWarps;
+        for (int64_t v = (int64_t)(blockIdx.x - kSortCtas) * kSortWarps + warp; v < a.vocab; v += step) {
+            Pack<G, V>* row = reinterpret_cast<Pack<G, V>*>((G*)a.dtable + v * a.dtable_stride);
+            for (int64_t k = lane; k < vectors; k += 32)
+                if (ZS_RANGE_OK(kSiteTable, v, 1, a.vocab)) row[k] = z;
+        }
+        return;
+    }
+    const uint32_t rank = cluster_rank();
+    const int64_t me = (int64_t)rank * kSortWarps + warp, warps = kSortCtas * kSortWarps;
+    const int64_t from = a.tokens * me / warps, to = a.tokens * (me + 1) / warps;
+    const int bins = 1 << a.bits;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        // the last pass writes keys, places
+        const bool first = pass == 0, even = ((a.passes - 1 - pass) & 1) == 0;
+        uint32_t *to_key = even ? a.keys : a.other_keys, *to_place = even ? a.places : a.other_places;
+        const uint32_t *from_key = even ? a.other_keys : a.keys, *from_place = even ? a.other_places : a.places;
+        const int shift = pass * a.bits;
+        auto key_of = [&](int64_t i) {
+            if (!first) return from_key[i];
+            const int64_t v = a.ids[i];
+            return v >= 0 && v < a.vocab ? (uint32_t)v : (uint32_t)a.vocab;
+        };
+        auto digit_of = [&](uint32_t key) { return (key >> shift) & (uint32_t)(bins - 1); };
+        for (int b = lane; b < bins; b += 32) count[warp][b] = 0;
+        __syncwarp();
+        for (int64_t i0 = from; i0 < to; i0 += 32) {
+            const bool in = i0 + lane < to;
+            const uint32_t d = in ? digit_of(key_of(i0 + lane)) : 0xffffffffu;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        uint32_t mine = 0;
+        if (threadIdx.x < bins) {
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = count[w][threadIdx.x];
+                count[w][threadIdx.x] = mine;
+                mine += c;
+            }
+            total[threadIdx.x] = mine;
+        }
+        cluster_arrive();
+        cluster_wait();
+        uint32_t below = 0, all = 0;
+        if (threadIdx.x < bins) {
+            for (uint32_t c = 0; c < kSortCtas; ++c) {
+                uint32_t at, x;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(total + threadIdx.x)), "r"(c));
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+                below += c < rank ? x : 0;
+                all += x;
+            }
+        }
+        // smaller digits
+        uint32_t scan = all;
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += x;
+        }
+        if (lane == 31) s_scan[warp] = scan;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) scan += s_scan[w];
+        if (threadIdx.x < bins) base[threadIdx.x] = scan - all + below;
+        __syncthreads();
+        for (int64_t i0 = from; i0 < to; i0 += 32) {
+            const int64_t i = i0 + lane;
+            const bool in = i < to;
+            const uint32_t key = in ? key_of(i) : 0u, d = in ? digit_of(key) : 0xffffffffu;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            if (in) {
+                const int64_t at = base[d] + count[warp][d] + (uint32_t)__popc(same & ((1u << lane) - 1u));
+                if (ZS_RANGE_OK(kSiteSort, at, 1, a.tokens)) {
+                    to_key[at] = key;
+                    to_place[at] = first ? (uint32_t)i : from_place[i];
+                }
+            }
+            __syncwarp();
+            if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
+            __syncwarp();
+        }
+        // (every CTA's writes, seen by every CTA; and the totals may be written again)
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// ---------------------------------------------------------------------- sums ---
+
+constexpr int kMaxChunk = 64;
+
+template <typename G, int V>
+__device__ __forceinline__ void add_to_table(const EmbedArgs& a, uint32_t key, int64_t k, const float* sum) {
+    Pack<G, V>* to = reinterpret_cast<Pack<G, V>*>((G*)a.dtable + (int64_t)key * a.dtable_stride + k);
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.0f;
+    if (a.accumulate) unpack<G, V>(*to, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = fmaf(sum[i], a.scale, x[i]);
+    if (ZS_RANGE_OK(kSiteTable, key, 1, a.vocab)) *to = pack<G, V>(x);
+}
+// Where the sum of a run that goes across chunks waits: what continues a run from the
+// chunk before in the chunk's first row, the start of one that goes on in its second.
+template <int V>
+__device__ __forceinline__ Pack<float, V>* part_at(const EmbedArgs& a, int64_t chunk, bool start, int64_t k) {
+    return reinterpret_cast<Pack<float, V>*>(a.part + (2 * chunk + (start ? 1 : 0)) * a.width + k);
+}
+
+// A block takes a chunk of the sorted list and up to blockDim.x vectors of the width, eight
+// tokens' vectors under way at once.
+template <typename T, typename G, int V>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ EmbedArgs a, int64_t chunks, int32_t columns) {
+    __shared__ uint32_t s_key[kMaxChunk + 2], s_place[kMaxChunk];
+    const int64_t vectors = a.width / V;
+    constexpr uint32_t kNone = 0xffffffffu;
+    griddep_wait();
+    for (int64_t work = blockIdx.x; work < chunks * columns; work += gridDim.x) {
+        const int64_t c = work / columns, q = (work % columns) * blockDim.x + threadIdx.x;
+        const int64_t first = c * a.chunk;
+        const int32_t n = a.tokens - first < a.chunk ? (int32_t)(a.tokens - first) : a.chunk;
+        __syncthreads();
+        for (int t = threadIdx.x; t < n + 2; t += blockDim.x) {
+            const int64_t i = first + t - 1;
+            s_key[t] = i >= 0 && i < a.tokens ? a.keys[i] : kNone;
+            if (t < n) s_place[t] = a.places[first + t];
+        }
+        __syncthreads();
+        if (q >= vectors) continue;
+        const int64_t k = q * V;
+        const T* const rows = (const T*)a.dout + k;
+        float sum[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+        bool from_before = s_key[0] == s_key[1];
+        for (int t0 = 0; t0 < n; t0 += 8) {
+            Pack<T, V> x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (t0 + u < n && s_key[t0 + u + 1] < (uint32_t)a.vocab)
+                    x[u] = *reinterpret_cast<const Pack<T, V>*>(rows + (int64_t)s_place[t0 + u] * a.dout_stride);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int t = t0 + u;
+                if (t >= n) break;
+                const uint32_t key = s_key[t + 1];
+                if (key >= (uint32_t)a.vocab) break;
+                float f[V];
+                unpack<T, V>(x[u], f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] += f[i];
+                const bool more = s_key[t + 2] == key;
+                if (more && t + 1 < n) continue;
+                // the run's end, here or at the chunk's
+                if (from_before || more) {
+                    *part_at<V>(a, c, !from_before, k) = pack<float, V>(sum);
+                } else {
+                    add_to_table<G, V>(a, key, k, sum);
+                }
+                from_before = false;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+            }
+        }
+    }
+}
+
+// Joins the runs that start in a chunk and go on in the next: their parts in the
+// chunks' order.
+template <typename G, int V>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedArgs a, int64_t chunks, int32_t columns) {
+    const int64_t vectors = a.width / V;
+    griddep_wait();
+    for (int64_t work = blockIdx.x; work < (chunks - 1) * columns; work += gridDim.x) {
+        const int64_t c = work / columns, q = (work % columns) * blockDim.x + threadIdx.x;
+        const int64_t first = c * a.chunk, end = first + a.chunk;
+        const uint32_t key = a.keys[end - 1];
+        if (a.keys[end] != key || key >= (uint32_t)a.vocab) continue;             // goes on, and
+        if (a.keys[first] == key && first > 0 && a.keys[first - 1] == key) continue;  // starts here
+        if (q >= vectors) continue;
+        const int64_t k = q * V;
+        // the last chunk it goes on to: the last whose first token has the key
+        int64_t last = c + 1, beyond = chunks;
+        while (beyond - last > 1) {
+            const int64_t j = (last + beyond) / 2;
+            if (a.keys[j * a.chunk] == key)
+                last = j;
+            else
+                beyond = j;
+        }
+        float sum[V];
+        unpack<float, V>(*part_at<V>(a, c, true, k), sum);
+#pragma unroll 4
+        for (int64_t j = c + 1; j <= last; ++j) {
+            float x[V];
+            unpack<float, V>(*part_at<V>(a, j, false, k), x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] += x[i];
+        }
+        add_to_table<G, V>(a, key, k, sum);
+    }
+}
+
+// ------------------------------------------------------------------- launches ---
+
+// Tokens of a chunk: few where there are few tokens, for more blocks.
+int32_t chunk_of(int64_t tokens) { return tokens >= 65536 ? 64 : tokens >= 32768 ? 32 : tokens >= 8192 ? 16 : 8; }
+
+// The parts of the scratch buffer, as offsets.
+struct Plan {
+    int64_t list[4], part, chunks, total;
+};
+Plan plan_of(int64_t tokens, int64_t width) {
+    Plan p;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 127) / 128 * 128;
+        return here;
+    };
+    for (int64_t& l : p.list) l = take(4 * tokens);
+    const int32_t chunk = chunk_of(tokens);
+    p.chunks = (tokens + chunk - 1) / chunk;
+    p.part = take(8 * p.chunks * width);
+    p.total = at > 0 ? at : 128;
+    return p;
+}
+
+// Blocks of a grid that fill the device, and no more than there is work for.
+template <typename K>
+unsigned grid_of(K kernel, int threads, int64_t blocks) {
+    int per_sm = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess || per_sm < 1) {
+        cudaGetLastError();
+        per_sm = 1;
+    }
+    const int64_t most = (int64_t)per_sm * zs::device_sm_count();
+    return (unsigned)(blocks < most ? (blocks > 0 ? blocks : 1) : most);
+}
+
+// Whether every row starts on a boundary of 16 bytes and has whole vectors of them.
+bool vectors_fit(const void* p, int64_t stride, int64_t width, int64_t size) {
+    return zs::aligned_to(p, 16) && stride * size % 16 == 0 && width * size % 16 == 0;
+}
+
+template <typename T, int V>
+int32_t launch_lookup(const EmbedArgs& a, cudaStream_t stream) {
+    const int64_t vectors = a.width / V;
+    int warps = 1;
+    while (warps < kThreads / 32 && vectors > 128ll * warps) warps *= 2;
+    const int teams = kThreads / (32 * warps);
+    const unsigned grid = grid_of(embed_kernel<T, V>, kThreads, (a.tokens + teams - 1) / teams);
+    return launch(embed_kernel<T, V>, dim3(grid), kThreads, stream, "embed_kernel", a, warps);
+}
+
+template <typename T, typename G, int V>
+int32_t launch_grad(const EmbedArgs& a, int64_t chunks, cudaStream_t stream) {
+    // the sort's cluster, and clusters that fill the other SMs with zeroing blocks
+    const void* sort = (const void*)embed_sort_kernel<G, V>;
+    cudaError_t err = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortShared);
+    const int most = err == cudaSuccess ? active_clusters(sort, kSortThreads, kSortCtas, kSortShared, &err) : 0;
+    if (most < 1) return zs::cuda_fail(err, "embed_sort_kernel");
+    ZS_TRY(launch_clusters(embed_sort_kernel<G, V>, a.accumulate ? 1 : most > 1 ? most : 2, kSortCtas, kSortThreads, kSortShared,
+                           stream, a, "embed_sort_kernel"));
+    if (chunks == 0) return ZS_OK;
+    const int64_t vectors = a.width / V;
+    const int threads = vectors < kThreads ? (int)((vectors + 31) / 32 * 32) : kThreads;
+    const int32_t columns = (int32_t)((vectors + threads - 1) / threads);
+    ZS_TRY(launch(embed_sum_kernel<T, G, V>, dim3(grid_of(embed_sum_kernel<T, G, V>, threads, chunks * columns)), threads, stream,
+                  "embed_sum_kernel", a, chunks, columns));
+    if (chunks == 1) return ZS_OK;
+    return launch(embed_join_kernel<G, V>, dim3(grid_of(embed_join_kernel<G, V>, threads, (chunks - 1) * columns)), threads,
+                  stream, "embed_join_kernel", a, chunks, columns);
 }
 
 bool valid_stride(int64_t rows, int64_t width, int64_t stride) {
@@ -118,13 +430,15 @@ ZS_API int32_t zero_embed_async(const zs_embed* e, void* out, int64_t out_stride
     a.out = out;
     a.out_stride = e->tokens > 1 ? out_stride : e->width;
     return with_elem(e->type, [&](auto t) {
-        return launch(embed_kernel<decltype(t)>, dim3(blocks_for(a.tokens)), 256, (cudaStream_t)stream, "embed_kernel", a);
+        using T = decltype(t);
+        const bool wide = vectors_fit(a.table, a.table_stride, a.width, sizeof(T)) && vectors_fit(out, a.out_stride, a.width, sizeof(T));
+        return wide ? launch_lookup<T, 16 / sizeof(T)>(a, (cudaStream_t)stream) : launch_lookup<T, 1>(a, (cudaStream_t)stream);
     });
 }
 
 ZS_API int64_t zero_embed_work_bytes(int64_t tokens, int64_t width) {
     if (tokens < 0 || tokens > kMaxTokens || width < 1 || width > kMaxWidth) return ZS_ERR_ARG;
-    return 128;
+    return plan_of(tokens, width).total;
 }
 
 ZS_API int32_t zero_embed_grad_async(const zs_embed* e, const void* dout, int64_t dout_stride, void* dtable,
@@ -146,12 +460,27 @@ ZS_API int32_t zero_embed_grad_async(const zs_embed* e, const void* dout, int64_
     a.dtable = dtable;
     a.dtable_stride = e->vocab > 1 ? dtable_stride : e->width;
     a.accumulate = accumulate;
+    if (accumulate && e->tokens == 0) return ZS_OK;
+    const Plan p = plan_of(e->tokens, e->width);
+    uint32_t** const lists[] = {&a.keys, &a.places, &a.other_keys, &a.other_places};
+    for (int i = 0; i < 4; ++i) *lists[i] = (uint32_t*)((char*)work_dev + p.list[i]);
+    a.part = (float*)((char*)work_dev + p.part);
+    a.chunk = chunk_of(e->tokens);
+    int32_t bits = 1;  // of the largest key, `vocab`
+    while (e->vocab >> bits != 0) ++bits;
+    a.passes = (bits + kMaxBits - 1) / kMaxBits;
+    a.bits = (bits + a.passes - 1) / a.passes;
     return with_elem(e->type, [&](auto t) {
         using T = decltype(t);
-        auto go = [&](auto kernel) {
-            return launch(kernel, dim3(blocks_for(a.vocab)), 256, (cudaStream_t)stream, "embed_grad_kernel", a);
+        auto go = [&](auto g) {
+            using G = decltype(g);
+            constexpr int V = 16 / sizeof(T);
+            const bool wide = vectors_fit(dout, a.dout_stride, a.width, sizeof(T)) &&
+                              vectors_fit(dtable, a.dtable_stride, a.width, sizeof(G));
+            return wide ? launch_grad<T, G, V>(a, p.chunks, (cudaStream_t)stream)
+                        : launch_grad<T, G, 1>(a, p.chunks, (cudaStream_t)stream);
         };
-        return dtable_type == ZS_F32 ? go(embed_grad_kernel<T, float>) : go(embed_grad_kernel<T, T>);
+        return dtable_type == ZS_F32 ? go(float()) : go(t);
     });
 }
 
