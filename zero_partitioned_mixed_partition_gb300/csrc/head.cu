@@ -45,14 +45,14 @@ struct Counts {
 // A live row.
 struct __align__(16) Row {
     float top, log_sum;  // t, lnS
-    float coef;          // c times d's scale
+    float coef;          // c
     int32_t label;
 };
 
 // The parts of the scratch buffer, as offsets from its start.
 struct Plan {
     int64_t rows_pad, tiles, piece, sums_room;
-    int64_t index, row, hidden, part, label_logit, d, total;
+    int64_t index, slot, row, hidden, part, label_logit, d, total;
 };
 Plan plan_of(int64_t rows, int64_t width, int64_t vocab, int64_t piece, bool gradient) {
     Plan p = {};
@@ -65,6 +65,7 @@ Plan plan_of(int64_t rows, int64_t width, int64_t vocab, int64_t piece, bool gra
         return here;
     };
     p.index = take(4 * p.rows_pad);
+    p.slot = take(4 * p.rows_pad);
     p.row = take((int64_t)sizeof(Row) * p.rows_pad);
     p.hidden = take(2 * p.rows_pad * width);
     if (gradient) {
@@ -78,7 +79,7 @@ Plan plan_of(int64_t rows, int64_t width, int64_t vocab, int64_t piece, bool gra
         p.part = take(4 * p.sums_room * width);
         p.d = take(2 * p.rows_pad * p.piece);
     } else {
-        p.part = take(8 * p.rows_pad * p.tiles);
+        p.part = take(2 * 8 * p.rows_pad * p.tiles);
         p.label_logit = take(4 * p.rows_pad);
     }
     p.total = at;
@@ -114,7 +115,7 @@ struct HeadArgs {
     uint16_t* dweight;
     int64_t dweight_stride;
     Counts* counts;
-    int32_t* index;
+    int32_t *index, *slot;       // a live row's row; a row's place among the live ones, or -1
     Row* row;
     uint16_t* compact;           // [rows_pad][width]
     void* part;
@@ -123,89 +124,124 @@ struct HeadArgs {
     int64_t rows_pad, tiles, piece, sums_room;
 };
 
-__device__ __forceinline__ bool is_live(const HeadArgs& a, int64_t i) {
-    const int64_t y = a.labels[i];
-    return y >= 0 && y < a.vocab && (a.dlogp == nullptr || a.dlogp[i] != 0.0f);
-}
-
-constexpr int kRowThreads = 1024;
+constexpr int kRowThreads = 1024, kRowsEach = 8;
 
 // Numbers the live rows in their order, and finds the power of 2 by which d is
-// scaled.  One block: the numbers depend on all rows before.
+// scaled.  One block, since the numbers depend on all rows before; kRowsEach rows to a
+// thread at a time, whose loads are under way together.
 __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ HeadArgs a) {
-    __shared__ int32_t s_count[kRowThreads / 32];
+    constexpr int kCounts = kRowsEach * kRowThreads / 32;
+    __shared__ int32_t s_count[kCounts], s_base;
     __shared__ float s_top[kRowThreads / 32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) s_base = 0;
+    griddep_launch_dependents();
     griddep_wait();
-    int32_t base = 0;
     float top = 0.0f;
     const float factor = loss_scale_of(a.ctrl) * a.it;
-    for (int64_t from = 0; from < a.rows; from += kRowThreads) {
-        const int64_t i = from + threadIdx.x;
-        const bool live = i < a.rows && is_live(a, i);
-        const uint32_t votes = __ballot_sync(0xffffffffu, live);
-        if (lane == 0) s_count[warp] = __popc(votes);
-        __syncthreads();
-        int32_t before = base, all = 0;
-        for (int w = 0; w < kRowThreads / 32; ++w) {
-            before += w < warp ? s_count[w] : 0;
-            all += s_count[w];
+    for (int64_t from = 0; from < a.rows; from += kRowsEach * kRowThreads) {
+        int64_t label[kRowsEach];
+        float dlogp[kRowsEach];
+        uint32_t votes[kRowsEach];
+#pragma unroll
+        for (int k = 0; k < kRowsEach; ++k) {
+            const int64_t i = from + k * kRowThreads + threadIdx.x;
+            label[k] = i < a.rows ? a.labels[i] : -1;
+            dlogp[k] = i < a.rows && a.dlogp != nullptr ? a.dlogp[i] : 1.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kRowsEach; ++k) {
+            votes[k] = __ballot_sync(0xffffffffu, label[k] >= 0 && label[k] < a.vocab && dlogp[k] != 0.0f);
+            if (lane == 0) s_count[k * (kRowThreads / 32) + warp] = __popc(votes[k]);
         }
         __syncthreads();
-        base += all;
-        if (live) {
-            const int32_t r = before + __popc(votes & ((1u << lane) - 1u));
-            Row row = {0.0f, 0.0f, 0.0f, (int32_t)a.labels[i]};
+        if (warp == 0) {
+            // counts become the numbers of live rows before them
+            int32_t c[kCounts / 32], sum = 0;
+#pragma unroll
+            for (int q = 0; q < kCounts / 32; ++q) {
+                c[q] = s_count[lane * (kCounts / 32) + q];
+                sum += c[q];
+            }
+            int32_t scan = sum;
+            for (int o = 1; o < 32; o *= 2) {
+                const int32_t x = __shfl_up_sync(0xffffffffu, scan, o);
+                if (lane >= o) scan += x;
+            }
+            int32_t before = s_base + scan - sum;
+#pragma unroll
+            for (int q = 0; q < kCounts / 32; ++q) {
+                s_count[lane * (kCounts / 32) + q] = before;
+                before += c[q];
+            }
+            __syncwarp();
+            if (lane == 31) s_base = before;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kRowsEach; ++k) {
+            const int64_t i = from + k * kRowThreads + threadIdx.x;
+            if (i >= a.rows) break;
+            const bool live = votes[k] >> lane & 1u;
+            const int32_t r = s_count[k * (kRowThreads / 32) + warp] + __popc(votes[k] & ((1u << lane) - 1u));
+            a.slot[i] = live ? r : -1;
+            if (!live) continue;
+            Row row = {0.0f, 0.0f, 0.0f, (int32_t)label[k]};
             if (a.dlogp != nullptr) {
                 row.top = a.saved[2 * i];
                 row.log_sum = a.saved[2 * i + 1];
                 // (a row of nothing but -inf has no gradient)
-                row.coef = row.log_sum == -__int_as_float(0x7f800000) ? 0.0f : factor * a.dlogp[i];
-                // (a NaN counts as infinite)
-                const float size = fabsf(row.coef);
-                top = fmaxf(top, size <= 3.402823466e38f ? size : __int_as_float(0x7f800000));
+                row.coef = row.log_sum == -__int_as_float(0x7f800000) ? 0.0f : factor * dlogp[k];
+                if (fabsf(row.coef) <= 3.402823466e38f) top = fmaxf(top, fabsf(row.coef));
             }
             a.index[r] = (int32_t)i;
             a.row[r] = row;
         }
+        __syncthreads();
     }
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) s_top[warp] = top;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 0; w < kRowThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-        // the largest |c| goes to [2^14, 2^15)
-        int e = top > 0.0f && top <= 3.402823466e38f ? 14 - ilogbf(top) : 0;
+        // the largest finite |c| goes to [2^14, 2^15)
+        int e = top > 0.0f ? 14 - ilogbf(top) : 0;
         e = e > 120 ? 120 : e < -120 ? -120 : e;
-        *a.counts = Counts{base, scalbnf(1.0f, e), scalbnf(1.0f, -e)};
+        *a.counts = Counts{s_base, scalbnf(1.0f, e), scalbnf(1.0f, -e)};
     }
 }
 
-// Copies the live rows' hidden states together, with zeros up to a whole tile,
-// and writes the outputs of the rows that are left out.
+// Copies the live rows' hidden states together, with zeros up to a whole tile, and
+// writes the outputs of the rows that are left out: a warp to a row.
 __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant__ HeadArgs a) {
+    griddep_launch_dependents();
     griddep_wait();
-    const int64_t vectors = a.width / 8;
-    const int32_t live = a.counts->live;
-    const int64_t pad = round_up(live, kTile);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int64_t r = blockIdx.x; r < pad; r += gridDim.x) {
-        const uint4* src = r < live ? reinterpret_cast<const uint4*>((const uint16_t*)a.hidden + a.index[r] * a.hidden_stride)
-                                    : nullptr;
-        uint4* dst = reinterpret_cast<uint4*>(a.compact + r * a.width);
-        for (int64_t k = threadIdx.x; k < vectors; k += blockDim.x) dst[k] = r < live ? src[k] : zero;
-        if (threadIdx.x == 0) {
-            if (r >= live) a.row[r] = Row{0.0f, 0.0f, 0.0f, -1};
-            else if (a.dlogp != nullptr) a.row[r].coef *= a.counts->scale;
+    const int lane = threadIdx.x % 32;
+    const int32_t vectors = (int32_t)(a.width / 8), live = a.counts->live;
+    const int64_t fill = round_up(live, kTile) - live;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < a.rows + fill; i += (int64_t)gridDim.x * 8) {
+        const int32_t slot = i < a.rows ? a.slot[i] : (int32_t)(live + i - a.rows);
+        const bool copy = i < a.rows && slot >= 0;
+        const uint4* from = reinterpret_cast<const uint4*>((const uint16_t*)a.hidden + i * a.hidden_stride);
+        uint4* to = slot >= 0             ? reinterpret_cast<uint4*>(a.compact + (int64_t)slot * a.width)
+                    : a.dhidden != nullptr ? reinterpret_cast<uint4*>(a.dhidden + i * a.dhidden_stride)
+                                           : nullptr;
+        if (to != nullptr) {
+            for (int32_t k0 = lane; k0 < vectors; k0 += 4 * 32) {
+                uint4 x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = copy && k0 + 32 * q < vectors ? from[k0 + 32 * q] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (k0 + 32 * q < vectors) to[k0 + 32 * q] = x[q];
+            }
         }
-    }
-    for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
-        if (is_live(a, i)) continue;
-        if (a.dhidden != nullptr)
-            for (int64_t k = threadIdx.x; k < vectors; k += blockDim.x)
-                reinterpret_cast<uint4*>(a.dhidden + i * a.dhidden_stride)[k] = zero;
-        if (threadIdx.x == 0 && a.logp != nullptr) a.logp[i] = 0.0f;
-        if (threadIdx.x < 2 && a.saved_out != nullptr) a.saved_out[2 * i + threadIdx.x] = 0.0f;
+        if (i >= a.rows) {
+            if (lane == 0) a.row[slot] = Row{0.0f, 0.0f, 0.0f, -1};
+        } else if (slot < 0) {
+            if (lane == 0 && a.logp != nullptr) a.logp[i] = 0.0f;
+            if (lane < 2 && a.saved_out != nullptr) a.saved_out[2 * i + lane] = 0.0f;
+        }
     }
 }
 
@@ -230,7 +266,17 @@ constexpr int kStages = 6, kStep = 64;                      // stages of the rin
 constexpr int kHalfBytes = 128 * kStep * 2;                 // a CTA's half of an operand's stage
 constexpr int kBoxBytes = 64 * kStep * 2;                   // 64 m of 64 k, across k
 constexpr int kRing = kStages * 2 * kHalfBytes;
-constexpr int kProductThreads = 256, kProductShared = kRing + 1024;
+// Steps that the tensor cores add up before their sums go to registers.  They cut a
+// sum off at fp32's last place after every 16 k; over 4096 k that left logits off by
+// 4e-6 of their size (a product in fp32 is off by 1e-7), over 512 k it leaves 5e-7.
+constexpr int kRun = 8;
+constexpr int kProductWarps = 8;                            // that take the sums
+constexpr int kProductThreads = 128 + 32 * kProductWarps;
+constexpr int kStaging = 4096;                              // bytes of a warp: 32 rows of 128
+constexpr int kProductShared = kRing + kProductWarps * kStaging + 1024;
+// Registers of a thread: 168 at launch (384 x 168 = 64,512); the copying and multiplying
+// warps give up what the others take (128 x 72 + 256 x 216 = 64,512).
+constexpr int kFewRegisters = 72, kManyRegisters = 216;
 struct ProductArgs {
     HeadArgs h;
     int64_t first, count;  // the piece
@@ -331,10 +377,47 @@ struct Ring {
     uint32_t bytes[kStages];                 // and what each CTA copied in the last ones
 };
 
+// The 128 columns of a thread's row, as 16-bit numbers or fp32, from registers to
+// memory by way of the warp's staging place, so that a row's 128 bytes go out together.
+// `row`: the lane's row in memory, NULL: none.  Only the first `columns`.
+template <int ELEM, typename F>
+__device__ __forceinline__ void store_rows(uint8_t* staging, int lane, char* row, int32_t columns, F vector_of) {
+    constexpr int kEach = 16 / ELEM, kColumns = 128 / ELEM;  // of a vector; of 128 bytes
+#pragma unroll
+    for (int part = 0; part < 128 / kColumns; ++part) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(staging + lane * 128 + ((q ^ (lane & 7)) << 4)) = vector_of(part * kColumns + q * kEach);
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const int r = t * 4 + lane / 8, q = lane % 8;
+            char* const to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
+            const int32_t column = part * kColumns + q * kEach;
+            if (to != nullptr && column < columns)
+                *reinterpret_cast<uint4*>(to + column * ELEM) =
+                    *reinterpret_cast<const uint4*>(staging + r * 128 + ((q ^ (r & 7)) << 4));
+        }
+        __syncwarp();
+    }
+}
+// One of 32 values (a tree of selections: an index would put them into memory).
+__device__ __forceinline__ float pick(const float* v, int32_t i) {
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = i & 16 ? v[k + 16] : v[k];
+#pragma unroll
+    for (int w = 8; w > 0; w /= 2)
+#pragma unroll
+        for (int k = 0; k < w; ++k) x[k] = i & w ? x[k + w] : x[k];
+    return x[0];
+}
+
 // A pair of CTAs (a cluster of two) takes tile after tile.  In each CTA one thread
 // copies its halves of A and B ahead into a ring of kStages stages; one thread of the
-// first CTA multiplies, 16 k at a time, into one of two sets of sums in tensor memory;
-// four warps turn the other set into the tile's outputs (a thread has a row of it).
+// first CTA multiplies, 16 k at a time, into one of two sets of sums in tensor memory,
+// kRun steps into each in turn; eight warps add the other set to sums in registers (a
+// thread has half a row of the tile) and turn those into the tile's outputs.
 template <typename T, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     head_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -355,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ring.sums_full[s], 1);
-            mbar_init(&ring.sums_empty[s], 2 * 4);
+            mbar_init(&ring.sums_empty[s], 2 * kProductWarps);
         }
         mbar_init(&ring.done, 1);
         ring.failed = 0;
@@ -376,6 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const Tiles w = work_of<MODE>(p, live, pairs);
     const int32_t units = w.m_tiles * w.n_tiles * w.split;
 
+    if (warp < 4) give_registers<kFewRegisters>();
     if (warp == 0 && lane == 0) {
         // what earlier kernels wrote, seen by the copies
         asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -422,149 +506,143 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         bool ok = true;
         for (int32_t u = pair; u < units && ok; u += pairs) {
             const Tile t = tile_of<MODE>(w, u);
-            if (t.from == t.to) continue;  // (nothing to add up: no turn of the sums)
             const uint32_t kind = product_kind<T, kAlongA, kAlongB>(2u * (uint32_t)half_of<MODE>(p, t.n));
-            const int set = turn & 1;
-            ok = mbar_wait(&ring.sums_empty[set], (uint32_t)(turn / 2 + 1) & 1u, &ring.failed);
-            if (!ok) break;
-            tensor_fence_after();
-            for (int32_t k = t.from; k < t.to; ++k, ++at) {
-                const int s = at % kStages;
-                ok = mbar_wait(&ring.full[s], (uint32_t)(at / kStages) & 1u, &ring.failed);
+            for (int32_t k = t.from; k < t.to; ++turn) {
+                const int set = turn & 1;
+                const int32_t stop = k + kRun < t.to ? k + kRun : t.to;
+                ok = mbar_wait(&ring.sums_empty[set], (uint32_t)(turn / 2 + 1) & 1u, &ring.failed);
                 if (!ok) break;
                 tensor_fence_after();
-                const uint8_t* const from = stage0 + s * 2 * kHalfBytes;
-                uint64_t da = operand<kAlongA>(from, kBoxBytes), db = operand<kAlongB>(from + kHalfBytes, kBoxBytes);
+                for (bool add = false; k < stop; ++k, ++at, add = true) {
+                    const int s = at % kStages;
+                    ok = mbar_wait(&ring.full[s], (uint32_t)(at / kStages) & 1u, &ring.failed);
+                    if (!ok) break;
+                    tensor_fence_after();
+                    const uint8_t* const from = stage0 + s * 2 * kHalfBytes;
+                    uint64_t da = operand<kAlongA>(from, kBoxBytes), db = operand<kAlongB>(from + kHalfBytes, kBoxBytes);
 #pragma unroll
-                for (int q = 0; q < kStep / 16; ++q) {
-                    multiply(sums + (uint32_t)set * 256u, da, db, kind, k > t.from || q > 0);
-                    da += operand_step<kAlongA>();
-                    db += operand_step<kAlongB>();
+                    for (int q = 0; q < kStep / 16; ++q) {
+                        multiply(sums + (uint32_t)set * 256u, da, db, kind, add || q > 0);
+                        da += operand_step<kAlongA>();
+                        db += operand_step<kAlongB>();
+                    }
+                    arrive_after_products(&ring.empty[s]);
                 }
-                arrive_after_products(&ring.empty[s]);
+                if (!ok) break;
+                arrive_after_products(&ring.sums_full[set]);
             }
-            if (ok) arrive_after_products(&ring.sums_full[set]);
-            ++turn;
         }
     } else if (warp >= 4) {
-        const int quarter = warp - 4;
+        take_registers<kManyRegisters>();
+        const int quarter = warp % 4, side = (warp - 4) / 4;  // 32 rows, 128 columns
+        uint8_t* const staging = stage0 + kRing + (warp - 4) * kStaging;
+        const float k2 = a.it * kLog2e;
         bool ok = true;
         int32_t turn = 0;
-        const float k2 = a.it * kLog2e;
         for (int32_t u = pair; u < units; u += pairs) {
             const Tile t = tile_of<MODE>(w, u);
-            const int set = turn & 1;
-            const bool any = t.from < t.to;
-            if (any) {
+            const bool mine = side == 0 || half_of<MODE>(p, t.n) == 128;
+            float v[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) v[i] = 0.0f;
+            for (int32_t k = t.from; k < t.to; k += kRun, ++turn) {
+                const int set = turn & 1;
                 ok = ok && all_lanes(mbar_wait<true>(&ring.sums_full[set], (uint32_t)(turn / 2) & 1u, &ring.failed));
                 tensor_fence_after();
-            }
-            const uint32_t from = sums + (uint32_t)set * 256u + ((uint32_t)quarter * 32u << 16);
-            const int64_t r = (int64_t)t.m * kTile + rank * 128 + quarter * 32 + lane;  // the thread's row of the tile
-            const int64_t n0 = (int64_t)t.n * kTile;
-            const int32_t chunks = half_of<MODE>(p, t.n) * 2 / 32;
-            float top = kLowestFloat, s = 0.0f;
-            Row row;
-            int32_t label = -1;  // its place in the tile
-            if (MODE == kLogits || MODE == kGrad) {
-                row = a.row[r];
-                label = row.label - (int32_t)(p.first + n0);
-            }
-            const float unscale = MODE == kDHidden || MODE == kDWeight ? a.counts->unscale : 0.0f;
-            const int32_t to_row = MODE == kDHidden && r < live ? a.index[r] : 0;
-#pragma unroll 1
-            for (int32_t c = 0; c < chunks; ++c) {
-                float v[32];
-                if (any && ok) {
-                    tensor_load(from + (uint32_t)c * 32u, v);
-                    tensor_load_wait();
-                } else {
+                if (mine && ok) {
+                    const uint32_t from = sums + (uint32_t)(set * 256 + side * 128) + ((uint32_t)quarter * 32u << 16);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = ok ? 0.0f : quiet_nan();
-                }
-                const int64_t j0 = n0 + c * 32;  // the chunk's first column
-                if (MODE == kLogits) {
-                    if (label >> 5 == c) {
-                        float x = 0.0f;
+                    for (int c = 0; c < 4; ++c) {
+                        float x[32];
+                        tensor_load(from + (uint32_t)c * 32u, x);
+                        tensor_load_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x = (label & 31) == i ? v[i] : x;
-                        a.label_logit[r] = x;
-                    }
-                    if (j0 + 32 > p.count) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = j0 + i < p.count ? v[i] : -infinity();
-                    }
-                    float high = top;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) high = fmaxf(high, v[i]);
-                    float add[4] = {};
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) add[i % 4] += exp2_approx((v[i] - high) * k2);
-                    s = s * exp2_approx((top - high) * k2) + ((add[0] + add[1]) + (add[2] + add[3]));
-                    top = high;
-                } else if (MODE == kGrad) {
-                    const float shift = row.log_sum * kLog2e, factor = -row.coef;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = factor * exp2_approx(fmaf(v[i] - row.top, k2, -shift));
-                    if (label >> 5 == c) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if ((label & 31) == i) v[i] += row.coef;
-                    }
-                    if (j0 + 32 > p.count) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = j0 + i < p.count ? v[i] : 0.0f;
-                    }
-                    uint4* out = reinterpret_cast<uint4*>(a.d + r * a.piece + j0);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint4 x = make_uint4(narrow2<T>(v[8 * q], v[8 * q + 1]), narrow2<T>(v[8 * q + 2], v[8 * q + 3]),
-                                             narrow2<T>(v[8 * q + 4], v[8 * q + 5]), narrow2<T>(v[8 * q + 6], v[8 * q + 7]));
-                        // (rows that only fill the tile, whatever W holds)
-                        if (row.coef == 0.0f) x = make_uint4(0, 0, 0, 0);
-                        out[q] = x;
-                    }
-                } else {
-                    const bool sum_only = MODE == kDHidden && !(w.split == 1 && p.first == 0 && p.last);
-                    if (MODE == kDHidden ? r < live : r < p.count) {
-                        if (sum_only) {
-                            float* out = (float*)a.part + ((int64_t)t.part * w.m_tiles * kTile + r) * a.width + j0;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if (j0 + 8 * q >= a.width) break;
-                                float4* o = reinterpret_cast<float4*>(out + 8 * q);
-                                float4 x = make_float4(v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]);
-                                float4 y = make_float4(v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]);
-                                if (p.first > 0) {
-                                    const float4 f = o[0], g = o[1];
-                                    x = make_float4(x.x + f.x, x.y + f.y, x.z + f.z, x.w + f.w);
-                                    y = make_float4(y.x + g.x, y.y + g.y, y.z + g.z, y.w + g.w);
-                                }
-                                o[0] = x;
-                                o[1] = y;
-                            }
-                        } else {
-                            uint16_t* out = MODE == kDHidden ? a.dhidden + to_row * a.dhidden_stride + j0
-                                                             : a.dweight + (p.first + r) * a.dweight_stride + j0;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if (j0 + 8 * q >= a.width) break;
-                                uint32_t x[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    x[i] = narrow2<T>(v[8 * q + 2 * i] * unscale, v[8 * q + 2 * i + 1] * unscale);
-                                reinterpret_cast<uint4*>(out)[q] = make_uint4(x[0], x[1], x[2], x[3]);
-                            }
-                        }
+                        for (int i = 0; i < 32; ++i) v[c * 32 + i] += x[i];
                     }
                 }
-            }
-            if (MODE == kLogits) ((float2*)a.part)[(int64_t)t.n * a.rows_pad + r] = make_float2(top, s);
-            if (any) {
                 tensor_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_at(peer_addr(&ring.sums_empty[set], 0));
-                ++turn;
+            }
+            if (!ok) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i) v[i] = quiet_nan();
+            }
+            if (!mine) continue;
+            const int64_t r = (int64_t)t.m * kTile + rank * 128 + quarter * 32 + lane;  // the thread's row of the tile,
+            const int64_t j0 = (int64_t)t.n * kTile + side * 128;                        // and its first column
+            if (MODE == kLogits) {
+                const int32_t label = a.row[r].label - (int32_t)j0;
+                if (__any_sync(0xffffffffu, (uint32_t)label < 128u)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float x = pick(v + c * 32, label & 31);
+                        if (label >> 5 == c) a.label_logit[r] = x;
+                    }
+                }
+                if (j0 + 128 > p.count) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) v[i] = j0 + i < p.count ? v[i] : -infinity();
+                }
+                float high[4] = {kLowestFloat, kLowestFloat, kLowestFloat, kLowestFloat}, add[4] = {};
+#pragma unroll
+                for (int i = 0; i < 128; ++i) high[i % 4] = fmaxf(high[i % 4], v[i]);
+                const float top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+#pragma unroll
+                for (int i = 0; i < 128; ++i) add[i % 4] += exp2_approx((v[i] - top) * k2);
+                ((float2*)a.part)[(2 * (int64_t)t.n + side) * a.rows_pad + r] =
+                    make_float2(top, (add[0] + add[1]) + (add[2] + add[3]));
+            } else if (MODE == kGrad) {
+                const Row row = a.row[r];
+                const float shift = row.log_sum * kLog2e, coef = row.coef * a.counts->scale;
+                const int32_t label = row.label - (int32_t)(p.first + j0);
+#pragma unroll
+                for (int i = 0; i < 128; ++i) v[i] = -coef * exp2_approx(fmaf(v[i] - row.top, k2, -shift));
+                if (__any_sync(0xffffffffu, (uint32_t)label < 128u)) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) v[i] += label == i ? coef : 0.0f;
+                }
+                if (j0 + 128 > p.count) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) v[i] = j0 + i < p.count ? v[i] : 0.0f;
+                }
+                // (rows that only fill the tile are 0, whatever W holds)
+                const bool none = coef == 0.0f;
+                store_rows<2>(staging, lane, reinterpret_cast<char*>(a.d + r * a.piece + j0), 128, [&](int j) {
+                    return none ? make_uint4(0, 0, 0, 0)
+                                : make_uint4(narrow2<T>(v[j], v[j + 1]), narrow2<T>(v[j + 2], v[j + 3]),
+                                             narrow2<T>(v[j + 4], v[j + 5]), narrow2<T>(v[j + 6], v[j + 7]));
+                });
+            } else {
+                const int64_t left = a.width - j0;
+                const int32_t columns = left < 128 ? (int32_t)left : 128;
+                if (MODE == kDHidden && !(w.split == 1 && p.first == 0 && p.last)) {
+                    float* const row = r < live ? (float*)a.part + ((int64_t)t.part * w.m_tiles * kTile + r) * a.width + j0 : nullptr;
+                    if (p.first > 0 && row != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 128; i += 4) {
+                            if (i >= columns) break;
+                            const float4 x = *reinterpret_cast<const float4*>(row + i);
+                            v[i] += x.x, v[i + 1] += x.y, v[i + 2] += x.z, v[i + 3] += x.w;
+                        }
+                    }
+                    __syncwarp();
+                    store_rows<4>(staging, lane, reinterpret_cast<char*>(row), columns, [&](int j) {
+                        return make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                                          __float_as_uint(v[j + 3]));
+                    });
+                } else {
+                    const float unscale = a.counts->unscale;
+                    uint16_t* row = nullptr;
+                    if (MODE == kDHidden && r < live) row = a.dhidden + a.index[r] * a.dhidden_stride + j0;
+                    if (MODE == kDWeight && r < p.count) row = a.dweight + (p.first + r) * a.dweight_stride + j0;
+                    store_rows<2>(staging, lane, reinterpret_cast<char*>(row), columns, [&](int j) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = narrow2<T>(v[j + 2 * i] * unscale, v[j + 2 * i + 1] * unscale);
+                        return make_uint4(x[0], x[1], x[2], x[3]);
+                    });
+                }
             }
         }
     }
@@ -596,30 +674,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     if (warp == 2) tensor_free(sums);
 }
 
-// Joins the statistics of a row's tiles: a warp to a row.
-__global__ void __launch_bounds__(256) head_join_kernel(const __grid_constant__ HeadArgs a) {
+// Joins the statistics of the rows' tiles: 32 rows to a block, 16 threads to a row.
+__global__ void __launch_bounds__(512) head_join_kernel(const __grid_constant__ HeadArgs a) {
+    __shared__ float2 s_part[16][32];
+    const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
+    const int64_t r = (int64_t)blockIdx.x * 32 + lane;
     griddep_wait();
-    const int lane = threadIdx.x % 32;
-    const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (r >= a.counts->live) return;
-    const float2* part = (const float2*)a.part + r;
+    const int32_t live = a.counts->live;
+    if ((int64_t)blockIdx.x * 32 >= live) return;
     const float k = a.it * kLog2e;
     float top = kLowestFloat, s = 0.0f;
-    for (int64_t t = lane; t < a.tiles; t += 32) top = fmaxf(top, part[t * a.rows_pad].x);
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int64_t t = lane; t < a.tiles; t += 32) {
-        const float2 q = part[t * a.rows_pad];
-        s += q.y * exp2_approx((q.x - top) * k);
+    auto join = [&](float2 q) {
+        const float high = fmaxf(top, q.x);
+        s = s * exp2_approx((top - high) * k) + q.y * exp2_approx((q.x - high) * k);
+        top = high;
+    };
+    const float2* part = (const float2*)a.part + r;  // (rows up to a whole tile have statistics)
+    for (int64_t t = group; t < 2 * a.tiles; t += 8 * 16) {
+        float2 q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = t + 16 * i < 2 * a.tiles ? part[(t + 16 * i) * a.rows_pad] : make_float2(kLowestFloat, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) join(q[i]);
     }
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-        const int64_t i = a.index[r];
-        const float log_sum = logf(s);
-        a.logp[i] = s == 0.0f ? log_sum : (a.label_logit[r] - top) * a.it - log_sum;
-        if (a.saved_out != nullptr) {
-            a.saved_out[2 * i] = top;
-            a.saved_out[2 * i + 1] = log_sum;
-        }
+    s_part[group][lane] = make_float2(top, s);
+    __syncthreads();
+    if (group != 0 || r >= live) return;
+    for (int g = 1; g < 16; ++g) join(s_part[g][lane]);
+    const int64_t i = a.index[r];
+    const float log_sum = logf(s);
+    a.logp[i] = s == 0.0f ? log_sum : (a.label_logit[r] - top) * a.it - log_sum;
+    if (a.saved_out != nullptr) {
+        a.saved_out[2 * i] = top;
+        a.saved_out[2 * i + 1] = log_sum;
     }
 }
 
@@ -638,6 +725,7 @@ __global__ void __launch_bounds__(256) head_dhidden_kernel(const __grid_constant
         uint16_t* to = a.dhidden + (int64_t)a.index[r] * a.dhidden_stride;
         for (int64_t k = 4 * threadIdx.x; k < a.width; k += 4 * blockDim.x) {
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
             for (int32_t q = 0; q < w.split; ++q) {
                 const float4 x = *reinterpret_cast<const float4*>(from + q * part + k);
                 s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
@@ -734,6 +822,7 @@ HeadArgs args_of(const zs_head* h, const Plan& p, void* work) {
     a.it = (float)h->inv_temperature;
     a.counts = (Counts*)base;
     a.index = (int32_t*)(base + p.index);
+    a.slot = (int32_t*)(base + p.slot);
     a.row = (Row*)(base + p.row);
     a.compact = (uint16_t*)(base + p.hidden);
     a.part = base + p.part;
@@ -748,9 +837,8 @@ HeadArgs args_of(const zs_head* h, const Plan& p, void* work) {
 
 int32_t launch_rows(const HeadArgs& a, cudaStream_t stream) {
     ZS_TRY(launch(head_rows_kernel, dim3(1), kRowThreads, stream, "head_rows_kernel", a));
-    const int64_t most = 8 * zs::device_sm_count();
-    return launch(head_gather_kernel, dim3((unsigned)(a.rows_pad < most ? a.rows_pad : most)), 256, stream,
-                  "head_gather_kernel", a);
+    const int64_t most = 6 * zs::device_sm_count(), blocks = (a.rows + kTile + 7) / 8;
+    return launch(head_gather_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, stream, "head_gather_kernel", a);
 }
 
 template <typename T> constexpr int32_t type_of();
@@ -766,7 +854,7 @@ int32_t launch_logp(const HeadArgs& a, cudaStream_t stream) {
     if (pairs < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
     ZS_TRY((launch_product<T, kLogits>(ProductArgs{a, 0, a.vocab, 1}, rows, entries, pairs, stream)));
-    return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 8) / 8)), 256, stream, "head_join_kernel", a);
+    return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 32) / 32)), 512, stream, "head_join_kernel", a);
 }
 
 template <typename T>

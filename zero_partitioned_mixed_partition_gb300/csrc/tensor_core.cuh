@@ -104,3 +104,14 @@ __device__ __forceinline__ void signal_after_products(uint64_t* barrier) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(barrier))
                  : "memory");
 }
+
+// ----------------------------------------------------------------- registers ---
+
+// The executing warpgroup (four warps, all of them) goes down to, or up to, N registers a
+// thread.  Those taken have to be given up by others of the block.
+template <int N> __device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
