@@ -10,6 +10,7 @@ namespace {
 #include "step_common.cuh"
 #include "step_end.cuh"
 #include "elem.cuh"
+#include "packed.cuh"
 #include "launch.cuh"
 
 [[maybe_unused]] constexpr uint32_t kSiteNormRow = 18;
@@ -59,8 +60,8 @@ __device__ __forceinline__ void store_param(void* p, int32_t type, int64_t k, fl
 // ------------------------------------------------------------------- teams ---
 
 // A team of 1 to 16 warps takes a row: C vectors of V elements to a thread, held in
-// registers from the first sum to the output, so that a row is read once and the
-// variance is of differences from the mean.  A block has threads / (32 warps) teams.
+// registers as they were read from the first sum to the output, so that a row is read
+// once and the variance is of differences from the mean.  A block has threads / (32 warps) teams.
 constexpr int kThreads = 256, kMaxThreads = 512;
 
 struct Team {
@@ -97,8 +98,37 @@ __device__ __forceinline__ float2 team_sum(const Team& t, uint32_t turn, float x
     return make_float2(x, y);
 }
 
+// The C vectors of a thread as C V / 2 pairs (with V = 1 of two vectors each).
 template <typename T, int V, int C>
-__global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
+__device__ __forceinline__ void pairs_of(const Pack<T, V>* x, uint64_t* p) {
+    float f[C * V];
+#pragma unroll
+    for (int c = 0; c < C; ++c) unpack<T, V>(x[c], f + c * V);
+#pragma unroll
+    for (int i = 0; i < C * V / 2; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+template <int N>
+__device__ __forceinline__ void split_all(const uint64_t* p, float* f) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) split(p[i], f[2 * i], f[2 * i + 1]);
+}
+// For elements one by one: a value for those of the thread's that are in the row, 0 for
+// the others.
+template <int C>
+__device__ __forceinline__ void where_in(const Team& t, int32_t width, float value, uint64_t* p) {
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i)
+        p[i] = pair(t.thread + 2 * i * t.threads < width ? value : 0.0f, t.thread + (2 * i + 1) * t.threads < width ? value : 0.0f);
+}
+__device__ __forceinline__ float sum_of(uint64_t p) {
+    float a, b;
+    split(p, a, b);
+    return a + b;
+}
+
+template <typename T, int V, int C>
+__global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
+    constexpr int N = C * V, H = N / 2;
     const Team t = team_of(warps);
     const int32_t vectors = (int32_t)(a.width / V);
     uint32_t turn = 0;
@@ -106,43 +136,59 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(const __grid_con
     for (int64_t r = (int64_t)blockIdx.x * t.teams + t.number; r < a.rows; r += (int64_t)gridDim.x * t.teams) {
         const Pack<T, V>* x = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
         Pack<T, V>* y = reinterpret_cast<Pack<T, V>*>((T*)a.y + r * a.y_stride);
-        float v[C][V], s = 0.0f;
+        Pack<T, V> raw[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int32_t q = t.thread + c * t.threads;
-            if (q < vectors) {
-                unpack<T, V>(x[q], v[c]);
-            } else {
+            raw[c] = Pack<T, V>{};
+            if (t.thread + c * t.threads < vectors) raw[c] = x[t.thread + c * t.threads];
+        }
+        uint64_t v[H], s[2] = {0, 0};
+        pairs_of<T, V, C>(raw, v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[c][i] = 0.0f;
+        for (int i = 0; i < H; ++i) s[i & 1] = add2(s[i & 1], v[i]);
+        const float mean = team_sum(t, turn++, sum_of(add2(s[0], s[1])), 0.0f).x * a.inv_width;
+        const uint64_t m2 = pair(-mean, -mean);
+        s[0] = s[1] = 0;
+        if constexpr (V == 1) {
+            uint64_t minus[H];
+            where_in<C>(t, vectors, -mean, minus);
+            pairs_of<T, V, C>(raw, v);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const uint64_t d = add2(v[i], minus[i]);
+                s[i & 1] = fma2(d, d, s[i & 1]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (t.thread + c * t.threads >= vectors) break;
+                uint64_t part[V / 2];
+                pairs_of<T, V, 1>(raw + c, part);
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const uint64_t d = add2(part[i], m2);
+                    s[i & 1] = fma2(d, d, s[i & 1]);
+                }
             }
         }
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s += v[c][i];
-        const float mean = team_sum(t, turn++, s, 0.0f).x * a.inv_width;
-        s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const bool in = t.thread + c * t.threads < vectors;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v[c][i] -= mean;
-                s = in ? fmaf(v[c][i], v[c][i], s) : s;
-            }
-        }
-        const float rstd = 1.0f / sqrtf(team_sum(t, turn++, s, 0.0f).x * a.inv_width + a.eps);
+        const float rstd = 1.0f / sqrtf(team_sum(t, turn++, sum_of(add2(s[0], s[1])), 0.0f).x * a.inv_width + a.eps);
+        const uint64_t r2 = pair(rstd, rstd);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int32_t q = t.thread + c * t.threads;
             if (q >= vectors) break;
-            float g[V], b[V];
+            float f[V], g[V], b[V];
+            unpack<T, V>(raw[c], f);
             params_at<V>(a.gamma, a.param_type, (int64_t)q * V, 1.0f, g);
             params_at<V>(a.beta, a.param_type, (int64_t)q * V, 0.0f, b);
+            if constexpr (V == 1) {
+                f[0] = fmaf((f[0] - mean) * rstd, g[0], b[0]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[i] = fmaf(v[c][i] * rstd, g[i], b[i]);
-            if (ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) y[q] = pack<T, V>(g);
+                for (int i = 0; i < V; i += 2)
+                    split(fma2(mul2(add2(pair(f[i], f[i + 1]), m2), r2), pair(g[i], g[i + 1]), pair(b[i], b[i + 1])), f[i], f[i + 1]);
+            }
+            if (ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) y[q] = pack<T, V>(f);
         }
         if (t.thread == 0 && a.saved_out != nullptr) {
             a.saved_out[2 * r] = mean;
@@ -157,22 +203,33 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_kernel(const __grid_con
 // block leaves one row of parts.
 template <typename T, int V, int C, bool PARAMS>
 __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
+    constexpr int N = C * V, H = N / 2;
     extern __shared__ float s_part[];  // [2][width], with several teams
     const Team t = team_of(warps);
     const int32_t vectors = (int32_t)(a.width / V);
     const int64_t step = (int64_t)gridDim.x * t.teams;
     uint32_t turn = 0;
     griddep_wait();
-    float g[C][V], dg[C][V], db[C][V];
+    uint64_t g[H], dg[H], db[H];
+    {
+        float f[N];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int32_t q = t.thread + c * t.threads;
+        for (int c = 0; c < C; ++c) {
+            const int32_t q = t.thread + c * t.threads;
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[c][i] = dg[c][i] = db[c][i] = 0.0f;
-        if (q < vectors) params_at<V>(a.gamma, a.param_type, (int64_t)q * V, 1.0f, g[c]);
+            for (int i = 0; i < V; ++i) f[c * V + i] = 0.0f;
+            if (q < vectors) params_at<V>(a.gamma, a.param_type, (int64_t)q * V, 1.0f, f + c * V);
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            g[i] = pair(f[2 * i], f[2 * i + 1]);
+            dg[i] = db[i] = 0;
+        }
     }
     Pack<T, V> x[C], dy[C];
     float mean = 0.0f, rstd = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) x[c] = dy[c] = Pack<T, V>{};
     auto load = [&](int64_t r) {
         const Pack<T, V>* px = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
         const Pack<T, V>* pd = reinterpret_cast<const Pack<T, V>*>((const T*)a.dy + r * a.dy_stride);
@@ -190,44 +247,43 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_con
     int64_t r = (int64_t)blockIdx.x * t.teams + t.number;
     if (r < a.rows) load(r);
     for (; r < a.rows; r += step) {
-        float xh[C][V], e[C][V], s = 0.0f, u = 0.0f;
-        const float scale = rstd;
+        uint64_t xh[H], e[H], s = 0, u = 0;
+        const uint64_t r2 = pair(rstd, rstd), m2 = pair(-mean, -mean);
+        pairs_of<T, V, C>(x, xh);
+        pairs_of<T, V, C>(dy, e);
+        // (vectors outside the row have dy = 0 and gamma = 0, so xh's value there is of no
+        // account as long as it is finite, and it is wherever the row's is)
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (t.thread + c * t.threads < vectors) {
-                unpack<T, V>(x[c], xh[c]);
-                unpack<T, V>(dy[c], e[c]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) xh[c][i] = mean, e[c][i] = 0.0f;
+        for (int i = 0; i < H; ++i) {
+            xh[i] = mul2(add2(xh[i], m2), r2);
+            if (PARAMS) {
+                dg[i] = fma2(e[i], xh[i], dg[i]);
+                db[i] = add2(db[i], e[i]);
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                xh[c][i] = (xh[c][i] - mean) * rstd;
-                if (PARAMS) {
-                    dg[c][i] = fmaf(e[c][i], xh[c][i], dg[c][i]);
-                    db[c][i] += e[c][i];
-                }
-                e[c][i] *= g[c][i];
-                s += e[c][i];
-                u = fmaf(e[c][i], xh[c][i], u);
-            }
+            e[i] = mul2(e[i], g[i]);
+            s = add2(s, e[i]);
+            u = fma2(e[i], xh[i], u);
         }
         if (r + step < a.rows) load(r + step);
         if (a.dx == nullptr) continue;
-        const float2 sums = team_sum(t, turn++, s, u);
-        const float m = sums.x * a.inv_width, n = sums.y * a.inv_width;
+        const float2 sums = team_sum(t, turn++, sum_of(s), sum_of(u));
+        const float m = -sums.x * a.inv_width, n = -sums.y * a.inv_width;
+        const uint64_t mm = pair(m, m), nn = pair(n, n);
         Pack<T, V>* dx = reinterpret_cast<Pack<T, V>*>((T*)a.dx + r * a.dx_stride);
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < H; ++i) split(mul2(fma2(xh[i], nn, add2(e[i], mm)), r2), f[2 * i], f[2 * i + 1]);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int32_t q = t.thread + c * t.threads;
-#pragma unroll
-            for (int i = 0; i < V; ++i) e[c][i] = scale * (e[c][i] - fmaf(xh[c][i], n, m));
-            if (q < vectors && ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) dx[q] = pack<T, V>(e[c]);
+            if (q < vectors && ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) dx[q] = pack<T, V>(f + c * V);
         }
     }
     if (!PARAMS) return;
     float* const out = a.part + 2 * (int64_t)blockIdx.x * a.width;
+    float pg[N], pb[N];
+    split_all<N>(dg, pg);
+    split_all<N>(db, pb);
     for (int n = 0; n < t.teams; ++n) {
         if (n == t.number) {
 #pragma unroll
@@ -237,7 +293,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int32_t k = q * V + i;
-                    float p = dg[c][i], b = db[c][i];
+                    float p = pg[c * V + i], b = pb[c * V + i];
                     if (n > 0) p += s_part[k], b += s_part[a.width + k];
                     if (n + 1 < t.teams) {
                         s_part[k] = p;
@@ -411,18 +467,14 @@ template <typename T>
 int32_t launch_forward(const NormArgs& a, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, a.beta, Matrix{a.x, a.x_stride}, Matrix{a.y, a.y_stride});
-    const Shape s = shape_of(a.width, wide ? V : 1, 4 * V);
+    const Shape s = shape_of(a.width, wide ? V : 1, 8 * V);
     if (s.c == 0) {
         const unsigned grid = grid_of(norm_long_kernel<T>, kMaxThreads, 0, a.rows);
         return launch(norm_long_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_kernel", a);
     }
     if (!wide) return s.c == 4 ? launch_rows<T, 1, 4>(a, s.warps, stream) : launch_rows<T, 1, 16>(a, s.warps, stream);
-    switch (s.c) {
-    case 1: return launch_rows<T, V, 1>(a, s.warps, stream);
-    case 2: return launch_rows<T, V, 2>(a, s.warps, stream);
-    case 3: return launch_rows<T, V, 3>(a, s.warps, stream);
-    default: return launch_rows<T, V, 4>(a, s.warps, stream);
-    }
+    if (s.c <= 2) return launch_rows<T, V, 2>(a, s.warps, stream);
+    return s.c <= 4 ? launch_rows<T, V, 4>(a, s.warps, stream) : launch_rows<T, V, 8>(a, s.warps, stream);
 }
 
 int32_t launch_params(const NormArgs& a, int64_t groups, cudaStream_t stream) {
