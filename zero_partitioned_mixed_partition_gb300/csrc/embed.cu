@@ -55,8 +55,12 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
     const int threads = 32 * warps, teams = kThreads / threads, thread = threadIdx.x % threads;
     const int64_t vectors = a.width / V;
     griddep_wait();
-    for (int64_t i = (int64_t)blockIdx.x * teams + threadIdx.x / threads; i < a.tokens; i += (int64_t)gridDim.x * teams) {
-        const int64_t v = a.ids[i];
+    const int64_t step = (int64_t)gridDim.x * teams;
+    int64_t i = (int64_t)blockIdx.x * teams + threadIdx.x / threads;
+    int64_t next = i < a.tokens ? a.ids[i] : 0;
+    for (; i < a.tokens; i += step) {
+        const int64_t v = next;
+        if (i + step < a.tokens) next = a.ids[i + step];  // (ahead: a row's load waits for its id)
         const bool inside = v >= 0 && v < a.vocab;
         const Pack<T, V>* row = reinterpret_cast<const Pack<T, V>*>((const T*)a.table + (inside ? v : 0) * a.table_stride);
         Pack<T, V>* out = reinterpret_cast<Pack<T, V>*>((T*)a.out + i * a.out_stride);
@@ -88,6 +92,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
 
 // --------------------------------------------------------------------- sort ---
 
+constexpr int kAhead = 8;  // loads of 32 tokens that a warp has under way
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCtas = 8, kMaxBits = 9, kBins = 1 << kMaxBits;
 constexpr int kSortShared = (kSortWarps * kBins + 2 * kBins) * 4;
 
@@ -105,6 +110,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
     uint32_t* const base = total + kBins;
     __shared__ uint32_t s_scan[kSortWarps];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    griddep_launch_dependents();
     griddep_wait();
     if (blockIdx.x >= kSortCtas) {
         if (a.accumulate) return;
@@ -136,12 +142,19 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
         auto digit_of = [&](uint32_t key) { return (key >> shift) & (uint32_t)(bins - 1); };
         for (int b = lane; b < bins; b += 32) count[warp][b] = 0;
         __syncwarp();
-        for (int64_t i0 = from; i0 < to; i0 += 32) {
-            const bool in = i0 + lane < to;
-            const uint32_t d = in ? digit_of(key_of(i0 + lane)) : 0xffffffffu;
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
-            __syncwarp();
+        for (int64_t i0 = from; i0 < to; i0 += 32 * kAhead) {
+            uint32_t key[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) key[q] = i0 + 32 * q + lane < to ? key_of(i0 + 32 * q + lane) : 0u;
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                if (i0 + 32 * q >= to) break;
+                const bool in = i0 + 32 * q + lane < to;
+                const uint32_t d = in ? digit_of(key[q]) : 0xffffffffu;
+                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
+                __syncwarp();
+            }
         }
         __syncthreads();
         uint32_t mine = 0;
@@ -176,21 +189,31 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
         for (int w = 0; w < warp; ++w) scan += s_scan[w];
         if (threadIdx.x < bins) base[threadIdx.x] = scan - all + below;
         __syncthreads();
-        for (int64_t i0 = from; i0 < to; i0 += 32) {
-            const int64_t i = i0 + lane;
-            const bool in = i < to;
-            const uint32_t key = in ? key_of(i) : 0u, d = in ? digit_of(key) : 0xffffffffu;
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            if (in) {
-                const int64_t at = base[d] + count[warp][d] + (uint32_t)__popc(same & ((1u << lane) - 1u));
-                if (ZS_RANGE_OK(kSiteSort, at, 1, a.tokens)) {
-                    to_key[at] = key;
-                    to_place[at] = first ? (uint32_t)i : from_place[i];
-                }
+        for (int64_t i0 = from; i0 < to; i0 += 32 * kAhead) {
+            uint32_t key[kAhead], place[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int64_t i = i0 + 32 * q + lane;
+                key[q] = i < to ? key_of(i) : 0u;
+                place[q] = first ? (uint32_t)i : i < to ? from_place[i] : 0u;
             }
-            __syncwarp();
-            if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
-            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                if (i0 + 32 * q >= to) break;
+                const bool in = i0 + 32 * q + lane < to;
+                const uint32_t d = in ? digit_of(key[q]) : 0xffffffffu;
+                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                if (in) {
+                    const int64_t at = base[d] + count[warp][d] + (uint32_t)__popc(same & ((1u << lane) - 1u));
+                    if (ZS_RANGE_OK(kSiteSort, at, 1, a.tokens)) {
+                        to_key[at] = key[q];
+                        to_place[at] = place[q];
+                    }
+                }
+                __syncwarp();
+                if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
+                __syncwarp();
+            }
         }
         // (every CTA's writes, seen by every CTA; and the totals may be written again)
         cluster_arrive();
@@ -204,14 +227,26 @@ constexpr int kMaxChunk = 64;
 
 template <typename G, int V>
 __device__ __forceinline__ void add_to_table(const EmbedArgs& a, uint32_t key, int64_t k, const float* sum) {
+    if (!ZS_RANGE_OK(kSiteTable, key, 1, a.vocab)) return;
     Pack<G, V>* to = reinterpret_cast<Pack<G, V>*>((G*)a.dtable + (int64_t)key * a.dtable_stride + k);
+    if constexpr (sizeof(G) == 4 && V % 4 == 0) {
+        // added in L2: nothing waits for the row (an element is added to once in a call, so
+        // no order can matter)
+        if (a.accumulate) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"((float*)to + i), "f"(sum[i] * a.scale),
+                             "f"(sum[i + 1] * a.scale), "f"(sum[i + 2] * a.scale), "f"(sum[i + 3] * a.scale) : "memory");
+            return;
+        }
+    }
     float x[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = 0.0f;
     if (a.accumulate) unpack<G, V>(*to, x);
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = fmaf(sum[i], a.scale, x[i]);
-    if (ZS_RANGE_OK(kSiteTable, key, 1, a.vocab)) *to = pack<G, V>(x);
+    *to = pack<G, V>(x);
 }
 // Where the sum of a run that goes across chunks waits: what continues a run from the
 // chunk before in the chunk's first row, the start of one that goes on in its second.
@@ -227,6 +262,7 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
     __shared__ uint32_t s_key[kMaxChunk + 2], s_place[kMaxChunk];
     const int64_t vectors = a.width / V;
     constexpr uint32_t kNone = 0xffffffffu;
+    griddep_launch_dependents();
     griddep_wait();
     for (int64_t work = blockIdx.x; work < chunks * columns; work += gridDim.x) {
         const int64_t c = work / columns, q = (work % columns) * blockDim.x + threadIdx.x;
@@ -290,25 +326,29 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
         const uint32_t key = a.keys[end - 1];
         if (a.keys[end] != key || key >= (uint32_t)a.vocab) continue;             // goes on, and
         if (a.keys[first] == key && first > 0 && a.keys[first - 1] == key) continue;  // starts here
+        // the last chunk it goes on to: the last of those whose first token has the key
+        int64_t last = c + 1;
+        for (bool more = true; more;) {
+            const int64_t j = last + 1 + threadIdx.x % 32;
+            const uint32_t votes = __ballot_sync(0xffffffffu, j < chunks && a.keys[j * a.chunk] == key);
+            last += votes == 0xffffffffu ? 32 : __ffs(~votes) - 1;
+            more = votes == 0xffffffffu;
+        }
         if (q >= vectors) continue;
         const int64_t k = q * V;
-        // the last chunk it goes on to: the last whose first token has the key
-        int64_t last = c + 1, beyond = chunks;
-        while (beyond - last > 1) {
-            const int64_t j = (last + beyond) / 2;
-            if (a.keys[j * a.chunk] == key)
-                last = j;
-            else
-                beyond = j;
-        }
         float sum[V];
         unpack<float, V>(*part_at<V>(a, c, true, k), sum);
-#pragma unroll 4
-        for (int64_t j = c + 1; j <= last; ++j) {
-            float x[V];
-            unpack<float, V>(*part_at<V>(a, j, false, k), x);
+        for (int64_t j = c + 1; j <= last; j += 8) {
+            Pack<float, V> x[8];
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] += x[i];
+            for (int u = 0; u < 8; ++u)
+                if (j + u <= last) x[u] = *part_at<V>(a, j + u, false, k);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (j + u > last) break;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] += x[u].v[i];
+            }
         }
         add_to_table<G, V>(a, key, k, sum);
     }
