@@ -49,6 +49,15 @@ struct EmbedArgs {
 
 constexpr int kThreads = 256;
 
+// (Rows written for another kernel to read once: they leave the table its place in L2.)
+template <typename T, int V>
+__device__ __forceinline__ void store_stream(Pack<T, V>* to, const Pack<T, V>& x) {
+    if constexpr (sizeof(x) == 16)
+        __stcs(reinterpret_cast<uint4*>(to), *reinterpret_cast<const uint4*>(&x));
+    else
+        *to = x;
+}
+
 // A team of `warps` warps copies a row, four vectors to a thread at a time.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedArgs a, int32_t warps) {
@@ -84,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
                     for (int j = 0; j < V; ++j) f[j] *= a.scale;
                     x[q] = pack<T, V>(f);
                 }
-                out[k] = x[q];
+                store_stream(out + k, x[q]);
             }
         }
     }
@@ -95,6 +104,17 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
 constexpr int kAhead = 8;  // loads of 32 tokens that a warp has under way
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCtas = 8, kMaxBits = 9, kBins = 1 << kMaxBits;
 constexpr int kSortShared = (kSortWarps * kBins + 2 * kBins) * 4;
+
+// The lanes of the warp with the same digit (those of `in`): a vote for each bit.  (The
+// instruction that matches values took 70 cycles of the SM; nine votes take some 10.)
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, int bits, bool in) {
+    uint32_t same = __ballot_sync(0xffffffffu, in);
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t votes = __ballot_sync(0xffffffffu, d >> b & 1u);
+        same &= d >> b & 1u ? votes : ~votes;
+    }
+    return same;
+}
 
 // Cluster 0 sorts: passes of `bits` bits of the id from the lowest up.  A warp has a
 // piece of the list, in order; in a pass it counts its digits, the counts turn into
@@ -116,6 +136,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
         if (a.accumulate) return;
         float zero[V] = {};
         const Pack<G, V> z = pack<G, V>(zero);
+        // (rows that lie end to end are one)
+        const bool flat = a.dtable_stride == a.width;
+        if (flat) {
+            const int64_t vectors = a.vocab * (a.width / V), step = (int64_t)(gridDim.x - kSortCtas) * kSortThreads;
+            Pack<G, V>* const table = reinterpret_cast<Pack<G, V>*>(a.dtable);
+            for (int64_t k = (int64_t)(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x; k < vectors; k += step)
+                if (ZS_RANGE_OK(kSiteTable, k * V, V, a.vocab * a.width)) table[k] = z;
+            return;
+        }
         const int64_t vectors = a.width / V, step = (int64_t)(gridDim.x - kSortCtas) * kSortWarps;
         for (int64_t v = (int64_t)(blockIdx.x - kSortCtas) * kSortWarps + warp; v < a.vocab; v += step) {
             Pack<G, V>* row = reinterpret_cast<Pack<G, V>*>((G*)a.dtable + v * a.dtable_stride);
@@ -150,8 +179,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
             for (int q = 0; q < kAhead; ++q) {
                 if (i0 + 32 * q >= to) break;
                 const bool in = i0 + 32 * q + lane < to;
-                const uint32_t d = in ? digit_of(key[q]) : 0xffffffffu;
-                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                const uint32_t d = digit_of(key[q]), same = same_digit(d, a.bits, in);
                 if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
                 __syncwarp();
             }
@@ -201,8 +229,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
             for (int q = 0; q < kAhead; ++q) {
                 if (i0 + 32 * q >= to) break;
                 const bool in = i0 + 32 * q + lane < to;
-                const uint32_t d = in ? digit_of(key[q]) : 0xffffffffu;
-                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                const uint32_t d = digit_of(key[q]), same = same_digit(d, a.bits, in);
                 if (in) {
                     const int64_t at = base[d] + count[warp][d] + (uint32_t)__popc(same & ((1u << lane) - 1u));
                     if (ZS_RANGE_OK(kSiteSort, at, 1, a.tokens)) {
@@ -379,18 +406,6 @@ Plan plan_of(int64_t tokens, int64_t width) {
     return p;
 }
 
-// Blocks of a grid that fill the device, and no more than there is work for.
-template <typename K>
-unsigned grid_of(K kernel, int threads, int64_t blocks) {
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess || per_sm < 1) {
-        cudaGetLastError();
-        per_sm = 1;
-    }
-    const int64_t most = (int64_t)per_sm * zs::device_sm_count();
-    return (unsigned)(blocks < most ? (blocks > 0 ? blocks : 1) : most);
-}
-
 // Whether every row starts on a boundary of 16 bytes and has whole vectors of them.
 bool vectors_fit(const void* p, int64_t stride, int64_t width, int64_t size) {
     return zs::aligned_to(p, 16) && stride * size % 16 == 0 && width * size % 16 == 0;
@@ -402,7 +417,8 @@ int32_t launch_lookup(const EmbedArgs& a, cudaStream_t stream) {
     int warps = 1;
     while (warps < kThreads / 32 && vectors > 128ll * warps) warps *= 2;
     const int teams = kThreads / (32 * warps);
-    const unsigned grid = grid_of(embed_kernel<T, V>, kThreads, (a.tokens + teams - 1) / teams);
+    const unsigned grid = grid_of((const void*)embed_kernel<T, V>, kThreads, 0, (a.tokens + teams - 1) / teams);
+    if (grid == 0) return ZS_ERR_CUDA;
     return launch(embed_kernel<T, V>, dim3(grid), kThreads, stream, "embed_kernel", a, warps);
 }
 
@@ -419,11 +435,12 @@ int32_t launch_grad(const EmbedArgs& a, int64_t chunks, cudaStream_t stream) {
     const int64_t vectors = a.width / V;
     const int threads = vectors < kThreads ? (int)((vectors + 31) / 32 * 32) : kThreads;
     const int32_t columns = (int32_t)((vectors + threads - 1) / threads);
-    ZS_TRY(launch(embed_sum_kernel<T, G, V>, dim3(grid_of(embed_sum_kernel<T, G, V>, threads, chunks * columns)), threads, stream,
-                  "embed_sum_kernel", a, chunks, columns));
+    const unsigned grid = grid_of((const void*)embed_sum_kernel<T, G, V>, threads, 0, chunks * columns);
+    const unsigned joins = grid_of((const void*)embed_join_kernel<G, V>, threads, 0, (chunks - 1) * columns);
+    if (grid == 0 || joins == 0) return ZS_ERR_CUDA;
+    ZS_TRY(launch(embed_sum_kernel<T, G, V>, dim3(grid), threads, stream, "embed_sum_kernel", a, chunks, columns));
     if (chunks == 1) return ZS_OK;
-    return launch(embed_join_kernel<G, V>, dim3(grid_of(embed_join_kernel<G, V>, threads, (chunks - 1) * columns)), threads,
-                  stream, "embed_join_kernel", a, chunks, columns);
+    return launch(embed_join_kernel<G, V>, dim3(joins), threads, stream, "embed_join_kernel", a, chunks, columns);
 }
 
 bool valid_stride(int64_t rows, int64_t width, int64_t stride) {

@@ -472,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             const int32_t m0 = t.m * (int32_t)kTile + (int32_t)rank * 128, n0 = t.n * (int32_t)kTile + (int32_t)rank * half;
             for (int32_t k = t.from; k < t.to; ++k, ++at) {
                 const int s = at % kStages;
-                if (!mbar_wait(&ring.empty[s], (uint32_t)(at / kStages + 1) & 1u, &ring.failed)) {
+                if (!mbar_wait<false, true>(&ring.empty[s], (uint32_t)(at / kStages + 1) & 1u, &ring.failed)) {
                     ok = false;
                     break;
                 }
@@ -500,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
         // (the last products' arrivals at this CTA's barriers, before it leaves)
         for (int32_t i = at > kStages ? at - kStages : 0; i < at && ok; ++i)
-            ok = mbar_wait(&ring.empty[i % kStages], (uint32_t)(i / kStages) & 1u, &ring.failed);
+            ok = mbar_wait<false, true>(&ring.empty[i % kStages], (uint32_t)(i / kStages) & 1u, &ring.failed);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         int32_t at = 0, turn = 0;
         bool ok = true;
@@ -510,12 +510,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             for (int32_t k = t.from; k < t.to; ++turn) {
                 const int set = turn & 1;
                 const int32_t stop = k + kRun < t.to ? k + kRun : t.to;
-                ok = mbar_wait(&ring.sums_empty[set], (uint32_t)(turn / 2 + 1) & 1u, &ring.failed);
+                ok = mbar_wait<false, true>(&ring.sums_empty[set], (uint32_t)(turn / 2 + 1) & 1u, &ring.failed);
                 if (!ok) break;
                 tensor_fence_after();
                 for (bool add = false; k < stop; ++k, ++at, add = true) {
                     const int s = at % kStages;
-                    ok = mbar_wait(&ring.full[s], (uint32_t)(at / kStages) & 1u, &ring.failed);
+                    ok = mbar_wait<false, true>(&ring.full[s], (uint32_t)(at / kStages) & 1u, &ring.failed);
                     if (!ok) break;
                     tensor_fence_after();
                     const uint8_t* const from = stage0 + s * 2 * kHalfBytes;
@@ -547,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             for (int i = 0; i < 128; ++i) v[i] = 0.0f;
             for (int32_t k = t.from; k < t.to; k += kRun, ++turn) {
                 const int set = turn & 1;
-                ok = ok && all_lanes(mbar_wait<true>(&ring.sums_full[set], (uint32_t)(turn / 2) & 1u, &ring.failed));
+                ok = ok && all_lanes(mbar_wait<true, true>(&ring.sums_full[set], (uint32_t)(turn / 2) & 1u, &ring.failed));
                 tensor_fence_after();
                 if (mine && ok) {
                     const uint32_t from = sums + (uint32_t)(set * 256 + side * 128) + ((uint32_t)quarter * 32u << 16);
@@ -674,9 +674,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     if (warp == 2) tensor_free(sums);
 }
 
-// Joins the statistics of the rows' tiles: 32 rows to a block, 16 threads to a row.
-__global__ void __launch_bounds__(512) head_join_kernel(const __grid_constant__ HeadArgs a) {
-    __shared__ float2 s_part[16][32];
+// Joins the statistics of the rows' tiles: 32 rows to a block, 32 threads to a row.
+__global__ void __launch_bounds__(1024) head_join_kernel(const __grid_constant__ HeadArgs a) {
+    __shared__ float2 s_part[32][33];
     const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
     const int64_t r = (int64_t)blockIdx.x * 32 + lane;
     griddep_wait();
@@ -690,20 +690,26 @@ __global__ void __launch_bounds__(512) head_join_kernel(const __grid_constant__ 
         top = high;
     };
     const float2* part = (const float2*)a.part + r;  // (rows up to a whole tile have statistics)
-    for (int64_t t = group; t < 2 * a.tiles; t += 8 * 16) {
+    for (int64_t t = group; t < 2 * a.tiles; t += 8 * 32) {
         float2 q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = t + 16 * i < 2 * a.tiles ? part[(t + 16 * i) * a.rows_pad] : make_float2(kLowestFloat, 0.0f);
+        for (int i = 0; i < 8; ++i) q[i] = t + 32 * i < 2 * a.tiles ? part[(t + 32 * i) * a.rows_pad] : make_float2(kLowestFloat, 0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) join(q[i]);
     }
     s_part[group][lane] = make_float2(top, s);
     __syncthreads();
-    if (group != 0 || r >= live) return;
-    for (int g = 1; g < 16; ++g) join(s_part[g][lane]);
-    const int64_t i = a.index[r];
+    // a warp to a row from here
+    const int64_t r1 = (int64_t)blockIdx.x * 32 + group;
+    const float2 mine = s_part[lane][group];
+    top = mine.x;
+    s = mine.y;
+    for (int o = 16; o > 0; o >>= 1)
+        join(make_float2(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, s, o)));
+    if (lane != 0 || r1 >= live) return;
+    const int64_t i = a.index[r1];
     const float log_sum = logf(s);
-    a.logp[i] = s == 0.0f ? log_sum : (a.label_logit[r] - top) * a.it - log_sum;
+    a.logp[i] = s == 0.0f ? log_sum : (a.label_logit[r1] - top) * a.it - log_sum;
     if (a.saved_out != nullptr) {
         a.saved_out[2 * i] = top;
         a.saved_out[2 * i + 1] = log_sum;
@@ -854,7 +860,7 @@ int32_t launch_logp(const HeadArgs& a, cudaStream_t stream) {
     if (pairs < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
     ZS_TRY((launch_product<T, kLogits>(ProductArgs{a, 0, a.vocab, 1}, rows, entries, pairs, stream)));
-    return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 32) / 32)), 512, stream, "head_join_kernel", a);
+    return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 32) / 32)), 1024, stream, "head_join_kernel", a);
 }
 
 template <typename T>

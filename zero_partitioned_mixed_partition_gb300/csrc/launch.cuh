@@ -1,6 +1,7 @@
 // launch.cuh -- launches of the head, norm and embedding kernels: with
 // programmatic serialization, so that every kernel waits by griddep_wait() before it
-// touches global memory.  Included inside an anonymous namespace.
+// touches global memory.  Included inside an anonymous namespace, cluster_counts.h
+// before it, outside.
 #pragma once
 
 template <typename... P, typename... A>
@@ -24,6 +25,31 @@ int32_t launch_shared(void (*kernel)(P...), dim3 grid, int threads, size_t share
 template <typename... P, typename... A>
 int32_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, const char* name, A... args) {
     return launch_shared(kernel, grid, threads, 0, stream, name, args...);
+}
+
+constexpr int kMaxShared = 200 * 1024;  // dynamic shared memory that these kernels ask for at most
+
+// The blocks of a grid that fill the current device, no more than there is work for; 0 and
+// the error recorded if that could not be found.
+unsigned grid_of(const void* kernel, int threads, size_t shared, int64_t work) {
+    static zs::ClusterCounts counts;
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    const int most = err != cudaSuccess ? 0 : counts.get(device, kernel, threads, (int)shared, [&] {
+        int per_sm = 0;
+        // (the limit is the kernel's, for calls of any size)
+        if (shared > 32 * 1024)  // (48 KB with what the kernel has statically need no asking)
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+        if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, shared);
+        if (err == cudaSuccess && per_sm < 1) err = cudaErrorInvalidConfiguration;
+        if (err != cudaSuccess) cudaGetLastError();
+        return err == cudaSuccess ? per_sm * zs::device_sm_count() : 0;
+    });
+    if (most < 1) {
+        zs::cuda_fail(err != cudaSuccess ? err : cudaErrorInvalidConfiguration, "grid_of");
+        return 0;
+    }
+    return (unsigned)(work < 1 ? 1 : work < most ? work : most);
 }
 
 #define ZS_TRY(call)                          \

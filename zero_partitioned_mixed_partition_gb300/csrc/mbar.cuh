@@ -18,11 +18,18 @@ __device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ void mbar_give(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
 }
-// Whether the phase of the given parity is over; waits up to 2 us for it.
+// Whether the phase of the given parity is over; waits up to 2 us for it.  CTA: what the
+// arrivals order is this CTA's own, or no ordinary memory at all (copies, tensor memory);
+// else the cluster's, for which the SM drops what its L1 holds.
+template <bool CTA = false>
 __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
     uint32_t done = 0;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(smem_addr(b)), "r"(parity), "r"(2000u) : "memory");
+    if (CTA)
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(smem_addr(b)), "r"(parity), "r"(2000u) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(smem_addr(b)), "r"(parity), "r"(2000u) : "memory");
     return done != 0;
 }
 // The tries of a wait: a second or two.
@@ -43,12 +50,12 @@ int32_t set_unit_wait_limit(int32_t tries) {
     return 0;
 #endif
 }
-template <bool RELAXED>
+template <bool RELAXED, bool CTA>
 __device__ __forceinline__ bool mbar_wait_on(uint64_t* b, uint32_t parity, int32_t* failed) {
     const int limit = wait_limit();
 #pragma unroll 1
     for (int i = 0; i < limit; ++i) {
-        if (mbar_try(b, parity)) return true;
+        if (mbar_try<CTA>(b, parity)) return true;
         if (*(volatile int32_t*)failed) return false;
         if (RELAXED) __nanosleep(100);
     }
@@ -60,12 +67,12 @@ __device__ __forceinline__ bool mbar_wait_on(uint64_t* b, uint32_t parity, int32
 // the warps that mostly wait; they leave the issue slots to the others.  (Most waits
 // are over at the first try; with that in the loop, 708 us for 684 in the largest
 // case of the logits kernels.)
-template <bool RELAXED = false>
+template <bool RELAXED = false, bool CTA = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, int32_t* failed) {
 #if ZS_CHECKED
-    if (wait_limit() == 0) return mbar_wait_on<RELAXED>(b, parity, failed);
+    if (wait_limit() == 0) return mbar_wait_on<RELAXED, CTA>(b, parity, failed);
 #endif
-    return mbar_try(b, parity) || mbar_wait_on<RELAXED>(b, parity, failed);
+    return mbar_try<CTA>(b, parity) || mbar_wait_on<RELAXED, CTA>(b, parity, failed);
 }
 // Whether every lane of the warp may go on.
 __device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(0xffffffffu, ok); }

@@ -3,6 +3,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "cluster_counts.h"
 #include "zs_internal.h"
 
 namespace {
@@ -126,35 +127,97 @@ __device__ __forceinline__ float sum_of(uint64_t p) {
     return a + b;
 }
 
+// --------------------------------------------------------------- rows ahead ---
+
+// A thread's vectors of the rows that its team takes next, copied ahead into shared
+// memory: `DEPTH` rows of `EACH` 16-byte vectors.  A thread reads only what it copied
+// itself, so nothing but its own copies has to be waited for.
+template <int EACH, int DEPTH>
+struct Ahead {
+    uint32_t base, stride;  // of the thread's first vector; from one vector to the next
+    __device__ __forceinline__ Ahead(const void* shared) {
+        stride = blockDim.x * 16;
+        base = (uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 16;
+    }
+    __device__ __forceinline__ uint32_t at(uint32_t row, int i) const { return base + ((row % DEPTH) * EACH + i) * stride; }
+    __device__ __forceinline__ void copy(uint32_t row, int i, const void* from) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(row, i)), "l"(from) : "memory");
+    }
+    __device__ __forceinline__ void done_row() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // Until all but the last DEPTH - 1 rows have come.
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
+    template <typename P>
+    __device__ __forceinline__ P get(uint32_t row, int i) const {
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at(row, i)) : "memory");
+        return *reinterpret_cast<P*>(&x);
+    }
+};
+// Rows ahead: as many as some 64 KB of a block of 256 threads hold.
+constexpr int depth_of(int each) { return each >= 8 ? 2 : each >= 4 ? 4 : 6; }
+constexpr size_t ahead_bytes(int each, int threads) { return (size_t)depth_of(each) * each * threads * 16; }
+
 template <typename T, int V, int C>
 __global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
-    constexpr int N = C * V, H = N / 2;
+    constexpr bool kRing = V * sizeof(T) == 16;
+    constexpr int D = depth_of(C);
+    extern __shared__ uint4 s_ahead[];
     const Team t = team_of(warps);
     const int32_t vectors = (int32_t)(a.width / V);
-    uint32_t turn = 0;
+    const int64_t step = (int64_t)gridDim.x * t.teams;
+    const Ahead<C, D> ahead(s_ahead);
+    int64_t r = (int64_t)blockIdx.x * t.teams + t.number, rc = r;
+    uint32_t turn = 0, row = 0, row_copied = 0;
     griddep_wait();
-    for (int64_t r = (int64_t)blockIdx.x * t.teams + t.number; r < a.rows; r += (int64_t)gridDim.x * t.teams) {
-        const Pack<T, V>* x = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
+    auto copy_row = [&]() {
+        if (rc < a.rows) {
+            const Pack<T, V>* x = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + rc * a.x_stride);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (t.thread + c * t.threads < vectors) ahead.copy(row_copied, c, x + t.thread + c * t.threads);
+        }
+        ahead.done_row();
+        rc += step;
+        ++row_copied;
+    };
+    if (kRing)
+        for (int i = 0; i < D - 1; ++i) copy_row();
+    for (; r < a.rows; r += step, ++row) {
         Pack<T, V>* y = reinterpret_cast<Pack<T, V>*>((T*)a.y + r * a.y_stride);
         Pack<T, V> raw[C];
+        if constexpr (kRing) {
+            copy_row();
+            ahead.wait();
+        }
+        const Pack<T, V>* x = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             raw[c] = Pack<T, V>{};
-            if (t.thread + c * t.threads < vectors) raw[c] = x[t.thread + c * t.threads];
+            if (t.thread + c * t.threads < vectors) {
+                if constexpr (kRing)
+                    raw[c] = ahead.template get<Pack<T, V>>(row, c);
+                else
+                    raw[c] = x[t.thread + c * t.threads];
+            }
         }
-        uint64_t v[H], s[2] = {0, 0};
-        pairs_of<T, V, C>(raw, v);
+        uint64_t s[2] = {0, 0};
+        constexpr int G = V == 1 ? C : V;  // elements taken together
 #pragma unroll
-        for (int i = 0; i < H; ++i) s[i & 1] = add2(s[i & 1], v[i]);
+        for (int c = 0; c < C * V / G; ++c) {
+            uint64_t part[G / 2];
+            pairs_of<T, V, G / V>(raw + c * (G / V), part);
+#pragma unroll
+            for (int i = 0; i < G / 2; ++i) s[i & 1] = add2(s[i & 1], part[i]);
+        }
         const float mean = team_sum(t, turn++, sum_of(add2(s[0], s[1])), 0.0f).x * a.inv_width;
         const uint64_t m2 = pair(-mean, -mean);
         s[0] = s[1] = 0;
         if constexpr (V == 1) {
-            uint64_t minus[H];
+            uint64_t minus[C / 2], v[C / 2];
             where_in<C>(t, vectors, -mean, minus);
             pairs_of<T, V, C>(raw, v);
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
+            for (int i = 0; i < C / 2; ++i) {
                 const uint64_t d = add2(v[i], minus[i]);
                 s[i & 1] = fma2(d, d, s[i & 1]);
             }
@@ -198,18 +261,40 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_
 }
 
 // The gradient in one pass over dy and x: a team keeps its columns' parts of dgamma and
-// dbeta in registers from row to row, and loads its next row before it sums up the
-// present one.  A block's teams add their parts up in shared memory, in their order; a
-// block leaves one row of parts.
+// dbeta in registers from row to row.  A block's teams add their parts up in shared
+// memory, in their order; a block leaves one row of parts.
 template <typename T, int V, int C, bool PARAMS>
 __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
-    constexpr int N = C * V, H = N / 2;
-    extern __shared__ float s_part[];  // [2][width], with several teams
+    constexpr bool kRing = V * sizeof(T) == 16;
+    constexpr int N = C * V, H = N / 2, D = depth_of(2 * C);
+    extern __shared__ uint4 s_ahead[];  // rows ahead; with several teams, [2][width] of parts after them
+    float* const s_part = reinterpret_cast<float*>(s_ahead + (kRing ? ahead_bytes(2 * C, blockDim.x) / 16 : 0));
     const Team t = team_of(warps);
     const int32_t vectors = (int32_t)(a.width / V);
     const int64_t step = (int64_t)gridDim.x * t.teams;
-    uint32_t turn = 0;
+    const Ahead<2 * C, D> ahead(s_ahead);
+    int64_t r = (int64_t)blockIdx.x * t.teams + t.number, rc = r;
+    uint32_t turn = 0, row = 0, row_copied = 0;
     griddep_wait();
+    auto copy_row = [&]() {
+        if (rc < a.rows) {
+            const Pack<T, V>* px = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + rc * a.x_stride);
+            const Pack<T, V>* pd = reinterpret_cast<const Pack<T, V>*>((const T*)a.dy + rc * a.dy_stride);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int32_t q = t.thread + c * t.threads;
+                if (q < vectors) {
+                    ahead.copy(row_copied, 2 * c, px + q);
+                    ahead.copy(row_copied, 2 * c + 1, pd + q);
+                }
+            }
+        }
+        ahead.done_row();
+        rc += step;
+        ++row_copied;
+    };
+    if (kRing)
+        for (int i = 0; i < D - 1; ++i) copy_row();
     uint64_t g[H], dg[H], db[H];
     {
         float f[N];
@@ -230,23 +315,35 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_con
     float mean = 0.0f, rstd = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c] = dy[c] = Pack<T, V>{};
-    auto load = [&](int64_t r) {
-        const Pack<T, V>* px = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
-        const Pack<T, V>* pd = reinterpret_cast<const Pack<T, V>*>((const T*)a.dy + r * a.dy_stride);
+    // (without the ring a row's vectors are loaded one row ahead, into registers)
+    auto load = [&](int64_t i) {
+        mean = a.saved[2 * i];
+        rstd = a.saved[2 * i + 1];
+        if constexpr (!kRing) {
+            const Pack<T, V>* px = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + i * a.x_stride);
+            const Pack<T, V>* pd = reinterpret_cast<const Pack<T, V>*>((const T*)a.dy + i * a.dy_stride);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int32_t q = t.thread + c * t.threads;
-            if (q < vectors) {
-                x[c] = px[q];
-                dy[c] = pd[q];
+            for (int c = 0; c < C; ++c) {
+                const int32_t q = t.thread + c * t.threads;
+                if (q < vectors) {
+                    x[c] = px[q];
+                    dy[c] = pd[q];
+                }
             }
         }
-        mean = a.saved[2 * r];
-        rstd = a.saved[2 * r + 1];
     };
-    int64_t r = (int64_t)blockIdx.x * t.teams + t.number;
     if (r < a.rows) load(r);
-    for (; r < a.rows; r += step) {
+    for (; r < a.rows; r += step, ++row) {
+        if constexpr (kRing) {
+            copy_row();
+            ahead.wait();
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (t.thread + c * t.threads < vectors) {
+                    x[c] = ahead.template get<Pack<T, V>>(row, 2 * c);
+                    dy[c] = ahead.template get<Pack<T, V>>(row, 2 * c + 1);
+                }
+        }
         uint64_t xh[H], e[H], s = 0, u = 0;
         const uint64_t r2 = pair(rstd, rstd), m2 = pair(-mean, -mean);
         pairs_of<T, V, C>(x, xh);
@@ -445,36 +542,27 @@ struct Matrix {
     int64_t second;
 };
 
-// Blocks of a grid that fill the device, and no more than there are rows for.
-template <typename K>
-unsigned grid_of(K kernel, int threads, size_t shared, int64_t blocks) {
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, shared) != cudaSuccess || per_sm < 1) {
-        cudaGetLastError();
-        per_sm = 1;
-    }
-    const int64_t most = (int64_t)per_sm * zs::device_sm_count();
-    return (unsigned)(blocks < most ? (blocks > 0 ? blocks : 1) : most);
-}
-
 template <typename T, int V, int C>
 int32_t launch_rows(const NormArgs& a, int warps, cudaStream_t stream) {
     const int threads = warps > kThreads / 32 ? 32 * warps : kThreads, teams = threads / (32 * warps);
-    const unsigned grid = grid_of(norm_rows_kernel<T, V, C>, threads, 0, (a.rows + teams - 1) / teams);
-    return launch(norm_rows_kernel<T, V, C>, dim3(grid), threads, stream, "norm_rows_kernel", a, warps);
+    const size_t shared = V * sizeof(T) == 16 ? ahead_bytes(C, threads) : 0;
+    const unsigned grid = grid_of((const void*)norm_rows_kernel<T, V, C>, threads, shared, (a.rows + teams - 1) / teams);
+    if (grid == 0) return ZS_ERR_CUDA;
+    return launch_shared(norm_rows_kernel<T, V, C>, dim3(grid), threads, shared, stream, "norm_rows_kernel", a, warps);
 }
 template <typename T>
 int32_t launch_forward(const NormArgs& a, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, a.beta, Matrix{a.x, a.x_stride}, Matrix{a.y, a.y_stride});
-    const Shape s = shape_of(a.width, wide ? V : 1, 8 * V);
+    const Shape s = shape_of(a.width, wide ? V : 1, 4 * V);
     if (s.c == 0) {
-        const unsigned grid = grid_of(norm_long_kernel<T>, kMaxThreads, 0, a.rows);
+        const unsigned grid = grid_of((const void*)norm_long_kernel<T>, kMaxThreads, 0, a.rows);
+        if (grid == 0) return ZS_ERR_CUDA;
         return launch(norm_long_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_kernel", a);
     }
     if (!wide) return s.c == 4 ? launch_rows<T, 1, 4>(a, s.warps, stream) : launch_rows<T, 1, 16>(a, s.warps, stream);
-    if (s.c <= 2) return launch_rows<T, V, 2>(a, s.warps, stream);
-    return s.c <= 4 ? launch_rows<T, V, 4>(a, s.warps, stream) : launch_rows<T, V, 8>(a, s.warps, stream);
+    if (s.c == 1) return launch_rows<T, V, 1>(a, s.warps, stream);
+    return s.c == 2 ? launch_rows<T, V, 2>(a, s.warps, stream) : launch_rows<T, V, 4>(a, s.warps, stream);
 }
 
 int32_t launch_params(const NormArgs& a, int64_t groups, cudaStream_t stream) {
@@ -484,9 +572,10 @@ template <typename T, int V, int C>
 int32_t launch_grad_rows(const NormArgs& a, int warps, cudaStream_t stream) {
     const bool params = a.dgamma != nullptr || a.dbeta != nullptr;
     const int threads = warps > kThreads / 32 ? 32 * warps : kThreads, teams = threads / (32 * warps);
-    const size_t shared = params && teams > 1 ? 8 * (size_t)a.width : 0;
+    const size_t shared = (V * sizeof(T) == 16 ? ahead_bytes(2 * C, threads) : 0) + (params && teams > 1 ? 8 * (size_t)a.width : 0);
     auto go = [&](auto kernel) {
-        unsigned grid = grid_of(kernel, threads, shared, (a.rows + teams - 1) / teams);
+        unsigned grid = grid_of((const void*)kernel, threads, shared, (a.rows + teams - 1) / teams);
+        if (grid == 0) return (int32_t)ZS_ERR_CUDA;
         if (grid > kMaxGroups) grid = kMaxGroups;
         const int32_t rc = launch_shared(kernel, dim3(grid), threads, shared, stream, "norm_grad_kernel", a, warps);
         return rc != ZS_OK || !params ? rc : launch_params(a, grid, stream);
@@ -509,7 +598,8 @@ int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
             ZS_TRY(launch_params(a, groups, stream));
         }
         if (a.dx == nullptr) return ZS_OK;
-        const unsigned grid = grid_of(norm_long_dx_kernel<T>, kMaxThreads, 0, a.rows);
+        const unsigned grid = grid_of((const void*)norm_long_dx_kernel<T>, kMaxThreads, 0, a.rows);
+        if (grid == 0) return ZS_ERR_CUDA;
         return launch(norm_long_dx_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_dx_kernel", a);
     }
     if (!wide) return s.c == 4 ? launch_grad_rows<T, 1, 4>(a, s.warps, stream) : launch_grad_rows<T, 1, 16>(a, s.warps, stream);

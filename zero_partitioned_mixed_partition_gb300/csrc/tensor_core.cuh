@@ -23,8 +23,11 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     return a;
 }
+// Arrives at a barrier of the pair after loads from tensor memory, which the fences of
+// tensor memory order.  (A release to the cluster would wait for the warp's stores to
+// global memory besides.)
 __device__ __forceinline__ void arrive_at(uint32_t barrier) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(barrier) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(barrier) : "memory");
 }
 __device__ __forceinline__ int32_t load_from_peer(const int32_t* p, uint32_t rank) {
     int32_t v;
