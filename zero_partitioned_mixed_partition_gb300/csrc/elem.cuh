@@ -31,34 +31,52 @@ template <> __device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t w) 
 }
 
 // V values of a type, as accesses of up to 16 bytes (V = 1: an element).
-template <typename T, int V> struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Pack {
-    T v[V];
+template <int BYTES> struct RawOf;
+template <> struct RawOf<2> { using type = uint16_t; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<16> { using type = uint4; };
+struct alignas(16) Raw32 {
+    uint4 a, b;
+};
+template <> struct RawOf<32> { using type = Raw32; };
+template <typename T, int V> struct Pack {
+    typename RawOf<V * sizeof(T)>::type raw;
 };
 template <typename T, int V>
-__device__ __forceinline__ void unpack(const Pack<T, V>& p, float* x) {
-    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float2 f = widen2<T>(w[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+__device__ __forceinline__ void unpack(Pack<T, V> p, float* x) {  // (by value: one load where p is in memory)
+    if constexpr (V == 1 && sizeof(T) == 2) {
+        x[0] = to_float<T>(*reinterpret_cast<const T*>(&p.raw));
     } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&p.raw);
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = to_float<T>(p.v[i]);
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 f = widen2<T>(w[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = __uint_as_float(w[i]);
+        }
     }
 }
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> pack(const float* x) {
     Pack<T, V> p;
-    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&p);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) w[i] = narrow2<T>(x[2 * i], x[2 * i + 1]);
+    if constexpr (V == 1 && sizeof(T) == 2) {
+        const T t = from_float<T>(x[0]);
+        p.raw = *reinterpret_cast<const uint16_t*>(&t);
     } else {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&p.raw);
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) p.v[i] = from_float<T>(x[i]);
+            for (int i = 0; i < V / 2; ++i) w[i] = narrow2<T>(x[2 * i], x[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(x[i]);
+        }
     }
     return p;
 }

@@ -43,6 +43,8 @@ struct EmbedArgs {
     int32_t passes, bits;  // of the sort, and of a pass
     float* part;           // sums of runs that go across chunks: two rows to a chunk
     int32_t chunk;         // tokens of a chunk
+    uint32_t* arrived;     // of the chunks that a run goes across, by the one it starts in and columns
+    int64_t arrivals;      // how many of those counts
 };
 
 // ------------------------------------------------------------------- lookup ---
@@ -53,7 +55,7 @@ constexpr int kThreads = 256;
 template <typename T, int V>
 __device__ __forceinline__ void store_stream(Pack<T, V>* to, const Pack<T, V>& x) {
     if constexpr (sizeof(x) == 16)
-        __stcs(reinterpret_cast<uint4*>(to), *reinterpret_cast<const uint4*>(&x));
+        __stcs(&to->raw, x.raw);
     else
         *to = x;
 }
@@ -64,12 +66,8 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
     const int threads = 32 * warps, teams = kThreads / threads, thread = threadIdx.x % threads;
     const int64_t vectors = a.width / V;
     griddep_wait();
-    const int64_t step = (int64_t)gridDim.x * teams;
-    int64_t i = (int64_t)blockIdx.x * teams + threadIdx.x / threads;
-    int64_t next = i < a.tokens ? a.ids[i] : 0;
-    for (; i < a.tokens; i += step) {
-        const int64_t v = next;
-        if (i + step < a.tokens) next = a.ids[i + step];  // (ahead: a row's load waits for its id)
+    for (int64_t i = (int64_t)blockIdx.x * teams + threadIdx.x / threads; i < a.tokens; i += (int64_t)gridDim.x * teams) {
+        const int64_t v = a.ids[i];
         const bool inside = v >= 0 && v < a.vocab;
         const Pack<T, V>* row = reinterpret_cast<const Pack<T, V>*>((const T*)a.table + (inside ? v : 0) * a.table_stride);
         Pack<T, V>* out = reinterpret_cast<Pack<T, V>*>((T*)a.out + i * a.out_stride);
@@ -153,6 +151,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
         }
         return;
     }
+    for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < a.arrivals; i += kSortCtas * kSortThreads)
+        a.arrived[i] = 0u;
     const uint32_t rank = cluster_rank();
     const int64_t me = (int64_t)rank * kSortWarps + warp, warps = kSortCtas * kSortWarps;
     const int64_t from = a.tokens * me / warps, to = a.tokens * (me + 1) / warps;
@@ -282,6 +282,78 @@ __device__ __forceinline__ Pack<float, V>* part_at(const EmbedArgs& a, int64_t c
     return reinterpret_cast<Pack<float, V>*>(a.part + (2 * chunk + (start ? 1 : 0)) * a.width + k);
 }
 
+template <int V>
+__device__ __forceinline__ Pack<float, V> load_part(const Pack<float, V>* p) {  // (written by other blocks: from L2)
+    Pack<float, V> x;
+    if constexpr (V == 8) {
+        x.raw.a = __ldcg(&p->raw.a);
+        x.raw.b = __ldcg(&p->raw.b);
+    } else {
+        x.raw = __ldcg(&p->raw);
+    }
+    return x;
+}
+// Adds up a run that goes across chunks once all of them have left their part: the block
+// that comes last does, in the chunks' order.  Called by the whole block.
+template <typename G, int V>
+__device__ __noinline__ void join_run(const EmbedArgs& a, int64_t chunks, int32_t columns, int64_t c, uint32_t key, bool started_before,
+                         int32_t column, int64_t q) {
+    __shared__ int64_t s_first, s_last;
+    __shared__ bool s_done;
+    const int64_t vectors = a.width / V;
+    __threadfence();  // (the block's part, before it is counted)
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        auto key_at = [&](int64_t j) { return a.keys[j * a.chunk]; };
+        int64_t first = c, last = c;  // chunks whose first token has the key, 32 at a time; and the one it starts in
+        if (started_before) {
+            for (bool more = true; more;) {
+                const int64_t j = first - 1 - lane;
+                const uint32_t votes = __ballot_sync(0xffffffffu, j >= 0 && key_at(j < 0 ? 0 : j) == key);
+                first -= votes == 0xffffffffu ? 32 : __ffs(~votes) - 1;
+                more = votes == 0xffffffffu;
+            }
+            if (first > 0 && a.keys[first * a.chunk - 1] == key) --first;
+        }
+        for (bool more = true; more;) {
+            const int64_t j = last + 1 + lane;
+            const uint32_t votes = __ballot_sync(0xffffffffu, j < chunks && key_at(j < chunks ? j : 0) == key);
+            last += votes == 0xffffffffu ? 32 : __ffs(~votes) - 1;
+            more = votes == 0xffffffffu;
+        }
+        if (lane == 0) {
+            s_first = first;
+            s_last = last;
+            s_done = atomicAdd(a.arrived + first * columns + column, 1u) == (uint32_t)(last - first);
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    const int64_t first = s_first, last = s_last;
+    const bool done = s_done;
+    __syncthreads();  // (the places may be written again)
+    if (!done || q >= vectors) return;
+    const int64_t k = q * V;
+    float sum[V];
+    unpack<float, V>(load_part<V>(part_at<V>(a, first, true, k)), sum);
+    for (int64_t j = first + 1; j <= last; j += 4) {
+        Pack<float, V> x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u <= last) x[u] = load_part<V>(part_at<V>(a, j + u, false, k));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (j + u > last) break;
+            float f[V];
+            unpack<float, V>(x[u], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] += f[i];
+        }
+    }
+    add_to_table<G, V>(a, key, k, sum);
+}
+
 // A block takes a chunk of the sorted list and up to blockDim.x vectors of the width, eight
 // tokens' vectors under way at once.
 template <typename T, typename G, int V>
@@ -289,11 +361,11 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
     __shared__ uint32_t s_key[kMaxChunk + 2], s_place[kMaxChunk];
     const int64_t vectors = a.width / V;
     constexpr uint32_t kNone = 0xffffffffu;
-    griddep_launch_dependents();
     griddep_wait();
     for (int64_t work = blockIdx.x; work < chunks * columns; work += gridDim.x) {
-        const int64_t c = work / columns, q = (work % columns) * blockDim.x + threadIdx.x;
-        const int64_t first = c * a.chunk;
+        const int64_t c = work / columns;
+        const int32_t column = (int32_t)(work - c * columns);
+        const int64_t q = (int64_t)column * blockDim.x + threadIdx.x, first = c * a.chunk;
         const int32_t n = a.tokens - first < a.chunk ? (int32_t)(a.tokens - first) : a.chunk;
         __syncthreads();
         for (int t = threadIdx.x; t < n + 2; t += blockDim.x) {
@@ -302,82 +374,48 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
             if (t < n) s_place[t] = a.places[first + t];
         }
         __syncthreads();
-        if (q >= vectors) continue;
-        const int64_t k = q * V;
-        const T* const rows = (const T*)a.dout + k;
-        float sum[V];
+        if (q < vectors) {
+            const int64_t k = q * V;
+            const T* const rows = (const T*)a.dout + k;
+            float sum[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-        bool from_before = s_key[0] == s_key[1];
-        for (int t0 = 0; t0 < n; t0 += 8) {
-            Pack<T, V> x[8];
+            for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+            bool from_before = s_key[0] == s_key[1];
+            for (int t0 = 0; t0 < n; t0 += 8) {
+                Pack<T, V> x[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (t0 + u < n && s_key[t0 + u + 1] < (uint32_t)a.vocab)
-                    x[u] = *reinterpret_cast<const Pack<T, V>*>(rows + (int64_t)s_place[t0 + u] * a.dout_stride);
+                for (int u = 0; u < 8; ++u)
+                    if (t0 + u < n && s_key[t0 + u + 1] < (uint32_t)a.vocab)
+                        x[u] = *reinterpret_cast<const Pack<T, V>*>(rows + (int64_t)s_place[t0 + u] * a.dout_stride);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int t = t0 + u;
-                if (t >= n) break;
-                const uint32_t key = s_key[t + 1];
-                if (key >= (uint32_t)a.vocab) break;
-                float f[V];
-                unpack<T, V>(x[u], f);
+                for (int u = 0; u < 8; ++u) {
+                    const int t = t0 + u;
+                    if (t >= n) break;
+                    const uint32_t key = s_key[t + 1];
+                    if (key >= (uint32_t)a.vocab) break;
+                    float f[V];
+                    unpack<T, V>(x[u], f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] += f[i];
-                const bool more = s_key[t + 2] == key;
-                if (more && t + 1 < n) continue;
-                // the run's end, here or at the chunk's
-                if (from_before || more) {
-                    *part_at<V>(a, c, !from_before, k) = pack<float, V>(sum);
-                } else {
-                    add_to_table<G, V>(a, key, k, sum);
+                    for (int i = 0; i < V; ++i) sum[i] += f[i];
+                    const bool more = s_key[t + 2] == key;
+                    if (more && t + 1 < n) continue;
+                    // the run's end, here or at the chunk's
+                    if (from_before || more)
+                        *part_at<V>(a, c, !from_before, k) = pack<float, V>(sum);
+                    else
+                        add_to_table<G, V>(a, key, k, sum);
+                    from_before = false;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[i] = 0.0f;
                 }
-                from_before = false;
-#pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] = 0.0f;
             }
         }
-    }
-}
-
-// Joins the runs that start in a chunk and go on in the next: their parts in the
-// chunks' order.
-template <typename G, int V>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedArgs a, int64_t chunks, int32_t columns) {
-    const int64_t vectors = a.width / V;
-    griddep_wait();
-    for (int64_t work = blockIdx.x; work < (chunks - 1) * columns; work += gridDim.x) {
-        const int64_t c = work / columns, q = (work % columns) * blockDim.x + threadIdx.x;
-        const int64_t first = c * a.chunk, end = first + a.chunk;
-        const uint32_t key = a.keys[end - 1];
-        if (a.keys[end] != key || key >= (uint32_t)a.vocab) continue;             // goes on, and
-        if (a.keys[first] == key && first > 0 && a.keys[first - 1] == key) continue;  // starts here
-        // the last chunk it goes on to: the last of those whose first token has the key
-        int64_t last = c + 1;
-        for (bool more = true; more;) {
-            const int64_t j = last + 1 + threadIdx.x % 32;
-            const uint32_t votes = __ballot_sync(0xffffffffu, j < chunks && a.keys[j * a.chunk] == key);
-            last += votes == 0xffffffffu ? 32 : __ffs(~votes) - 1;
-            more = votes == 0xffffffffu;
-        }
-        if (q >= vectors) continue;
-        const int64_t k = q * V;
-        float sum[V];
-        unpack<float, V>(*part_at<V>(a, c, true, k), sum);
-        for (int64_t j = c + 1; j <= last; j += 8) {
-            Pack<float, V> x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (j + u <= last) x[u] = *part_at<V>(a, j + u, false, k);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (j + u > last) break;
-#pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] += x[u].v[i];
-            }
-        }
-        add_to_table<G, V>(a, key, k, sum);
+        // runs that go across chunks: the one from before, and one that starts here and goes on
+        const uint32_t head = s_key[1], tail = s_key[n];
+        const bool from_before = s_key[0] == head && head < (uint32_t)a.vocab;
+        const bool goes_on = s_key[n + 1] == tail && tail < (uint32_t)a.vocab && !(from_before && head == tail);
+        if (from_before) join_run<G, V>(a, chunks, columns, c, head, true, column, q);
+        if (goes_on) join_run<G, V>(a, chunks, columns, c, tail, false, column, q);
     }
 }
 
@@ -388,7 +426,7 @@ int32_t chunk_of(int64_t tokens) { return tokens >= 65536 ? 64 : tokens >= 32768
 
 // The parts of the scratch buffer, as offsets.
 struct Plan {
-    int64_t list[4], part, chunks, total;
+    int64_t list[4], part, arrived, arrivals, chunks, total;
 };
 Plan plan_of(int64_t tokens, int64_t width) {
     Plan p;
@@ -402,6 +440,8 @@ Plan plan_of(int64_t tokens, int64_t width) {
     const int32_t chunk = chunk_of(tokens);
     p.chunks = (tokens + chunk - 1) / chunk;
     p.part = take(8 * p.chunks * width);
+    p.arrivals = p.chunks * ((width + kThreads - 1) / kThreads);
+    p.arrived = take(4 * p.arrivals);
     p.total = at > 0 ? at : 128;
     return p;
 }
@@ -417,9 +457,8 @@ int32_t launch_lookup(const EmbedArgs& a, cudaStream_t stream) {
     int warps = 1;
     while (warps < kThreads / 32 && vectors > 128ll * warps) warps *= 2;
     const int teams = kThreads / (32 * warps);
-    const unsigned grid = grid_of((const void*)embed_kernel<T, V>, kThreads, 0, (a.tokens + teams - 1) / teams);
-    if (grid == 0) return ZS_ERR_CUDA;
-    return launch(embed_kernel<T, V>, dim3(grid), kThreads, stream, "embed_kernel", a, warps);
+    const int64_t blocks = (a.tokens + teams - 1) / teams, most = 1 << 24;
+    return launch(embed_kernel<T, V>, dim3((unsigned)(blocks < most ? blocks : most)), kThreads, stream, "embed_kernel", a, warps);
 }
 
 template <typename T, typename G, int V>
@@ -435,12 +474,10 @@ int32_t launch_grad(const EmbedArgs& a, int64_t chunks, cudaStream_t stream) {
     const int64_t vectors = a.width / V;
     const int threads = vectors < kThreads ? (int)((vectors + 31) / 32 * 32) : kThreads;
     const int32_t columns = (int32_t)((vectors + threads - 1) / threads);
-    const unsigned grid = grid_of((const void*)embed_sum_kernel<T, G, V>, threads, 0, chunks * columns);
-    const unsigned joins = grid_of((const void*)embed_join_kernel<G, V>, threads, 0, (chunks - 1) * columns);
-    if (grid == 0 || joins == 0) return ZS_ERR_CUDA;
-    ZS_TRY(launch(embed_sum_kernel<T, G, V>, dim3(grid), threads, stream, "embed_sum_kernel", a, chunks, columns));
-    if (chunks == 1) return ZS_OK;
-    return launch(embed_join_kernel<G, V>, dim3(joins), threads, stream, "embed_join_kernel", a, chunks, columns);
+    // (a block to a chunk, as they come: chunks differ in their stores)
+    const int64_t blocks = chunks * columns, limit = 1 << 24;
+    return launch(embed_sum_kernel<T, G, V>, dim3((unsigned)(blocks < limit ? blocks : limit)), threads, stream, "embed_sum_kernel",
+                  a, chunks, columns);
 }
 
 bool valid_stride(int64_t rows, int64_t width, int64_t stride) {
@@ -523,6 +560,8 @@ ZS_API int32_t zero_embed_grad_async(const zs_embed* e, const void* dout, int64_
     for (int i = 0; i < 4; ++i) *lists[i] = (uint32_t*)((char*)work_dev + p.list[i]);
     a.part = (float*)((char*)work_dev + p.part);
     a.chunk = chunk_of(e->tokens);
+    a.arrived = (uint32_t*)((char*)work_dev + p.arrived);
+    a.arrivals = p.arrivals;
     int32_t bits = 1;  // of the largest key, `vocab`
     while (e->vocab >> bits != 0) ++bits;
     a.passes = (bits + kMaxBits - 1) / kMaxBits;

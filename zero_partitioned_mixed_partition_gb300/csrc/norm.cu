@@ -3,6 +3,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cluster_counts.h"
 #include "zs_internal.h"
 
@@ -31,23 +33,24 @@ struct NormArgs {
 
 // ------------------------------------------------------------- parameters ---
 
-// V values of gamma or beta from k on (`missing` without one).  Their type is a run-time
-// choice: one branch, the same for all threads, for a load from L1.
-template <int V>
-__device__ __forceinline__ void params_at(const void* p, int32_t type, int64_t k, float missing, float* out) {
+// V values of gamma or beta from k on (`missing` without one).
+template <typename P, int V>
+__device__ __forceinline__ void params_at(const void* p, int64_t k, float missing, float* out) {
     if (p == nullptr) {
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = missing;
-    } else if (type == ZS_F32) {
-        constexpr int N = V < 4 ? V : 4;
-#pragma unroll
-        for (int i = 0; i < V; i += N)
-            unpack<float, N>(*reinterpret_cast<const Pack<float, N>*>((const float*)p + k + i), out + i);
-    } else if (type == ZS_F16) {
-        unpack<__half, V>(*reinterpret_cast<const Pack<__half, V>*>((const __half*)p + k), out);
     } else {
-        unpack<__nv_bfloat16, V>(*reinterpret_cast<const Pack<__nv_bfloat16, V>*>((const __nv_bfloat16*)p + k), out);
+        unpack<P, V>(*reinterpret_cast<const Pack<P, V>*>((const P*)p + k), out);
     }
+}
+template <int V>
+__device__ __forceinline__ void params_at(const void* p, int32_t type, int64_t k, float missing, float* out) {
+    if (type == ZS_F32)
+        params_at<float, V>(p, k, missing, out);
+    else if (type == ZS_F16)
+        params_at<__half, V>(p, k, missing, out);
+    else
+        params_at<__nv_bfloat16, V>(p, k, missing, out);
 }
 __device__ __forceinline__ void store_param(void* p, int32_t type, int64_t k, float x) {
     if (type == ZS_F32)
@@ -65,39 +68,53 @@ __device__ __forceinline__ void store_param(void* p, int32_t type, int64_t k, fl
 // once and the variance is of differences from the mean.  A block has threads / (32 warps) teams.
 constexpr int kThreads = 256, kMaxThreads = 512;
 
-struct Team {
-    int warps, number, teams, thread, threads;  // thread: of the team
-};
-__device__ __forceinline__ Team team_of(int warps) {
-    Team t;
-    t.warps = warps;
-    t.threads = 32 * warps;
-    t.number = threadIdx.x / t.threads;
-    t.teams = blockDim.x / t.threads;
-    t.thread = threadIdx.x % t.threads;
-    return t;
-}
-// The sums of x and y over the team, in every thread.  `turn` numbers the team's
-// calls: two places in turn, so that one barrier is enough (who writes a place again has
-// passed the barrier between, which its readers reach after reading).
-__device__ __forceinline__ float2 team_sum(const Team& t, uint32_t turn, float x, float y) {
-    __shared__ float2 s[2][kMaxThreads / 32];
+template <int WARPS> struct Team {
+    static constexpr int kTeamThreads = 32 * WARPS;
+    static constexpr int kBlock = kTeamThreads > kThreads ? kTeamThreads : kThreads;
+    static constexpr int kTeams = kBlock / kTeamThreads;
+    int number, thread;  // the team of the block, the thread of the team
+    uint32_t turn = 0;   // which of the places is next
+    __device__ __forceinline__ Team() : number(threadIdx.x / kTeamThreads), thread(threadIdx.x % kTeamThreads) {}
+    __device__ __forceinline__ void barrier() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(number + 1), "n"(kTeamThreads) : "memory");
+    }
+    // The sums over the team, in every thread.  Two places in turn, so that one barrier is
+    // enough: who writes a place again has passed the barrier between, which its readers
+    // reach after reading.  Every warp adds the warps' sums up anew, in one order.
+    __device__ __forceinline__ float sum(float x) {
+        __shared__ float s[2][kMaxThreads / 32];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-        y += __shfl_xor_sync(0xffffffffu, y, o);
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if constexpr (WARPS > 1) {
+            const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+            if (lane == 0) s[turn][warp] = x;
+            barrier();
+            x = s[turn][number * WARPS + lane % WARPS];
+            turn ^= 1;
+#pragma unroll
+            for (int o = WARPS / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        }
+        return x;
     }
-    if (t.warps == 1) return make_float2(x, y);
-    float2* const place = s[turn & 1] + t.number * t.warps;
-    if (t.thread % 32 == 0) place[t.thread / 32] = make_float2(x, y);
-    asm volatile("bar.sync %0, %1;" ::"r"(t.number + 1), "r"(t.threads) : "memory");
-    x = y = 0.0f;
-    for (int w = 0; w < t.warps; ++w) {
-        x += place[w].x;
-        y += place[w].y;
+    // Of two numbers: the warp's halves take one each, for half the exchanges.
+    __device__ __forceinline__ float2 sum(float x, float y) {
+        __shared__ float s[2][2][kMaxThreads / 32];
+        const int lane = threadIdx.x % 32, half = lane / 16;
+        float v = (half ? y : x) + __shfl_xor_sync(0xffffffffu, half ? x : y, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if constexpr (WARPS > 1) {
+            if (lane % 16 == 0) s[turn][half][threadIdx.x / 32] = v;
+            barrier();
+            v = s[turn][half][number * WARPS + lane % WARPS];
+            turn ^= 1;
+#pragma unroll
+            for (int o = WARPS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        }
+        const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+        return half ? make_float2(w, v) : make_float2(v, w);
     }
-    return make_float2(x, y);
-}
+};
 
 // The C vectors of a thread as C V / 2 pairs (with V = 1 of two vectors each).
 template <typename T, int V, int C>
@@ -113,14 +130,6 @@ __device__ __forceinline__ void split_all(const uint64_t* p, float* f) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) split(p[i], f[2 * i], f[2 * i + 1]);
 }
-// For elements one by one: a value for those of the thread's that are in the row, 0 for
-// the others.
-template <int C>
-__device__ __forceinline__ void where_in(const Team& t, int32_t width, float value, uint64_t* p) {
-#pragma unroll
-    for (int i = 0; i < C / 2; ++i)
-        p[i] = pair(t.thread + 2 * i * t.threads < width ? value : 0.0f, t.thread + (2 * i + 1) * t.threads < width ? value : 0.0f);
-}
 __device__ __forceinline__ float sum_of(uint64_t p) {
     float a, b;
     split(p, a, b);
@@ -130,76 +139,87 @@ __device__ __forceinline__ float sum_of(uint64_t p) {
 // --------------------------------------------------------------- rows ahead ---
 
 // A thread's vectors of the rows that its team takes next, copied ahead into shared
-// memory: `DEPTH` rows of `EACH` 16-byte vectors.  A thread reads only what it copied
-// itself, so nothing but its own copies has to be waited for.
-template <int EACH, int DEPTH>
+// memory: DEPTH rows of EACH 16-byte vectors.  A thread reads only what it copied itself,
+// so nothing but its own copies has to be waited for.
+template <int EACH, int DEPTH, int THREADS>
 struct Ahead {
-    uint32_t base, stride;  // of the thread's first vector; from one vector to the next
+    static constexpr uint32_t stride = THREADS * 16, row_bytes = EACH * stride;
+    uint32_t base, in, out;  // in, out: the rows copied and read next
     __device__ __forceinline__ Ahead(const void* shared) {
-        stride = blockDim.x * 16;
-        base = (uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 16;
+        base = in = out = (uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * 16;
     }
-    __device__ __forceinline__ uint32_t at(uint32_t row, int i) const { return base + ((row % DEPTH) * EACH + i) * stride; }
-    __device__ __forceinline__ void copy(uint32_t row, int i, const void* from) const {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(row, i)), "l"(from) : "memory");
+    __device__ __forceinline__ void copy(int i, const void* from) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(in + i * stride), "l"(from) : "memory");
     }
-    __device__ __forceinline__ void done_row() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    __device__ __forceinline__ uint32_t next(uint32_t at) const {
+        return at == base + (DEPTH - 1) * row_bytes ? base : at + row_bytes;
+    }
+    __device__ __forceinline__ void copied() {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in = next(in);
+    }
     // Until all but the last DEPTH - 1 rows have come.
     __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
-    template <typename P>
-    __device__ __forceinline__ P get(uint32_t row, int i) const {
+    __device__ __forceinline__ uint4 get(int i) const {
         uint4 x;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at(row, i)) : "memory");
-        return *reinterpret_cast<P*>(&x);
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(out + i * stride) : "memory");
+        return x;
     }
+    __device__ __forceinline__ void read() { out = next(out); }
 };
 // Rows ahead: as many as some 64 KB of a block of 256 threads hold.
 constexpr int depth_of(int each) { return each >= 8 ? 2 : each >= 4 ? 4 : 6; }
 constexpr size_t ahead_bytes(int each, int threads) { return (size_t)depth_of(each) * each * threads * 16; }
 
-template <typename T, int V, int C>
-__global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
+template <typename T, typename P, int V, int C, int WARPS>
+__global__ void __launch_bounds__(Team<WARPS>::kBlock, 1024 / Team<WARPS>::kBlock) norm_rows_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kRing = V * sizeof(T) == 16;
-    constexpr int D = depth_of(C);
     extern __shared__ uint4 s_ahead[];
-    const Team t = team_of(warps);
+    Team<WARPS> t;
+    constexpr int kTeam = Team<WARPS>::kTeamThreads;
     const int32_t vectors = (int32_t)(a.width / V);
-    const int64_t step = (int64_t)gridDim.x * t.teams;
-    const Ahead<C, D> ahead(s_ahead);
-    int64_t r = (int64_t)blockIdx.x * t.teams + t.number, rc = r;
-    uint32_t turn = 0, row = 0, row_copied = 0;
+    const int64_t step = (int64_t)gridDim.x * Team<WARPS>::kTeams;
+    Ahead<C, depth_of(C), Team<WARPS>::kBlock> ahead(s_ahead);
+    int64_t r = (int64_t)blockIdx.x * Team<WARPS>::kTeams + t.number, rc = r;
+    bool in[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) in[c] = t.thread + c * kTeam < vectors;
+    const int64_t x_step = step * a.x_stride, y_step = step * a.y_stride;
+    const T* x = (const T*)a.x + r * a.x_stride + t.thread * V;  // of the row to copy (to load) next
+    T* y = (T*)a.y + r * a.y_stride + t.thread * V;
     griddep_wait();
     auto copy_row = [&]() {
         if (rc < a.rows) {
-            const Pack<T, V>* x = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + rc * a.x_stride);
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                if (t.thread + c * t.threads < vectors) ahead.copy(row_copied, c, x + t.thread + c * t.threads);
+                if (in[c]) ahead.copy(c, x + c * kTeam * V);
         }
-        ahead.done_row();
+        ahead.copied();
         rc += step;
-        ++row_copied;
+        x += x_step;
     };
     if (kRing)
-        for (int i = 0; i < D - 1; ++i) copy_row();
-    for (; r < a.rows; r += step, ++row) {
-        Pack<T, V>* y = reinterpret_cast<Pack<T, V>*>((T*)a.y + r * a.y_stride);
+        for (int i = 0; i < depth_of(C) - 1; ++i) copy_row();
+    for (; r < a.rows; r += step, y += y_step) {
         Pack<T, V> raw[C];
         if constexpr (kRing) {
             copy_row();
             ahead.wait();
         }
-        const Pack<T, V>* x = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + r * a.x_stride);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             raw[c] = Pack<T, V>{};
-            if (t.thread + c * t.threads < vectors) {
+            if (in[c]) {
                 if constexpr (kRing)
-                    raw[c] = ahead.template get<Pack<T, V>>(row, c);
+                    raw[c].raw = ahead.get(c);
                 else
-                    raw[c] = x[t.thread + c * t.threads];
+                    raw[c] = *reinterpret_cast<const Pack<T, V>*>(x + c * kTeam * V);
             }
         }
+        if constexpr (kRing)
+            ahead.read();
+        else
+            x += x_step;
         uint64_t s[2] = {0, 0};
         constexpr int G = V == 1 ? C : V;  // elements taken together
 #pragma unroll
@@ -209,22 +229,21 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_
 #pragma unroll
             for (int i = 0; i < G / 2; ++i) s[i & 1] = add2(s[i & 1], part[i]);
         }
-        const float mean = team_sum(t, turn++, sum_of(add2(s[0], s[1])), 0.0f).x * a.inv_width;
+        const float mean = t.sum(sum_of(add2(s[0], s[1]))) * a.inv_width;
         const uint64_t m2 = pair(-mean, -mean);
         s[0] = s[1] = 0;
         if constexpr (V == 1) {
-            uint64_t minus[C / 2], v[C / 2];
-            where_in<C>(t, vectors, -mean, minus);
+            uint64_t v[C / 2];
             pairs_of<T, V, C>(raw, v);
 #pragma unroll
             for (int i = 0; i < C / 2; ++i) {
-                const uint64_t d = add2(v[i], minus[i]);
+                const uint64_t d = add2(v[i], pair(in[2 * i] ? -mean : 0.0f, in[2 * i + 1] ? -mean : 0.0f));
                 s[i & 1] = fma2(d, d, s[i & 1]);
             }
         } else {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                if (t.thread + c * t.threads >= vectors) break;
+                if (!in[c]) continue;
                 uint64_t part[V / 2];
                 pairs_of<T, V, 1>(raw + c, part);
 #pragma unroll
@@ -234,16 +253,17 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_
                 }
             }
         }
-        const float rstd = 1.0f / sqrtf(team_sum(t, turn++, sum_of(add2(s[0], s[1])), 0.0f).x * a.inv_width + a.eps);
+        // (the hardware's reciprocal root is off by some 2^-22.9 of itself)
+        const float rstd = rsqrtf(fmaf(t.sum(sum_of(add2(s[0], s[1]))), a.inv_width, a.eps));
         const uint64_t r2 = pair(rstd, rstd);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int32_t q = t.thread + c * t.threads;
-            if (q >= vectors) break;
+            if (!in[c]) continue;
+            const int32_t k = (t.thread + c * kTeam) * V;
             float f[V], g[V], b[V];
             unpack<T, V>(raw[c], f);
-            params_at<V>(a.gamma, a.param_type, (int64_t)q * V, 1.0f, g);
-            params_at<V>(a.beta, a.param_type, (int64_t)q * V, 0.0f, b);
+            params_at<P, V>(a.gamma, k, 1.0f, g);
+            params_at<P, V>(a.beta, k, 0.0f, b);
             if constexpr (V == 1) {
                 f[0] = fmaf((f[0] - mean) * rstd, g[0], b[0]);
             } else {
@@ -251,7 +271,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_
                 for (int i = 0; i < V; i += 2)
                     split(fma2(mul2(add2(pair(f[i], f[i + 1]), m2), r2), pair(g[i], g[i + 1]), pair(b[i], b[i + 1])), f[i], f[i + 1]);
             }
-            if (ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) y[q] = pack<T, V>(f);
+            if (ZS_RANGE_OK(kSiteNormRow, k, V, a.width))
+                *reinterpret_cast<Pack<T, V>*>(y + c * kTeam * V) = pack<T, V>(f);
         }
         if (t.thread == 0 && a.saved_out != nullptr) {
             a.saved_out[2 * r] = mean;
@@ -263,47 +284,51 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_rows_kernel(const __grid_
 // The gradient in one pass over dy and x: a team keeps its columns' parts of dgamma and
 // dbeta in registers from row to row.  A block's teams add their parts up in shared
 // memory, in their order; a block leaves one row of parts.
-template <typename T, int V, int C, bool PARAMS>
-__global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_constant__ NormArgs a, int32_t warps) {
+template <typename T, int V, int C, int WARPS, bool PARAMS>
+__global__ void __launch_bounds__(Team<WARPS>::kBlock, 512 / Team<WARPS>::kBlock) norm_grad_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kRing = V * sizeof(T) == 16;
-    constexpr int N = C * V, H = N / 2, D = depth_of(2 * C);
+    constexpr int N = C * V, H = N / 2;
     extern __shared__ uint4 s_ahead[];  // rows ahead; with several teams, [2][width] of parts after them
-    float* const s_part = reinterpret_cast<float*>(s_ahead + (kRing ? ahead_bytes(2 * C, blockDim.x) / 16 : 0));
-    const Team t = team_of(warps);
+    float* const s_part = reinterpret_cast<float*>(s_ahead + (kRing ? ahead_bytes(2 * C, Team<WARPS>::kBlock) / 16 : 0));
+    Team<WARPS> t;
+    constexpr int kTeam = Team<WARPS>::kTeamThreads;
     const int32_t vectors = (int32_t)(a.width / V);
-    const int64_t step = (int64_t)gridDim.x * t.teams;
-    const Ahead<2 * C, D> ahead(s_ahead);
-    int64_t r = (int64_t)blockIdx.x * t.teams + t.number, rc = r;
-    uint32_t turn = 0, row = 0, row_copied = 0;
+    const int64_t step = (int64_t)gridDim.x * Team<WARPS>::kTeams;
+    Ahead<2 * C, depth_of(2 * C), Team<WARPS>::kBlock> ahead(s_ahead);
+    int64_t r = (int64_t)blockIdx.x * Team<WARPS>::kTeams + t.number, rc = r;
+    bool in[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) in[c] = t.thread + c * kTeam < vectors;
+    const int64_t x_step = step * a.x_stride, dy_step = step * a.dy_stride, dx_step = step * a.dx_stride;
+    const T* px = (const T*)a.x + r * a.x_stride + t.thread * V;
+    const T* pd = (const T*)a.dy + r * a.dy_stride + t.thread * V;
+    T* dx = (T*)a.dx + r * a.dx_stride + t.thread * V;
+    const float* saved = a.saved + 2 * r;
     griddep_wait();
     auto copy_row = [&]() {
         if (rc < a.rows) {
-            const Pack<T, V>* px = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + rc * a.x_stride);
-            const Pack<T, V>* pd = reinterpret_cast<const Pack<T, V>*>((const T*)a.dy + rc * a.dy_stride);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int32_t q = t.thread + c * t.threads;
-                if (q < vectors) {
-                    ahead.copy(row_copied, 2 * c, px + q);
-                    ahead.copy(row_copied, 2 * c + 1, pd + q);
+            for (int c = 0; c < C; ++c)
+                if (in[c]) {
+                    ahead.copy(2 * c, px + c * kTeam * V);
+                    ahead.copy(2 * c + 1, pd + c * kTeam * V);
                 }
-            }
         }
-        ahead.done_row();
+        ahead.copied();
         rc += step;
-        ++row_copied;
+        px += x_step;
+        pd += dy_step;
     };
     if (kRing)
-        for (int i = 0; i < D - 1; ++i) copy_row();
+        for (int i = 0; i < depth_of(2 * C) - 1; ++i) copy_row();
     uint64_t g[H], dg[H], db[H];
     {
         float f[N];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int32_t q = t.thread + c * t.threads;
 #pragma unroll
             for (int i = 0; i < V; ++i) f[c * V + i] = 0.0f;
-            if (q < vectors) params_at<V>(a.gamma, a.param_type, (int64_t)q * V, 1.0f, f + c * V);
+            if (in[c]) params_at<V>(a.gamma, a.param_type, (t.thread + c * kTeam) * V, 1.0f, f + c * V);
         }
 #pragma unroll
         for (int i = 0; i < H; ++i) {
@@ -316,33 +341,33 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_con
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c] = dy[c] = Pack<T, V>{};
     // (without the ring a row's vectors are loaded one row ahead, into registers)
-    auto load = [&](int64_t i) {
-        mean = a.saved[2 * i];
-        rstd = a.saved[2 * i + 1];
+    auto load = [&]() {
+        mean = saved[0];
+        rstd = saved[1];
+        saved += 2 * step;
         if constexpr (!kRing) {
-            const Pack<T, V>* px = reinterpret_cast<const Pack<T, V>*>((const T*)a.x + i * a.x_stride);
-            const Pack<T, V>* pd = reinterpret_cast<const Pack<T, V>*>((const T*)a.dy + i * a.dy_stride);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int32_t q = t.thread + c * t.threads;
-                if (q < vectors) {
-                    x[c] = px[q];
-                    dy[c] = pd[q];
+            for (int c = 0; c < C; ++c)
+                if (in[c]) {
+                    x[c] = *reinterpret_cast<const Pack<T, V>*>(px + c * kTeam * V);
+                    dy[c] = *reinterpret_cast<const Pack<T, V>*>(pd + c * kTeam * V);
                 }
-            }
+            px += x_step;
+            pd += dy_step;
         }
     };
-    if (r < a.rows) load(r);
-    for (; r < a.rows; r += step, ++row) {
+    if (r < a.rows) load();
+    for (; r < a.rows; r += step, dx += dx_step) {
         if constexpr (kRing) {
             copy_row();
             ahead.wait();
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                if (t.thread + c * t.threads < vectors) {
-                    x[c] = ahead.template get<Pack<T, V>>(row, 2 * c);
-                    dy[c] = ahead.template get<Pack<T, V>>(row, 2 * c + 1);
+                if (in[c]) {
+                    x[c].raw = ahead.get(2 * c);
+                    dy[c].raw = ahead.get(2 * c + 1);
                 }
+            ahead.read();
         }
         uint64_t xh[H], e[H], s = 0, u = 0;
         const uint64_t r2 = pair(rstd, rstd), m2 = pair(-mean, -mean);
@@ -361,48 +386,45 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_con
             s = add2(s, e[i]);
             u = fma2(e[i], xh[i], u);
         }
-        if (r + step < a.rows) load(r + step);
+        if (r + step < a.rows) load();
         if (a.dx == nullptr) continue;
-        const float2 sums = team_sum(t, turn++, sum_of(s), sum_of(u));
+        const float2 sums = t.sum(sum_of(s), sum_of(u));
         const float m = -sums.x * a.inv_width, n = -sums.y * a.inv_width;
         const uint64_t mm = pair(m, m), nn = pair(n, n);
-        Pack<T, V>* dx = reinterpret_cast<Pack<T, V>*>((T*)a.dx + r * a.dx_stride);
         float f[N];
 #pragma unroll
         for (int i = 0; i < H; ++i) split(mul2(fma2(xh[i], nn, add2(e[i], mm)), r2), f[2 * i], f[2 * i + 1]);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int32_t q = t.thread + c * t.threads;
-            if (q < vectors && ZS_RANGE_OK(kSiteNormRow, (int64_t)q * V, V, a.width)) dx[q] = pack<T, V>(f + c * V);
-        }
+        for (int c = 0; c < C; ++c)
+            if (in[c] && ZS_RANGE_OK(kSiteNormRow, (int64_t)(t.thread + c * kTeam) * V, V, a.width))
+                *reinterpret_cast<Pack<T, V>*>(dx + c * kTeam * V) = pack<T, V>(f + c * V);
     }
     if (!PARAMS) return;
     float* const out = a.part + 2 * (int64_t)blockIdx.x * a.width;
     float pg[N], pb[N];
     split_all<N>(dg, pg);
     split_all<N>(db, pb);
-    for (int n = 0; n < t.teams; ++n) {
+    for (int n = 0; n < Team<WARPS>::kTeams; ++n) {
         if (n == t.number) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int32_t q = t.thread + c * t.threads;
-                if (q >= vectors) break;
+                if (!in[c]) continue;
+                const int32_t k = (t.thread + c * kTeam) * V;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int32_t k = q * V + i;
-                    float p = pg[c * V + i], b = pb[c * V + i];
-                    if (n > 0) p += s_part[k], b += s_part[a.width + k];
-                    if (n + 1 < t.teams) {
-                        s_part[k] = p;
-                        s_part[a.width + k] = b;
-                    } else {
-                        out[k] = p;
-                        out[a.width + k] = b;
+                    if (n > 0) pg[c * V + i] += s_part[k + i], pb[c * V + i] += s_part[a.width + k + i];
+                    if (n + 1 < Team<WARPS>::kTeams) {
+                        s_part[k + i] = pg[c * V + i];
+                        s_part[a.width + k + i] = pb[c * V + i];
                     }
+                }
+                if (n + 1 == Team<WARPS>::kTeams) {
+                    *reinterpret_cast<Pack<float, V>*>(out + k) = pack<float, V>(pg + c * V);
+                    *reinterpret_cast<Pack<float, V>*>(out + a.width + k) = pack<float, V>(pb + c * V);
                 }
             }
         }
-        if (t.teams > 1) __syncthreads();
+        if (Team<WARPS>::kTeams > 1) __syncthreads();
     }
 }
 
@@ -432,12 +454,12 @@ __global__ void __launch_bounds__(512) norm_param_kernel(const __grid_constant__
 
 // ----------------------------------------------------------------- long rows ---
 
-// Rows that a team's registers do not hold are read once for each sum, from L2 after
-// the first: a block to a row.
+// Rows that a team's registers do not hold (and forward those with gamma and beta of the
+// other 16-bit type, or of a 16-bit type next to fp32 rows) are read once for each sum, from
+// L2 after the first: a block to a row.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const __grid_constant__ NormArgs a) {
-    const Team t = team_of(kMaxThreads / 32);
-    uint32_t turn = 0;
+    Team<kMaxThreads / 32> t;
     griddep_wait();
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T* x = (const T*)a.x + r * a.x_stride;
@@ -445,14 +467,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const __grid_con
         float s = 0.0f;
 #pragma unroll 4
         for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) s += to_float(x[k]);
-        const float mean = team_sum(t, turn++, s, 0.0f).x * a.inv_width;
+        const float mean = t.sum(s) * a.inv_width;
         s = 0.0f;
 #pragma unroll 4
         for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) {
             const float d = to_float(x[k]) - mean;
             s = fmaf(d, d, s);
         }
-        const float rstd = 1.0f / sqrtf(team_sum(t, turn++, s, 0.0f).x * a.inv_width + a.eps);
+        const float rstd = rsqrtf(fmaf(t.sum(s), a.inv_width, a.eps));
 #pragma unroll 4
         for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) {
             float g, b;
@@ -468,8 +490,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const __grid_con
 }
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_long_dx_kernel(const __grid_constant__ NormArgs a) {
-    const Team t = team_of(kMaxThreads / 32);
-    uint32_t turn = 0;
+    Team<kMaxThreads / 32> t;
     griddep_wait();
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *x = (const T*)a.x + r * a.x_stride, *dy = (const T*)a.dy + r * a.dy_stride;
@@ -482,7 +503,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_dx_kernel(const __grid_
             s += g;
             u = fmaf(g, (to_float(x[k]) - mean) * rstd, u);
         }
-        const float2 sums = team_sum(t, turn++, s, u);
+        const float2 sums = t.sum(s, u);
         const float m = sums.x * a.inv_width, n = sums.y * a.inv_width;
 #pragma unroll 4
         for (int64_t k = threadIdx.x; k < a.width; k += kMaxThreads) {
@@ -513,20 +534,28 @@ __global__ void __launch_bounds__(256) norm_long_part_kernel(const __grid_consta
 
 int64_t groups_of(int64_t rows) { return rows < kMaxGroups ? (rows > 0 ? rows : 1) : kMaxGroups; }
 
-// How a row is dealt to a team: V elements to a vector, C vectors to a thread.  c = 0: the
-// row is too long.
+// How a row is dealt to a team: c vectors of v elements to a thread, `most` at most, with
+// as few warps as that takes; warps = 0: the row is too long.
 struct Shape {
-    int v, c, warps;
+    int c, warps;
 };
+constexpr int kElements = 16;  // of a thread, where rows are taken element by element
 Shape shape_of(int64_t width, int v, int most) {
     const int64_t vectors = width / v;
-    const int per_thread = v == 1 ? 16 : most / v;
-    for (int warps = 1; warps <= kMaxThreads / 32; warps *= 2) {
-        if (vectors > 32ll * warps * per_thread) continue;
-        const int c = (int)((vectors + 32 * warps - 1) / (32 * warps));
-        return {v, v == 1 ? (c <= 4 ? 4 : 16) : c, warps};
+    for (int warps = 1; warps <= kMaxThreads / 32; warps *= 2)
+        if (vectors <= 32ll * warps * most) return {(int)((vectors + 32 * warps - 1) / (32 * warps)), warps};
+    return {0, 0};
+}
+// Calls f with the number of warps as a constant.
+template <typename F>
+int32_t with_warps(int warps, F f) {
+    switch (warps) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 8: return f(std::integral_constant<int, 8>());
+    default: return f(std::integral_constant<int, 16>());
     }
-    return {v, 0, kMaxThreads / 32};
 }
 // Whether rows of these matrices (row strides in elements) and the parameters can be
 // accessed as 16-byte vectors.
@@ -542,54 +571,59 @@ struct Matrix {
     int64_t second;
 };
 
-template <typename T, int V, int C>
-int32_t launch_rows(const NormArgs& a, int warps, cudaStream_t stream) {
-    const int threads = warps > kThreads / 32 ? 32 * warps : kThreads, teams = threads / (32 * warps);
-    const size_t shared = V * sizeof(T) == 16 ? ahead_bytes(C, threads) : 0;
-    const unsigned grid = grid_of((const void*)norm_rows_kernel<T, V, C>, threads, shared, (a.rows + teams - 1) / teams);
+template <typename T, typename P, int V, int C, int WARPS>
+int32_t launch_rows(const NormArgs& a, cudaStream_t stream) {
+    constexpr int threads = Team<WARPS>::kBlock, teams = Team<WARPS>::kTeams;
+    constexpr size_t shared = V * sizeof(T) == 16 ? ahead_bytes(C, threads) : 0;
+    const auto kernel = norm_rows_kernel<T, P, V, C, WARPS>;
+    const unsigned grid = grid_of((const void*)kernel, threads, shared, (a.rows + teams - 1) / teams);
     if (grid == 0) return ZS_ERR_CUDA;
-    return launch_shared(norm_rows_kernel<T, V, C>, dim3(grid), threads, shared, stream, "norm_rows_kernel", a, warps);
+    return launch_shared(kernel, dim3(grid), threads, shared, stream, "norm_rows_kernel", a);
 }
 template <typename T>
+int32_t launch_long(const NormArgs& a, cudaStream_t stream, T) {
+    const unsigned grid = grid_of((const void*)norm_long_kernel<T>, kMaxThreads, 0, a.rows);
+    if (grid == 0) return ZS_ERR_CUDA;
+    return launch(norm_long_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_kernel", a);
+}
+template <typename T, typename P>
 int32_t launch_forward(const NormArgs& a, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), M = 4;
     const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, a.beta, Matrix{a.x, a.x_stride}, Matrix{a.y, a.y_stride});
-    const Shape s = shape_of(a.width, wide ? V : 1, 4 * V);
-    if (s.c == 0) {
-        const unsigned grid = grid_of((const void*)norm_long_kernel<T>, kMaxThreads, 0, a.rows);
-        if (grid == 0) return ZS_ERR_CUDA;
-        return launch(norm_long_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_kernel", a);
-    }
-    if (!wide) return s.c == 4 ? launch_rows<T, 1, 4>(a, s.warps, stream) : launch_rows<T, 1, 16>(a, s.warps, stream);
-    if (s.c == 1) return launch_rows<T, V, 1>(a, s.warps, stream);
-    return s.c == 2 ? launch_rows<T, V, 2>(a, s.warps, stream) : launch_rows<T, V, 4>(a, s.warps, stream);
+    const Shape s = shape_of(a.width, wide ? V : 1, wide ? M : kElements);
+    if (s.warps == 0) return launch_long(a, stream, T());
+    if (!wide)
+        return with_warps(s.warps, [&](auto w) { return launch_rows<T, P, 1, kElements, decltype(w)::value>(a, stream); });
+    if (s.c == 1) return launch_rows<T, P, V, 1, 1>(a, stream);
+    if (s.c == 2) return launch_rows<T, P, V, 2, 1>(a, stream);
+    return with_warps(s.warps, [&](auto w) { return launch_rows<T, P, V, M, decltype(w)::value>(a, stream); });
 }
 
 int32_t launch_params(const NormArgs& a, int64_t groups, cudaStream_t stream) {
     return launch(norm_param_kernel, dim3((unsigned)((a.width + 31) / 32)), 512, stream, "norm_param_kernel", a, (int32_t)groups);
 }
-template <typename T, int V, int C>
-int32_t launch_grad_rows(const NormArgs& a, int warps, cudaStream_t stream) {
+template <typename T, int V, int C, int WARPS>
+int32_t launch_grad_rows(const NormArgs& a, cudaStream_t stream) {
     const bool params = a.dgamma != nullptr || a.dbeta != nullptr;
-    const int threads = warps > kThreads / 32 ? 32 * warps : kThreads, teams = threads / (32 * warps);
+    constexpr int threads = Team<WARPS>::kBlock, teams = Team<WARPS>::kTeams;
     const size_t shared = (V * sizeof(T) == 16 ? ahead_bytes(2 * C, threads) : 0) + (params && teams > 1 ? 8 * (size_t)a.width : 0);
     auto go = [&](auto kernel) {
         unsigned grid = grid_of((const void*)kernel, threads, shared, (a.rows + teams - 1) / teams);
         if (grid == 0) return (int32_t)ZS_ERR_CUDA;
         if (grid > kMaxGroups) grid = kMaxGroups;
-        const int32_t rc = launch_shared(kernel, dim3(grid), threads, shared, stream, "norm_grad_kernel", a, warps);
+        const int32_t rc = launch_shared(kernel, dim3(grid), threads, shared, stream, "norm_grad_kernel", a);
         return rc != ZS_OK || !params ? rc : launch_params(a, grid, stream);
     };
-    return params ? go(norm_grad_kernel<T, V, C, true>) : go(norm_grad_kernel<T, V, C, false>);
+    return params ? go(norm_grad_kernel<T, V, C, WARPS, true>) : go(norm_grad_kernel<T, V, C, WARPS, false>);
 }
 template <typename T>
 int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), M = 16 / V;
     const bool params = a.dgamma != nullptr || a.dbeta != nullptr;
     const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, nullptr, Matrix{a.x, a.x_stride}, Matrix{a.dy, a.dy_stride},
                                   Matrix{a.dx, a.dx_stride});
-    const Shape s = shape_of(a.width, wide ? V : 1, 16);
-    if (s.c == 0) {
+    const Shape s = shape_of(a.width, wide ? V : 1, wide ? M : kElements);
+    if (s.warps == 0) {
         if (params) {
             // (before dx, which may take dy's or x's place)
             const int64_t groups = a.rows < 64 ? groups_of(a.rows) : 64;
@@ -602,10 +636,10 @@ int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
         if (grid == 0) return ZS_ERR_CUDA;
         return launch(norm_long_dx_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_dx_kernel", a);
     }
-    if (!wide) return s.c == 4 ? launch_grad_rows<T, 1, 4>(a, s.warps, stream) : launch_grad_rows<T, 1, 16>(a, s.warps, stream);
-    if (s.c == 1) return launch_grad_rows<T, V, 1>(a, s.warps, stream);
-    if (V == 8 || s.c == 2) return launch_grad_rows<T, V, 2>(a, s.warps, stream);
-    return launch_grad_rows<T, V, 16 / V>(a, s.warps, stream);
+    if (!wide)
+        return with_warps(s.warps, [&](auto w) { return launch_grad_rows<T, 1, kElements, decltype(w)::value>(a, stream); });
+    if (s.c == 1) return launch_grad_rows<T, V, 1, 1>(a, stream);
+    return with_warps(s.warps, [&](auto w) { return launch_grad_rows<T, V, M, decltype(w)::value>(a, stream); });
 }
 
 bool valid_sizes(int64_t rows, int64_t width) {
@@ -656,7 +690,12 @@ ZS_API int32_t zero_layer_norm_async(const zs_norm* n, void* y, int64_t y_stride
     a.y = y;
     a.y_stride = n->rows > 1 ? y_stride : n->width;
     a.saved_out = saved;
-    return with_elem(n->type, [&](auto t) { return launch_forward<decltype(t)>(a, (cudaStream_t)stream); });
+    return with_elem(n->type, [&](auto t) {
+        using T = decltype(t);
+        return n->param_type == n->type ? launch_forward<T, T>(a, (cudaStream_t)stream)
+               : n->param_type == ZS_F32 ? launch_forward<T, float>(a, (cudaStream_t)stream)
+                                         : launch_long(a, (cudaStream_t)stream, t);
+    });
 }
 
 ZS_API int64_t zero_layer_norm_work_bytes(int64_t rows, int64_t width) {
