@@ -105,11 +105,13 @@ constexpr int kSortShared = (kSortWarps * kBins + 2 * kBins) * 4;
 
 // The lanes of the warp with the same digit (those of `in`): a vote for each bit.  (The
 // instruction that matches values took 70 cycles of the SM; nine votes take some 10.)
-__device__ __forceinline__ uint32_t same_digit(uint32_t d, int bits, bool in) {
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, bool in) {
     uint32_t same = __ballot_sync(0xffffffffu, in);
-    for (int b = 0; b < bits; ++b) {
-        const uint32_t votes = __ballot_sync(0xffffffffu, d >> b & 1u);
-        same &= d >> b & 1u ? votes : ~votes;
+#pragma unroll
+    for (int b = 0; b < kMaxBits; ++b) {  // (bits that the digit does not have are 0 in all lanes)
+        const bool set = (d & (1u << b)) != 0;
+        const uint32_t votes = __ballot_sync(0xffffffffu, set);
+        same &= set ? votes : ~votes;
     }
     return same;
 }
@@ -176,13 +178,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
 #pragma unroll
             for (int q = 0; q < kAhead; ++q) key[q] = i0 + 32 * q + lane < to ? key_of(i0 + 32 * q + lane) : 0u;
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                if (i0 + 32 * q >= to) break;
-                const bool in = i0 + 32 * q + lane < to;
-                const uint32_t d = digit_of(key[q]), same = same_digit(d, a.bits, in);
-                if (in && __ffs(same) - 1 == lane) count[warp][d] += __popc(same);
-                __syncwarp();
-            }
+            for (int q = 0; q < kAhead; ++q)
+                if (i0 + 32 * q + lane < to) atomicAdd(&count[warp][digit_of(key[q])], 1u);
         }
         __syncthreads();
         uint32_t mine = 0;
@@ -229,7 +226,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
             for (int q = 0; q < kAhead; ++q) {
                 if (i0 + 32 * q >= to) break;
                 const bool in = i0 + 32 * q + lane < to;
-                const uint32_t d = digit_of(key[q]), same = same_digit(d, a.bits, in);
+                const uint32_t d = digit_of(key[q]), same = same_digit(d, in);
                 if (in) {
                     const int64_t at = base[d] + count[warp][d] + (uint32_t)__popc(same & ((1u << lane) - 1u));
                     if (ZS_RANGE_OK(kSiteSort, at, 1, a.tokens)) {

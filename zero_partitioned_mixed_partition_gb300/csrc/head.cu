@@ -11,6 +11,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cluster_counts.h"
 #include "zs_internal.h"
 
@@ -33,6 +35,9 @@ constexpr int kMaxSplit = 16;               // parts of dH's sums
 constexpr int64_t kPieceBytes = 1ll << 30;  // of a piece's gradient, where the caller leaves the choice
 
 constexpr int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Rows between the statistics of two half tiles: not a power of 2, for the memory's channels.
+__host__ __device__ constexpr int64_t part_pitch(int64_t rows_pad) { return rows_pad + 32; }
 
 // ------------------------------------------------------------------ scratch ---
 
@@ -79,7 +84,7 @@ Plan plan_of(int64_t rows, int64_t width, int64_t vocab, int64_t piece, bool gra
         p.part = take(4 * p.sums_room * width);
         p.d = take(2 * p.rows_pad * p.piece);
     } else {
-        p.part = take(2 * 8 * p.rows_pad * p.tiles);
+        p.part = take(2 * 8 * part_pitch(p.rows_pad) * p.tiles);
         p.label_logit = take(4 * p.rows_pad);
     }
     p.total = at;
@@ -124,103 +129,146 @@ struct HeadArgs {
     int64_t rows_pad, tiles, piece, sums_room;
 };
 
-constexpr int kRowThreads = 1024, kRowsEach = 8;
+constexpr int kRowThreads = 1024;
+// Rows of one pass of the rows kernel's block; up to so many are numbered by every block of
+// the gather kernel for itself instead, which saves a launch.
+constexpr int kRowsEach = 8, kFewRows = 1024;
 
-// Numbers the live rows in their order, and finds the power of 2 by which d is
-// scaled.  One block, since the numbers depend on all rows before; kRowsEach rows to a
-// thread at a time, whose loads are under way together.
-__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ HeadArgs a) {
-    constexpr int kCounts = kRowsEach * kRowThreads / 32;
-    __shared__ int32_t s_count[kCounts], s_base;
-    __shared__ float s_top[kRowThreads / 32];
+// Numbers live rows in their order, EACH to a thread, whose loads are under way together,
+// and writes what `emit` is called with: a row, its label and dlogp, its number or -1.  Called by the
+// whole block of THREADS; returns the number of live rows up to here.
+template <int THREADS, int EACH, typename F>
+__device__ int32_t number_rows(const HeadArgs& a, int64_t from, int32_t before, F emit) {
+    constexpr int kWarps = THREADS / 32, kCounts = EACH * kWarps;
+    static_assert(kCounts % 32 == 0, "a warp scans the counts");
+    __shared__ int32_t s_count[kCounts + 1];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    if (threadIdx.x == 0) s_base = 0;
-    griddep_launch_dependents();
-    griddep_wait();
-    float top = 0.0f;
-    const float factor = loss_scale_of(a.ctrl) * a.it;
-    for (int64_t from = 0; from < a.rows; from += kRowsEach * kRowThreads) {
-        int64_t label[kRowsEach];
-        float dlogp[kRowsEach];
-        uint32_t votes[kRowsEach];
+    int64_t label[EACH];
+    float dlogp[EACH];
+    uint32_t votes[EACH];
 #pragma unroll
-        for (int k = 0; k < kRowsEach; ++k) {
-            const int64_t i = from + k * kRowThreads + threadIdx.x;
-            label[k] = i < a.rows ? a.labels[i] : -1;
-            dlogp[k] = i < a.rows && a.dlogp != nullptr ? a.dlogp[i] : 1.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < kRowsEach; ++k) {
-            votes[k] = __ballot_sync(0xffffffffu, label[k] >= 0 && label[k] < a.vocab && dlogp[k] != 0.0f);
-            if (lane == 0) s_count[k * (kRowThreads / 32) + warp] = __popc(votes[k]);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // counts become the numbers of live rows before them
-            int32_t c[kCounts / 32], sum = 0;
-#pragma unroll
-            for (int q = 0; q < kCounts / 32; ++q) {
-                c[q] = s_count[lane * (kCounts / 32) + q];
-                sum += c[q];
-            }
-            int32_t scan = sum;
-            for (int o = 1; o < 32; o *= 2) {
-                const int32_t x = __shfl_up_sync(0xffffffffu, scan, o);
-                if (lane >= o) scan += x;
-            }
-            int32_t before = s_base + scan - sum;
-#pragma unroll
-            for (int q = 0; q < kCounts / 32; ++q) {
-                s_count[lane * (kCounts / 32) + q] = before;
-                before += c[q];
-            }
-            __syncwarp();
-            if (lane == 31) s_base = before;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kRowsEach; ++k) {
-            const int64_t i = from + k * kRowThreads + threadIdx.x;
-            if (i >= a.rows) break;
-            const bool live = votes[k] >> lane & 1u;
-            const int32_t r = s_count[k * (kRowThreads / 32) + warp] + __popc(votes[k] & ((1u << lane) - 1u));
-            a.slot[i] = live ? r : -1;
-            if (!live) continue;
-            Row row = {0.0f, 0.0f, 0.0f, (int32_t)label[k]};
-            if (a.dlogp != nullptr) {
-                row.top = a.saved[2 * i];
-                row.log_sum = a.saved[2 * i + 1];
-                // (a row of nothing but -inf has no gradient)
-                row.coef = row.log_sum == -__int_as_float(0x7f800000) ? 0.0f : factor * dlogp[k];
-                if (fabsf(row.coef) <= 3.402823466e38f) top = fmaxf(top, fabsf(row.coef));
-            }
-            a.index[r] = (int32_t)i;
-            a.row[r] = row;
-        }
-        __syncthreads();
+    for (int k = 0; k < EACH; ++k) {
+        const int64_t i = from + k * THREADS + threadIdx.x;
+        label[k] = i < a.rows ? a.labels[i] : -1;
+        dlogp[k] = i < a.rows && a.dlogp != nullptr ? a.dlogp[i] : 1.0f;
     }
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        votes[k] = __ballot_sync(0xffffffffu, label[k] >= 0 && label[k] < a.vocab && dlogp[k] != 0.0f);
+        if (lane == 0) s_count[k * kWarps + warp] = __popc(votes[k]);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // counts become the numbers of live rows before them
+        int32_t c[kCounts / 32], sum = 0;
+#pragma unroll
+        for (int q = 0; q < kCounts / 32; ++q) {
+            c[q] = s_count[lane * (kCounts / 32) + q];
+            sum += c[q];
+        }
+        int32_t scan = sum;
+        for (int o = 1; o < 32; o *= 2) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += x;
+        }
+        int32_t n = before + scan - sum;
+#pragma unroll
+        for (int q = 0; q < kCounts / 32; ++q) {
+            s_count[lane * (kCounts / 32) + q] = n;
+            n += c[q];
+        }
+        if (lane == 31) s_count[kCounts] = n;
+    }
+    __syncthreads();
+    const int32_t all = s_count[kCounts];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int64_t i = from + k * THREADS + threadIdx.x;
+        if (i >= a.rows) break;
+        const int32_t r = s_count[k * kWarps + warp] + __popc(votes[k] & ((1u << lane) - 1u));
+        emit(i, label[k], dlogp[k], votes[k] >> lane & 1u ? r : -1);
+    }
+    __syncthreads();
+    return all;
+}
+// What the products need of a live row.
+__device__ __forceinline__ Row row_of(const HeadArgs& a, int64_t i, int64_t label, float dlogp, float factor) {
+    Row row = {0.0f, 0.0f, 0.0f, (int32_t)label};
+    if (a.dlogp != nullptr) {
+        row.top = a.saved[2 * i];
+        row.log_sum = a.saved[2 * i + 1];
+        // (a row of nothing but -inf has no gradient)
+        row.coef = row.log_sum == -__int_as_float(0x7f800000) ? 0.0f : factor * dlogp;
+    }
+    return row;
+}
+// From the largest finite |c| of each thread: the numbers, and the power of 2 that takes it
+// to [2^14, 2^15).  Called by the whole block of THREADS.
+template <int THREADS>
+__device__ void write_counts(const HeadArgs& a, int32_t live, float top) {
+    __shared__ float s_top[THREADS / 32];
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) s_top[warp] = top;
+    if (threadIdx.x % 32 == 0) s_top[threadIdx.x / 32] = top;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 0; w < kRowThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-        // the largest finite |c| goes to [2^14, 2^15)
+        for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, s_top[w]);
         int e = top > 0.0f ? 14 - ilogbf(top) : 0;
         e = e > 120 ? 120 : e < -120 ? -120 : e;
-        *a.counts = Counts{s_base, scalbnf(1.0f, e), scalbnf(1.0f, -e)};
+        *a.counts = Counts{live, scalbnf(1.0f, e), scalbnf(1.0f, -e)};
     }
+}
+__device__ __forceinline__ float larger_finite(float top, float c) {
+    return fabsf(c) <= 3.402823466e38f ? fmaxf(top, fabsf(c)) : top;
+}
+
+// Many rows: one block numbers them, since the numbers depend on all rows before.
+__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ HeadArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const float factor = loss_scale_of(a.ctrl) * a.it;
+    float top = 0.0f;
+    int32_t live = 0;
+    for (int64_t from = 0; from < a.rows; from += kRowsEach * kRowThreads)
+        live = number_rows<kRowThreads, kRowsEach>(a, from, live, [&](int64_t i, int64_t label, float dlogp, int32_t r) {
+            a.slot[i] = r;
+            if (r < 0) return;
+            const Row row = row_of(a, i, label, dlogp, factor);
+            top = larger_finite(top, row.coef);
+            a.index[r] = (int32_t)i;
+            a.row[r] = row;
+        });
+    write_counts<kRowThreads>(a, live, top);
 }
 
 // Copies the live rows' hidden states together, with zeros up to a whole tile, and
-// writes the outputs of the rows that are left out: a warp to a row.
+// writes the outputs of the rows that are left out: a warp to a row.  FEW: numbers the
+// rows as well, in every block; the first one writes the numbers down.
+template <bool FEW>
 __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant__ HeadArgs a) {
+    __shared__ int32_t s_slot[FEW ? kFewRows : 1];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % 32;
-    const int32_t vectors = (int32_t)(a.width / 8), live = a.counts->live;
+    const int32_t vectors = (int32_t)(a.width / 8);
+    int32_t live;
+    if (FEW) {
+        const float factor = loss_scale_of(a.ctrl) * a.it;
+        float top = 0.0f;
+        live = number_rows<256, kFewRows / 256>(a, 0, 0, [&](int64_t i, int64_t label, float dlogp, int32_t r) {
+            s_slot[i] = r;
+            if (r < 0 || blockIdx.x != 0) return;
+            const Row row = row_of(a, i, label, dlogp, factor);
+            top = larger_finite(top, row.coef);
+            a.index[r] = (int32_t)i;
+            a.row[r] = row;
+        });
+        if (blockIdx.x == 0) write_counts<256>(a, live, top);
+    } else {
+        live = a.counts->live;
+    }
     const int64_t fill = round_up(live, kTile) - live;
     for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < a.rows + fill; i += (int64_t)gridDim.x * 8) {
-        const int32_t slot = i < a.rows ? a.slot[i] : (int32_t)(live + i - a.rows);
+        const int32_t slot = i >= a.rows ? (int32_t)(live + i - a.rows) : FEW ? s_slot[i] : a.slot[i];
         const bool copy = i < a.rows && slot >= 0;
         const uint4* from = reinterpret_cast<const uint4*>((const uint16_t*)a.hidden + i * a.hidden_stride);
         uint4* to = slot >= 0             ? reinterpret_cast<uint4*>(a.compact + (int64_t)slot * a.width)
@@ -262,10 +310,16 @@ __device__ __forceinline__ float infinity() { return __int_as_float(0x7f800000);
 //   kDWeight   d^T H: the piece's rows of dW
 enum { kLogits, kGrad, kDHidden, kDWeight };
 
-constexpr int kStages = 6, kStep = 64;                      // stages of the ring, k in one of them
-constexpr int kHalfBytes = 128 * kStep * 2;                 // a CTA's half of an operand's stage
-constexpr int kBoxBytes = 64 * kStep * 2;                   // 64 m of 64 k, across k
-constexpr int kRing = kStages * 2 * kHalfBytes;
+constexpr int kStep = 64;                                   // k of a stage of the ring
+constexpr int kRowBytes = kStep * 2;                        // of an operand's row in a stage
+constexpr int kBoxBytes = 64 * kRowBytes;                   // 64 m of 64 k, across k
+constexpr int kBytesA = 128 * kRowBytes;                    // A's stage in a CTA
+constexpr int columns_of(int ctas) { return (int)kTile / ctas; }  // of B in a CTA
+constexpr int stage_bytes(int ctas) { return kBytesA + columns_of(ctas) * kRowBytes; }
+constexpr int stages_of(int ctas) { return ctas == 2 ? 6 : 4; }
+constexpr int kRing = 6 * stage_bytes(2);
+static_assert(kRing == 4 * stage_bytes(1), "both fill the same shared memory");
+constexpr int kMaxStages = 6;
 // Steps that the tensor cores add up before their sums go to registers.  They cut a
 // sum off at fp32's last place after every 16 k; over 4096 k that left logits off by
 // 4e-6 of their size (a product in fp32 is off by 1e-7), over 512 k it leaves 5e-7.
@@ -360,21 +414,20 @@ __device__ __forceinline__ Tile tile_of(const Tiles& w, int32_t u) {
     }
     return t;
 }
-// Columns of B in a tile that a CTA holds: 64 where the width's last tile has no more
-// than 128.
+// Columns of B in a tile: 128 where the width's last tile has no more.
 template <int MODE>
-__device__ __forceinline__ int32_t half_of(const ProductArgs& p, int32_t n) {
-    return (MODE == kDHidden || MODE == kDWeight) && p.h.width - (int64_t)n * kTile <= 128 ? 64 : 128;
+__device__ __forceinline__ int32_t wide_of(const ProductArgs& p, int32_t n) {
+    return (MODE == kDHidden || MODE == kDWeight) && p.h.width - (int64_t)n * kTile <= 128 ? 128 : (int32_t)kTile;
 }
 
 struct Ring {
-    uint64_t full[kStages], empty[kStages];  // full: the first CTA's counts both CTAs' copies
+    uint64_t full[kMaxStages], empty[kMaxStages];  // full: the first CTA's counts both CTAs' copies
     uint64_t sums_full[2], sums_empty[2];    // sums_empty: the first CTA's counts both CTAs' warps
     uint64_t done;
     uint32_t sums;                           // address of the tensor memory
     int32_t failed;                          // a wait ran out
     int32_t issued;                          // steps whose copies were issued,
-    uint32_t bytes[kStages];                 // and what each CTA copied in the last ones
+    uint32_t bytes[kMaxStages];                 // and what each CTA copied in the last ones
 };
 
 // The 128 columns of a thread's row, as 16-bit numbers or fp32, from registers to
@@ -413,22 +466,25 @@ __device__ __forceinline__ float pick(const float* v, int32_t i) {
     return x[0];
 }
 
-// A pair of CTAs (a cluster of two) takes tile after tile.  In each CTA one thread
-// copies its halves of A and B ahead into a ring of kStages stages; one thread of the
+// CTAS = 2: a pair of CTAs (a cluster of two) takes tile after tile.  In each CTA one
+// thread copies its halves of A and B ahead into a ring of stages; one thread of the
 // first CTA multiplies, 16 k at a time, into one of two sets of sums in tensor memory,
 // kRun steps into each in turn; eight warps add the other set to sums in registers (a
-// thread has half a row of the tile) and turn those into the tile's outputs.
-template <typename T, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+// thread has half a row of the tile) and turn those into the tile's outputs.  CTAS = 1,
+// for up to 128 rows: a CTA by itself has a tile of 128 rows, so that no half of the
+// products is of rows that are not there.
+template <typename T, int MODE, int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 1)
     head_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ ProductArgs p) {
+    constexpr int kStages = stages_of(CTAS), kStage = stage_bytes(CTAS);
     constexpr bool kAlongA = MODE != kDWeight, kAlongB = MODE == kLogits || MODE == kGrad;  // operands along k
     extern __shared__ uint8_t s_raw[];
     __shared__ Ring ring;
     uint8_t* const stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
-    const int32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int32_t pair = blockIdx.x / CTAS, pairs = gridDim.x / CTAS;
     const HeadArgs& a = p.h;
 
     if (threadIdx.x == 0) {
@@ -438,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ring.sums_full[s], 1);
-            mbar_init(&ring.sums_empty[s], 2 * kProductWarps);
+            mbar_init(&ring.sums_empty[s], CTAS * kProductWarps);
         }
         mbar_init(&ring.done, 1);
         ring.failed = 0;
@@ -447,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         prefetch_map(&map_a);
         prefetch_map(&map_b);
     }
-    if (warp == 2) tensor_alloc(&ring.sums);
+    if (warp == 2) tensor_alloc<CTAS>(&ring.sums);
     tensor_fence_before();
     __syncthreads();
     cluster_arrive();
@@ -467,9 +523,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         bool ok = true;
         for (int32_t u = pair; u < units && ok; u += pairs) {
             const Tile t = tile_of<MODE>(w, u);
-            const int32_t half = half_of<MODE>(p, t.n);
-            const uint32_t bytes = (uint32_t)(kHalfBytes + half * kStep * 2);
-            const int32_t m0 = t.m * (int32_t)kTile + (int32_t)rank * 128, n0 = t.n * (int32_t)kTile + (int32_t)rank * half;
+            const int32_t mine = wide_of<MODE>(p, t.n) / CTAS;  // columns of B in this CTA
+            const uint32_t bytes = (uint32_t)(kBytesA + mine * kRowBytes);
+            const int32_t m0 = t.m * (CTAS * 128) + (int32_t)rank * 128, n0 = t.n * (int32_t)kTile + (int32_t)rank * mine;
             for (int32_t k = t.from; k < t.to; ++k, ++at) {
                 const int s = at % kStages;
                 if (!mbar_wait<false, true>(&ring.empty[s], (uint32_t)(at / kStages + 1) & 1u, &ring.failed)) {
@@ -478,23 +534,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 }
                 ring.bytes[s] = bytes;
                 ring.issued = at + 1;
-                if (rank == 0) mbar_expect(&ring.full[s], 2 * bytes);
+                if (rank == 0) mbar_expect(&ring.full[s], CTAS * bytes);
                 const uint32_t full = peer_addr(&ring.full[s], 0);
-                uint8_t* const to_a = stage0 + s * 2 * kHalfBytes;
-                uint8_t* const to_b = to_a + kHalfBytes;
+                uint8_t* const to_a = stage0 + s * kStage;
+                uint8_t* const to_b = to_a + kBytesA;
                 const int32_t x = k * kStep;
                 if (kAlongA) {
-                    copy_box(to_a, &map_a, x, m0, full);
+                    copy_box<CTAS>(to_a, &map_a, x, m0, full);
                 } else {
-                    copy_box(to_a, &map_a, m0, x, full);
-                    copy_box(to_a + kBoxBytes, &map_a, m0 + 64, x, full);
+                    copy_box<CTAS>(to_a, &map_a, m0, x, full);
+                    copy_box<CTAS>(to_a + kBoxBytes, &map_a, m0 + 64, x, full);
                 }
                 if (kAlongB) {
-                    copy_box(to_b, &map_b, x, (int32_t)p.first + n0, full);
+                    copy_box<CTAS>(to_b, &map_b, x, (int32_t)p.first + n0, full);
                 } else {
                     const int32_t y = MODE == kDHidden ? (int32_t)p.first + x : x;
-                    copy_box(to_b, &map_b, n0, y, full);
-                    if (half == 128) copy_box(to_b + kBoxBytes, &map_b, n0 + 64, y, full);
+                    for (int32_t c = 0; c < mine; c += 64) copy_box<CTAS>(to_b + c * kRowBytes, &map_b, n0 + c, y, full);
                 }
             }
         }
@@ -506,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         bool ok = true;
         for (int32_t u = pair; u < units && ok; u += pairs) {
             const Tile t = tile_of<MODE>(w, u);
-            const uint32_t kind = product_kind<T, kAlongA, kAlongB>(2u * (uint32_t)half_of<MODE>(p, t.n));
+            const uint32_t kind = product_kind<CTAS, T, kAlongA, kAlongB>((uint32_t)wide_of<MODE>(p, t.n));
             for (int32_t k = t.from; k < t.to; ++turn) {
                 const int set = turn & 1;
                 const int32_t stop = k + kRun < t.to ? k + kRun : t.to;
@@ -518,18 +573,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     ok = mbar_wait<false, true>(&ring.full[s], (uint32_t)(at / kStages) & 1u, &ring.failed);
                     if (!ok) break;
                     tensor_fence_after();
-                    const uint8_t* const from = stage0 + s * 2 * kHalfBytes;
-                    uint64_t da = operand<kAlongA>(from, kBoxBytes), db = operand<kAlongB>(from + kHalfBytes, kBoxBytes);
+                    const uint8_t* const from = stage0 + s * kStage;
+                    uint64_t da = operand<kAlongA>(from, kBoxBytes), db = operand<kAlongB>(from + kBytesA, kBoxBytes);
 #pragma unroll
                     for (int q = 0; q < kStep / 16; ++q) {
-                        multiply(sums + (uint32_t)set * 256u, da, db, kind, add || q > 0);
+                        multiply<CTAS>(sums + (uint32_t)set * 256u, da, db, kind, add || q > 0);
                         da += operand_step<kAlongA>();
                         db += operand_step<kAlongB>();
                     }
-                    arrive_after_products(&ring.empty[s]);
+                    arrive_after_products<CTAS>(&ring.empty[s]);
                 }
                 if (!ok) break;
-                arrive_after_products(&ring.sums_full[set]);
+                arrive_after_products<CTAS>(&ring.sums_full[set]);
             }
         }
     } else if (warp >= 4) {
@@ -541,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         int32_t turn = 0;
         for (int32_t u = pair; u < units; u += pairs) {
             const Tile t = tile_of<MODE>(w, u);
-            const bool mine = side == 0 || half_of<MODE>(p, t.n) == 128;
+            const bool mine = side == 0 || wide_of<MODE>(p, t.n) > 128;
             float v[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) v[i] = 0.0f;
@@ -569,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 for (int i = 0; i < 128; ++i) v[i] = quiet_nan();
             }
             if (!mine) continue;
-            const int64_t r = (int64_t)t.m * kTile + rank * 128 + quarter * 32 + lane;  // the thread's row of the tile,
+            const int64_t r = (int64_t)t.m * (CTAS * 128) + rank * 128 + quarter * 32 + lane;  // the thread's row of the tile,
             const int64_t j0 = (int64_t)t.n * kTile + side * 128;                        // and its first column
             if (MODE == kLogits) {
                 const int32_t label = a.row[r].label - (int32_t)j0;
@@ -590,7 +645,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 const float top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
 #pragma unroll
                 for (int i = 0; i < 128; ++i) add[i % 4] += exp2_approx((v[i] - top) * k2);
-                ((float2*)a.part)[(2 * (int64_t)t.n + side) * a.rows_pad + r] =
+                ((float2*)a.part)[(2 * (int64_t)t.n + side) * part_pitch(a.rows_pad) + r] =
                     make_float2(top, (add[0] + add[1]) + (add[2] + add[3]));
             } else if (MODE == kGrad) {
                 const Row row = a.row[r];
@@ -654,14 +709,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     // before the products are done and the barriers of the last steps that either
     // issued have counted their copies (of a step that one of the two did not reach,
     // that one's are made up for).
-    if ((load_from_peer(&ring.failed, 0) | load_from_peer(&ring.failed, 1)) != 0 && rank == 0 && threadIdx.x == 32) {
-            signal_after_products(&ring.done);
+    if ((load_from_peer(&ring.failed, 0) | load_from_peer(&ring.failed, CTAS - 1)) != 0 && rank == 0 && threadIdx.x == 32) {
+            signal_after_products<CTAS>(&ring.done);
             drain(&ring.done, 0);
-            const int32_t mine = ring.issued, other = load_from_peer(&ring.issued, 1);
+            const int32_t mine = ring.issued, other = load_from_peer(&ring.issued, CTAS - 1);
             const int32_t most = mine > other ? mine : other;
             for (int32_t i = most > kStages ? most - kStages : 0; i < most; ++i) {
                 const int s = i % kStages;
-                if (i >= mine) mbar_expect(&ring.full[s], (uint32_t)load_from_peer((const int32_t*)&ring.bytes[s], 1));
+                if (i >= mine) mbar_expect(&ring.full[s], (uint32_t)load_from_peer((const int32_t*)&ring.bytes[s], CTAS - 1));
                 if (i >= other) mbar_give(&ring.full[s], ring.bytes[s]);
                 drain(&ring.full[s], (uint32_t)(i / kStages) & 1u);
             }
@@ -671,12 +726,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     cluster_arrive();
     cluster_wait();
     tensor_fence_after();
-    if (warp == 2) tensor_free(sums);
+    if (warp == 2) tensor_free<CTAS>(sums);
 }
 
-// Joins the statistics of the rows' tiles: 32 rows to a block, 32 threads to a row.
-__global__ void __launch_bounds__(1024) head_join_kernel(const __grid_constant__ HeadArgs a) {
-    __shared__ float2 s_part[32][33];
+// Joins the statistics of the rows' half tiles: 32 rows to a block, 16 threads to a row.
+__global__ void __launch_bounds__(512) head_join_kernel(const __grid_constant__ HeadArgs a) {
+    __shared__ float2 s_part[16][32];
     const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
     const int64_t r = (int64_t)blockIdx.x * 32 + lane;
     griddep_wait();
@@ -690,26 +745,24 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const __grid_constant__
         top = high;
     };
     const float2* part = (const float2*)a.part + r;  // (rows up to a whole tile have statistics)
-    for (int64_t t = group; t < 2 * a.tiles; t += 8 * 32) {
+    const int64_t pitch = part_pitch(a.rows_pad);
+    const int32_t n = (int32_t)(2 * a.tiles);
+    for (int32_t t = group; t < n; t += 8 * 16) {
         float2 q[8];
+        // (all eight loads under way at once: past the end the last one's again)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = t + 32 * i < 2 * a.tiles ? part[(t + 32 * i) * a.rows_pad] : make_float2(kLowestFloat, 0.0f);
+        for (int i = 0; i < 8; ++i) q[i] = part[(t + 16 * i < n ? t + 16 * i : n - 1) * pitch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) join(q[i]);
+        for (int i = 0; i < 8; ++i)
+            if (t + 16 * i < n) join(q[i]);
     }
     s_part[group][lane] = make_float2(top, s);
     __syncthreads();
-    // a warp to a row from here
-    const int64_t r1 = (int64_t)blockIdx.x * 32 + group;
-    const float2 mine = s_part[lane][group];
-    top = mine.x;
-    s = mine.y;
-    for (int o = 16; o > 0; o >>= 1)
-        join(make_float2(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, s, o)));
-    if (lane != 0 || r1 >= live) return;
-    const int64_t i = a.index[r1];
+    if (group != 0 || r >= live) return;
+    for (int g = 1; g < 16; ++g) join(s_part[g][lane]);
+    const int64_t i = a.index[r];
     const float log_sum = logf(s);
-    a.logp[i] = s == 0.0f ? log_sum : (a.label_logit[r1] - top) * a.it - log_sum;
+    a.logp[i] = s == 0.0f ? log_sum : (a.label_logit[r] - top) * a.it - log_sum;
     if (a.saved_out != nullptr) {
         a.saved_out[2 * i] = top;
         a.saved_out[2 * i + 1] = log_sum;
@@ -771,20 +824,20 @@ int32_t make_map(CUtensorMap* map, int32_t type, const void* base, int64_t rows,
     return rc == CUDA_SUCCESS ? ZS_OK : zs::fail_with(ZS_ERR_CUDA, "cuTensorMapEncodeTiled: refused a matrix of the head");
 }
 
-// Pairs of CTAs that run at once; 0: a CUDA error, reported.
-template <typename T, int MODE>
+// Pairs of CTAs (CTAS = 1: CTAs) that run at once; 0: a CUDA error, reported.
+template <typename T, int MODE, int CTAS>
 int pairs_of() {
-    const void* kernel = (const void*)head_product_kernel<T, MODE>;
+    const void* kernel = (const void*)head_product_kernel<T, MODE, CTAS>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductShared);
-    const int pairs = err == cudaSuccess ? active_clusters(kernel, kProductThreads, 2, kProductShared, &err) : 0;
+    const int pairs = err == cudaSuccess ? active_clusters(kernel, kProductThreads, CTAS, kProductShared, &err) : 0;
     if (pairs < 1) zs::cuda_fail(err, "head_product_kernel");
     return pairs;
 }
-template <typename T, int MODE>
+template <typename T, int MODE, int CTAS>
 int32_t launch_product(const ProductArgs& p, const CUtensorMap& map_a, const CUtensorMap& map_b, int pairs,
                        cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2u * (unsigned)pairs);
+    cfg.gridDim = dim3((unsigned)(CTAS * pairs));
     cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = kProductShared;
     cfg.stream = stream;
@@ -793,7 +846,7 @@ int32_t launch_product(const ProductArgs& p, const CUtensorMap& map_a, const CUt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, head_product_kernel<T, MODE>, map_a, map_b, p);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, head_product_kernel<T, MODE, CTAS>, map_a, map_b, p);
     if (err != cudaSuccess) return zs::cuda_fail(err, "head_product_kernel");
     return zs::check_launch("head_product_kernel");
 }
@@ -842,53 +895,65 @@ HeadArgs args_of(const zs_head* h, const Plan& p, void* work) {
 }
 
 int32_t launch_rows(const HeadArgs& a, cudaStream_t stream) {
-    ZS_TRY(launch(head_rows_kernel, dim3(1), kRowThreads, stream, "head_rows_kernel", a));
     const int64_t most = 6 * zs::device_sm_count(), blocks = (a.rows + kTile + 7) / 8;
-    return launch(head_gather_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, stream, "head_gather_kernel", a);
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
+    if (a.rows <= kFewRows) return launch(head_gather_kernel<true>, grid, 256, stream, "head_gather_kernel", a);
+    ZS_TRY(launch(head_rows_kernel, dim3(1), kRowThreads, stream, "head_rows_kernel", a));
+    return launch(head_gather_kernel<false>, grid, 256, stream, "head_gather_kernel", a);
 }
 
 template <typename T> constexpr int32_t type_of();
 template <> constexpr int32_t type_of<__half>() { return ZS_F16; }
 template <> constexpr int32_t type_of<__nv_bfloat16>() { return ZS_BF16; }
 
-template <typename T>
+template <typename T, int CTAS>
 int32_t launch_logp(const HeadArgs& a, cudaStream_t stream) {
     CUtensorMap rows, entries;
     ZS_TRY(make_map(&rows, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
-    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 128));
-    const int pairs = pairs_of<T, kLogits>();
+    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, columns_of(CTAS)));
+    const int pairs = pairs_of<T, kLogits, CTAS>();
     if (pairs < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
-    ZS_TRY((launch_product<T, kLogits>(ProductArgs{a, 0, a.vocab, 1}, rows, entries, pairs, stream)));
-    return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 32) / 32)), 1024, stream, "head_join_kernel", a);
+    ZS_TRY((launch_product<T, kLogits, CTAS>(ProductArgs{a, 0, a.vocab, 1}, rows, entries, pairs, stream)));
+    return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 32) / 32)), 512, stream, "head_join_kernel", a);
 }
 
-template <typename T>
+template <typename T, int CTAS>
 int32_t launch_grad(const HeadArgs& a, cudaStream_t stream) {
     // the operands of the three products: H, W and d, along k or across it
     CUtensorMap rows, entries, d_rows, w_across, d_across, h_across;
     ZS_TRY(make_map(&rows, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
-    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 128));
+    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, columns_of(CTAS)));
     ZS_TRY(make_map(&d_rows, type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 128));
     ZS_TRY(make_map(&w_across, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 64));
     ZS_TRY(make_map(&d_across, type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 64));
     ZS_TRY(make_map(&h_across, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 64));
-    const int pairs = pairs_of<T, kGrad>(), pairs_h = pairs_of<T, kDHidden>(), pairs_w = pairs_of<T, kDWeight>();
+    const int pairs = pairs_of<T, kGrad, CTAS>(), pairs_h = pairs_of<T, kDHidden, CTAS>(), pairs_w = pairs_of<T, kDWeight, 2>();
     if (pairs < 1 || pairs_h < 1 || pairs_w < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
     ProductArgs p = {a, 0, 0, 0};
     for (p.first = 0;; p.first += a.piece) {
         p.last = p.first + a.piece >= a.vocab;
         p.count = p.last ? a.vocab - p.first : a.piece;
-        ZS_TRY((launch_product<T, kGrad>(p, rows, entries, pairs, stream)));
-        if (a.dhidden != nullptr) ZS_TRY((launch_product<T, kDHidden>(p, d_rows, w_across, pairs_h, stream)));
-        if (a.dweight != nullptr) ZS_TRY((launch_product<T, kDWeight>(p, d_across, h_across, pairs_w, stream)));
+        ZS_TRY((launch_product<T, kGrad, CTAS>(p, rows, entries, pairs, stream)));
+        if (a.dhidden != nullptr) ZS_TRY((launch_product<T, kDHidden, CTAS>(p, d_rows, w_across, pairs_h, stream)));
+        if (a.dweight != nullptr) ZS_TRY((launch_product<T, kDWeight, 2>(p, d_across, h_across, pairs_w, stream)));
         if (p.last) break;
     }
     if (a.dhidden == nullptr) return ZS_OK;
     const int64_t most = 8 * zs::device_sm_count();
     return launch(head_dhidden_kernel<T>, dim3((unsigned)(a.rows_pad < most ? a.rows_pad : most)), 256, stream,
                   "head_dhidden_kernel", p, (int32_t)pairs_h);
+}
+
+// Calls f with a value of the type, and the CTAs of a tile as a constant: one for up to
+// 128 rows (4 x 32000 x 4096: XX us for YY), two above.
+template <typename F>
+int32_t with_head(const zs_head* h, F f) {
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    if (h->type == ZS_F16) return h->rows <= 128 ? f(__half(), one) : f(__half(), two);
+    return h->rows <= 128 ? f(__nv_bfloat16(), one) : f(__nv_bfloat16(), two);
 }
 
 }  // namespace
@@ -919,7 +984,7 @@ ZS_API int32_t zero_head_logp_async(const zs_head* h, const int64_t* labels, flo
     a.labels = labels;
     a.logp = logp;
     a.saved_out = saved;
-    return h->type == ZS_F16 ? launch_logp<__half>(a, (cudaStream_t)stream) : launch_logp<__nv_bfloat16>(a, (cudaStream_t)stream);
+    return with_head(h, [&](auto t, auto ctas) { return launch_logp<decltype(t), decltype(ctas)::value>(a, (cudaStream_t)stream); });
 }
 
 ZS_API int32_t zero_head_logp_grad_async(const zs_head* h, const int64_t* labels, const float* saved,
@@ -950,7 +1015,7 @@ ZS_API int32_t zero_head_logp_grad_async(const zs_head* h, const int64_t* labels
     a.dhidden_stride = h->rows > 1 ? dhidden_stride : h->width;
     a.dweight = (uint16_t*)dweight;
     a.dweight_stride = h->vocab > 1 ? dweight_stride : h->width;
-    return h->type == ZS_F16 ? launch_grad<__half>(a, (cudaStream_t)stream) : launch_grad<__nv_bfloat16>(a, (cudaStream_t)stream);
+    return with_head(h, [&](auto t, auto ctas) { return launch_grad<decltype(t), decltype(ctas)::value>(a, (cudaStream_t)stream); });
 }
 
 }  // extern "C"

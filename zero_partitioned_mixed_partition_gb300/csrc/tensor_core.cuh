@@ -1,6 +1,6 @@
 // tensor_core.cuh -- what the head's products need of the fifth-generation tensor
-// cores and the tensor copies: a pair of CTAs (two SMs) works on one tile, operands
-// lie in shared memory in the 128-byte swizzle, sums in tensor memory.  Included
+// cores and the tensor copies: CTAS = 2, a pair of CTAs (two SMs), or 1, works on one
+// tile, operands lie in shared memory in the 128-byte swizzle, sums in tensor memory.  Included
 // inside an anonymous namespace after mbar.cuh.
 #pragma once
 
@@ -9,10 +9,16 @@
 // A box of a tensor map at (x, y), x the contiguous coordinate (a multiple of 16
 // bytes), into this CTA's shared memory, counted by a barrier that may be the
 // pair's other CTA's (a shared::cluster address).
+template <int CTAS>
 __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t barrier) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(barrier) : "memory");
+    if (CTAS == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(barrier) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(barrier) : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -39,14 +45,25 @@ __device__ __forceinline__ int32_t load_from_peer(const int32_t* p, uint32_t ran
 
 constexpr uint32_t kTensorColumns = 512;  // of 128 lanes and 32 bits: all there are
 
-// By one warp of each CTA of the pair; the address is written to *at.
+// By one warp of each CTA; the address is written to *at.
+template <int CTAS>
 __device__ __forceinline__ void tensor_alloc(uint32_t* at) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(kTensorColumns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    if (CTAS == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(kTensorColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(kTensorColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
 }
+template <int CTAS>
 __device__ __forceinline__ void tensor_free(uint32_t base) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTensorColumns));
+    if (CTAS == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTensorColumns));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTensorColumns));
 }
 __device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -78,34 +95,49 @@ __device__ __forceinline__ uint64_t operand(const void* p, uint32_t next) {
 // The step of 16 k of an operand's descriptor: 32 bytes along a row, or 16 rows.
 template <bool K_MAJOR> __device__ __forceinline__ uint64_t operand_step() { return (K_MAJOR ? 32 : 2048) >> 4; }
 
-// What an instruction multiplies: A of 256 rows and B of n columns, each half in one
-// CTA of the pair, 16-bit types, fp32 sums.
+// What an instruction multiplies: A of 128 rows to a CTA and B of n columns in all, an
+// even share in each CTA, 16-bit types, fp32 sums.
 template <typename T> constexpr uint32_t operand_type();
 template <> constexpr uint32_t operand_type<__half>() { return 0; }
 template <> constexpr uint32_t operand_type<__nv_bfloat16>() { return 1; }
-template <typename T, bool A_K_MAJOR, bool B_K_MAJOR>
+template <int CTAS, typename T, bool A_K_MAJOR, bool B_K_MAJOR>
 __device__ __forceinline__ uint32_t product_kind(uint32_t n) {
     return 1u << 4 | operand_type<T>() << 7 | operand_type<T>() << 10 | (A_K_MAJOR ? 0u : 1u) << 15 |
-           (B_K_MAJOR ? 0u : 1u) << 16 | (n >> 3) << 17 | (256u >> 4) << 24;
+           (B_K_MAJOR ? 0u : 1u) << 16 | (n >> 3) << 17 | (128u * CTAS >> 4) << 24;
 }
-// sums [+]= A B over 16 k, by one thread of the pair's first CTA.
+// sums [+]= A B over 16 k, by one thread of the (first) CTA.
+template <int CTAS>
 __device__ __forceinline__ void multiply(uint32_t sums, uint64_t a, uint64_t b, uint32_t kind, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(sums), "l"(a), "l"(b), "r"(kind),
-        "r"(add ? 1u : 0u) : "memory");
+    if (CTAS == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(sums), "l"(a), "l"(b), "r"(kind),
+            "r"(add ? 1u : 0u) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(sums), "l"(a), "l"(b), "r"(kind),
+            "r"(add ? 1u : 0u) : "memory");
 }
-// Arrives at the barrier at this place in both CTAs once the thread's products so
-// far are done.
-__device__ __forceinline__ void arrive_after_products(uint64_t* barrier) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_addr(barrier)), "h"((uint16_t)3) : "memory");
-}
-// The same at a barrier of this CTA alone.
+// Arrives at the barrier of this CTA once the thread's products so far are done.
+template <int CTAS>
 __device__ __forceinline__ void signal_after_products(uint64_t* barrier) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(barrier))
-                 : "memory");
+    if (CTAS == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(barrier))
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(barrier))
+                     : "memory");
+}
+// The same at the barrier at this place in every CTA of the tile.
+template <int CTAS>
+__device__ __forceinline__ void arrive_after_products(uint64_t* barrier) {
+    if (CTAS == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_addr(barrier)), "h"((uint16_t)3) : "memory");
+    else
+        signal_after_products<1>(barrier);
 }
 
 // ----------------------------------------------------------------- registers ---
