@@ -1080,7 +1080,7 @@ ZS_API int64_t zero_kernel_launches(void);
  * ZS_CHECKED=1 give libzeroshard_checked.so, whose kernels test every element
  * range they are about to touch against the extent the call was given (the
  * shard's n, or its qwZ block count); a failed test records the first failure
- * -- (site << 48) | first element, site 1-17 naming the kernel and access --
+ * -- (site << 48) | first element, site 1-23 naming the kernel and access --
  * and skips the access instead of trapping.  This call synchronises the
  * device, writes that record (0: none) to *first_fault, clears it, and
  * returns 1 in the checked build; the ordinary build has no checks and
@@ -1090,7 +1090,7 @@ ZS_API int64_t zero_kernel_launches(void);
 ZS_API int32_t zero_debug_checks(uint64_t* first_fault);
 
 /* Debug build: sets how many tries, 0 to 2^20 (the ordinary build's number), the
- * waits of the logits kernels make for their own copies and warps before they
+ * waits of the logits kernels and the head's products make for their own copies and warps before they
  * give up, and returns 1.  With few tries waits run out that would have been met,
  * which shows what a call does then (see zero_token_logp_async).  Synchronises
  * the device.  The ordinary build changes nothing and returns 0.

@@ -137,3 +137,36 @@ def test_gradient_against_differences(zs, cuda_device):
     # the lookup is linear in the table
     slope = float((u[ids] * 1.5 * dout.double()).sum())
     assert abs(float((dtable.double() * u).sum()) - slope) <= 64 * U * float((u[ids] * 1.5 * dout.double()).abs().sum())
+
+
+def test_far_rows(zs, cuda_device):
+    """Rows of the table more than 2^32 bytes from the first."""
+    vocab, width = 70_001, 64
+    table = torch.empty(vocab, 32_768, dtype=torch.bfloat16, device="cuda")[:, :width]
+    table.normal_()
+    ids = torch.tensor([0, vocab - 1, 69_999, 3, vocab - 1], device="cuda")
+    out = torch.empty(5, width, dtype=torch.bfloat16, device="cuda")
+    zs.zero_embed_async(table, ids, out)
+    assert torch.equal(out, table[ids])
+    work = zs.new_embed_work(5, width)
+    zs.zero_embed_grad_async(ids, out, table, work)
+    want = torch.zeros(vocab, width, dtype=torch.bfloat16, device="cuda")
+    zs.zero_embed_grad_async(ids, out, want, work)
+    assert torch.equal(table, want) and torch.equal(want[3], out[3]) and torch.equal(want[vocab - 1], (out[1].float() * 2).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("n", [7, 8, 9, 255, 256, 257, 8191, 8192, 32768, 65535, 65536, 65537])
+def test_runs_across_chunks(zs, cuda_device, n):
+    """One id from end to end, two that meet anywhere, and one on a chunk's edge: small
+    integers, so that every order gives the same sum."""
+    width, vocab = 40, 9
+    dout = (torch.arange(n, device="cuda")[:, None] * 7 + torch.arange(width, device="cuda")[None]) % 5 - 2
+    dout = dout.float()
+    work = zs.new_embed_work(n, width)
+    for cut in (0, 1, n // 2, n - 1, n // 64 * 64, n // 16 * 16):
+        ids = (torch.arange(n, device="cuda") >= cut).long() * 8
+        ids = ids[torch.randperm(n, device="cuda")]
+        dtable = torch.full((vocab, width), 7.0, device="cuda")
+        zs.zero_embed_grad_async(ids, dout, dtable, work)
+        want = torch.zeros(vocab, width, device="cuda").double().index_add_(0, ids, dout.double())
+        assert torch.equal(dtable.double(), want)

@@ -291,3 +291,70 @@ def test_gradient_against_differences(zs, cuda_device):
         mine = float((dh.double() * u).sum() + (dw.double() * v).sum())
         size = float((dh.double() * u).abs().sum() + (dw.double() * v).abs().sum())
         assert abs(mine - slope) <= 3 * HALF[torch.float16] * size
+
+
+@pytest.mark.parametrize("rows", [127, 128, 129, 1023, 1024, 1025, 8192, 8193, 20000])
+def test_numbers_of_rows(zs, cuda_device, rows):
+    """Around the numbers of rows at which the kernels change, with most rows left out."""
+    vocab, width, dtype = 400, 64, torch.bfloat16
+    h, w, y, g = _inputs(rows, vocab, width, dtype, rows, exact=True)
+    y[torch.rand(rows, generator=g, device="cuda") < 0.7] = -1
+    valid = y >= 0
+    x, _, lp, ref, yy = _reference(h, w, y, 1.0, valid)
+    e = (400 + vocab / 128) * U
+    logp, saved = torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+    work = zs.new_head_work(rows, width, vocab)
+    zs.zero_head_logp_async(h, w, y, logp, work, saved=saved)
+    spread = x.amax(1) - x[torch.arange(rows, device="cuda"), yy]
+    _close(logp, ref, torch.where(valid, e + 4 * U * ref.abs() + 4 * U * spread, 0.0), "logp")
+    dlogp = torch.randn(rows, generator=g, device="cuda") / rows
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    zs.zero_head_logp_grad_async(h, w, y, saved, dlogp, dh, dw, work)
+    c = torch.where(valid, dlogp.double(), 0.0)
+    d = -lp.exp() * c[:, None]
+    d[torch.arange(rows, device="cuda"), yy] += c
+    for got, want, size in ((dh, d @ w.double(), d.abs() @ w.double().abs()),
+                            (dw, d.t() @ h.double(), d.abs().t() @ h.double().abs())):
+        tol = (HALF[dtype] * 1.01 + 2 * e + 400 * U + (rows + vocab) / 2 * U) * size * 1.02 + HALF[dtype] * 1.01 * want.abs() + 1e-30
+        _close(got, want, tol, "gradient")
+    assert (dh[~valid] == 0).all()
+
+
+def test_infinite_and_nan_dlogp(zs, cuda_device):
+    """One row's coefficient that is no number leaves the other rows' gradients as they are."""
+    rows, vocab, width, dtype = 40, 600, 64, torch.float16
+    h, w, y, g = _inputs(rows, vocab, width, dtype, 21)
+    work = zs.new_head_work(rows, width, vocab)
+    logp, saved = torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+    zs.zero_head_logp_async(h, w, y, logp, work, saved=saved)
+    dlogp = torch.randn(rows, generator=g, device="cuda") * 1e-6
+    keep = torch.arange(rows, device="cuda") != 7
+    zeroed = dlogp.clone()
+    zeroed[7] = 0.0
+    want = torch.empty_like(h)
+    zs.zero_head_logp_grad_async(h, w, y, saved, zeroed, want, None, work)
+    for bad in (math.inf, -math.inf, math.nan):
+        dlogp[7] = bad
+        dh, dw = torch.empty_like(h), torch.empty_like(w)
+        zs.zero_head_logp_grad_async(h, w, y, saved, dlogp, dh, dw, work)
+        assert torch.equal(dh[keep], want[keep]) and not dh[7].isfinite().any() and not dw.isfinite().all()
+
+
+def test_large_offsets(zs, cuda_device):
+    """A vocabulary matrix and its gradient of more than 2^32 bytes, rows far apart."""
+    rows, vocab, width, stride = 5, 70_001, 64, 32_768
+    w = torch.empty(vocab, stride, dtype=torch.bfloat16, device="cuda")[:, :width]
+    dw = torch.empty(vocab, stride, dtype=torch.bfloat16, device="cuda")[:, :width]
+    h, small, y, g = _inputs(rows, vocab, width, torch.bfloat16, 2, exact=True)
+    w.copy_(small)
+    y[0] = vocab - 1
+    logp, saved, want = (torch.empty(n, device="cuda") for n in (rows, 2 * rows, rows))
+    work = zs.new_head_work(rows, width, vocab)
+    zs.zero_head_logp_async(h, small, y, want, work, saved=saved)
+    zs.zero_head_logp_async(h, w, y, logp, work, saved=saved)
+    assert torch.equal(logp, want)
+    a, b, c = torch.empty_like(h), torch.empty_like(h), torch.empty_like(small)
+    ones = torch.ones(rows, device="cuda")
+    zs.zero_head_logp_grad_async(h, small, y, saved, ones, a, c, work)
+    zs.zero_head_logp_grad_async(h, w, y, saved, ones, b, dw, work)
+    assert torch.equal(a, b) and torch.equal(c, dw)

@@ -8,6 +8,8 @@ embedding's rows, out, dout and d, dx, the table's gradient twice.  Rounding of
 inputs moves logits by about 2^-8 of their spread (3 here, so a logp by about 0.01 and
 a p by 1 %); the sums of independent parts stay below a few of these: 4 % in norm."""
 import math
+import os
+import sys
 
 import pytest
 import torch
@@ -15,6 +17,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 BF16 = torch.bfloat16
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
 class Step:
@@ -132,3 +135,51 @@ def test_given_stream(zs, cuda_device):
     zs.zero_layer_norm_async(s.x, s.gamma, s.beta, s.y, stream=stream)
     stream.synchronize()
     assert torch.equal(s.y, want)
+
+
+def test_example(zs, cuda_device):
+    """The supervised example runs every step, repeatably, and its first gradients are autograd's."""
+    import finetune_step
+    mean, ctrl = finetune_step.run_supervised(steps=6, vocab=2003, width=128, tokens=360)
+    again, _ = finetune_step.run_supervised(steps=6, vocab=2003, width=128, tokens=360)
+    assert ctrl["step"] == 6 and ctrl["skipped"] == 0 and mean.isfinite().all() and torch.equal(mean, again)
+    n, width = 360, 128
+    model = finetune_step.TiedModel(2003, width, n, 3)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    ids, label = (torch.randint(0, 2003, (n,), generator=g, device="cuda") for _ in range(2))
+    dlogp = -torch.rand(n, generator=g, device="cuda") / n
+    ctrl = zs.new_ctrl()
+    zs.zero_ctrl_init(ctrl, 256.0)
+    model.gradients(ids, label, dlogp, ctrl)
+    table, gamma, beta = (t.double().requires_grad_() for t in (model.table, model.master["gamma"], model.master["beta"]))
+    out = torch.nn.functional.layer_norm(table[ids] * model.scale, (width,), gamma, beta, 1e-5)
+    lp = torch.log_softmax(out @ table.t(), 1)[torch.arange(n, device="cuda"), label]
+    ((lp * dlogp.double()).sum() * 256.0).backward()
+    for got, want in ((model.grad["table"], table.grad), (model.grad["gamma"], gamma.grad), (model.grad["beta"], beta.grad)):
+        assert (got.double() - want).norm() <= 0.04 * want.norm()
+
+
+def test_first_calls_of_a_process_in_a_graph():
+    """Captured before anything has run: nothing in a call's set-up disturbs a capture."""
+    import subprocess
+    code = """
+import sys; sys.path[:0] = ['tests', '.']
+import torch
+from zero_partitioned_mixed_partition_gb300 import binding as zs
+from test_gpu_model_ends import Step
+s = Step(zs, 300, 700, 128, 5)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    s.run()
+graph.replay()
+torch.cuda.synchronize()
+got = s.outputs()
+s.run()
+assert all(torch.equal(a, b) for a, b in zip(got, s.outputs())) and s.logp.isfinite().all()
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, (r.stdout + r.stderr)[-1500:]

@@ -161,3 +161,45 @@ def test_gradient_against_differences(zs, cuda_device):
         size = sum(float(t.abs().sum()) for t in parts)
         # the terms' fp32 errors, and the difference's own (1e-6 in 64 bits)
         assert abs(sum(float(t.sum()) for t in parts) - slope) <= (77 * 4 * U + 1e-6) * size
+
+
+@pytest.mark.parametrize("x_type", TYPES)
+@pytest.mark.parametrize("p_type", TYPES)
+@pytest.mark.parametrize("offset", [0, 1])
+def test_parameter_types_and_places(zs, cuda_device, x_type, p_type, offset):
+    """Every pair of types, parameters on and off a vector boundary, with and without each."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    rows, width = 37, 520
+    x, dy = (torch.randn(rows, width, generator=g, device="cuda").to(x_type) for _ in range(2))
+    gamma, beta, dgamma, dbeta = (torch.randn(width + 1, generator=g, device="cuda").to(p_type)[offset:offset + width] for _ in range(4))
+    work = zs.new_layer_norm_work(rows, width)
+    xd, m = x.double(), x.double().mean(1, keepdim=True)
+    r = 1.0 / ((xd - m).square().mean(1, keepdim=True) + 1e-5).sqrt()
+    xh = (xd - m) * r
+    y, saved, dx = torch.empty_like(x), torch.empty(rows, 2, device="cuda"), torch.empty_like(x)
+    for ga, be in ((gamma, beta), (gamma, None), (None, beta)):
+        gd = ga.double() if ga is not None else torch.ones(width, device="cuda").double()
+        bd = be.double() if be is not None else torch.zeros(width, device="cuda").double()
+        zs.zero_layer_norm_async(x, ga, be, y, saved=saved)
+        want = xh * gd + bd
+        _close(y, want, 2 * (width + 16) * U * (xh.abs() + 1) * gd.abs() + 2 * U * bd.abs() + HALF[x_type] * 1.01 * want.abs() + TINY[x_type], "y")
+        if ga is None:
+            continue
+        zs.zero_layer_norm_grad_async(dy, x, ga, saved, dx, dgamma, dbeta, work)
+        a = dy.double() * gd
+        want = r * (a - a.mean(1, keepdim=True) - xh * (a * xh).mean(1, keepdim=True))
+        size = r * (a.abs() + a.abs().mean(1, keepdim=True) + xh.abs() * (a * xh).abs().mean(1, keepdim=True))
+        _close(dx, want, (4 * width + 64) * U * size + HALF[x_type] * 1.01 * want.abs() + TINY[x_type], "dx")
+        for got, t in ((dgamma, dy.double() * xh), (dbeta, dy.double())):
+            _close(got, t.sum(0), (2 * width + rows + 64) * U * (t.abs() + dy.double().abs()).sum(0) + HALF[p_type] * 1.01 * t.sum(0).abs() + TINY[p_type], "params")
+
+
+def test_far_rows(zs, cuda_device):
+    """Rows more than 2^32 bytes from the first."""
+    x = torch.empty(70_000, 32_768, dtype=torch.bfloat16, device="cuda")[:, :64]
+    x.normal_()
+    y, want = torch.empty_like(x), torch.empty(70_000, 64, dtype=torch.bfloat16, device="cuda")
+    zs.zero_layer_norm_async(x.contiguous(), None, None, want)
+    zs.zero_layer_norm_async(x, None, None, y)
+    assert torch.equal(y, want)

@@ -26,6 +26,8 @@ namespace {
 #include "elem.cuh"
 #include "launch.cuh"
 
+[[maybe_unused]] constexpr uint32_t kSiteHeadRow = 22, kSiteHeadSum = 23;
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowestFloat = -3.402823466e38f;
 
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
         uint4* to = slot >= 0             ? reinterpret_cast<uint4*>(a.compact + (int64_t)slot * a.width)
                     : a.dhidden != nullptr ? reinterpret_cast<uint4*>(a.dhidden + i * a.dhidden_stride)
                                            : nullptr;
-        if (to != nullptr) {
+        if (to != nullptr && ZS_RANGE_OK(kSiteHeadRow, slot >= 0 ? slot : i, 1, slot >= 0 ? a.rows_pad : a.rows)) {
             for (int32_t k0 = lane; k0 < vectors; k0 += 4 * 32) {
                 uint4 x[4];
 #pragma unroll
@@ -617,7 +619,9 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 }
                 tensor_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(peer_addr(&ring.sums_empty[set], 0));
+                // (not after a wait that ran out: an arrival out of turn could stand for another
+                // warp's, and its sums would be written over unread)
+                if (ok && lane == 0) arrive_at(peer_addr(&ring.sums_empty[set], 0));
             }
             if (!ok) {
 #pragma unroll
@@ -663,7 +667,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 }
                 // (rows that only fill the tile are 0, whatever W holds)
                 const bool none = coef == 0.0f;
-                store_rows<2>(staging, lane, reinterpret_cast<char*>(a.d + r * a.piece + j0), 128, [&](int j) {
+                const bool in = ZS_RANGE_OK(kSiteHeadSum, r, 1, a.rows_pad) && ZS_RANGE_OK(kSiteHeadSum, j0, 128, a.piece);
+                store_rows<2>(staging, lane, in ? reinterpret_cast<char*>(a.d + r * a.piece + j0) : nullptr, 128, [&](int j) {
                     return none ? make_uint4(0, 0, 0, 0)
                                 : make_uint4(narrow2<T>(v[j], v[j + 1]), narrow2<T>(v[j + 2], v[j + 3]),
                                              narrow2<T>(v[j + 4], v[j + 5]), narrow2<T>(v[j + 6], v[j + 7]));
@@ -672,7 +677,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 const int64_t left = a.width - j0;
                 const int32_t columns = left < 128 ? (int32_t)left : 128;
                 if (MODE == kDHidden && !(w.split == 1 && p.first == 0 && p.last)) {
-                    float* const row = r < live ? (float*)a.part + ((int64_t)t.part * w.m_tiles * kTile + r) * a.width + j0 : nullptr;
+                    const int64_t at = (int64_t)t.part * w.m_tiles * kTile + r;
+                    float* const row = r < live && ZS_RANGE_OK(kSiteHeadSum, at, 1, a.sums_room) ? (float*)a.part + at * a.width + j0 : nullptr;
                     if (p.first > 0 && row != nullptr) {
 #pragma unroll
                         for (int i = 0; i < 128; i += 4) {
@@ -689,8 +695,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 } else {
                     const float unscale = a.counts->unscale;
                     uint16_t* row = nullptr;
-                    if (MODE == kDHidden && r < live) row = a.dhidden + a.index[r] * a.dhidden_stride + j0;
-                    if (MODE == kDWeight && r < p.count) row = a.dweight + (p.first + r) * a.dweight_stride + j0;
+                    if (MODE == kDHidden && r < live && ZS_RANGE_OK(kSiteHeadRow, a.index[r], 1, a.rows)) row = a.dhidden + a.index[r] * a.dhidden_stride + j0;
+                    if (MODE == kDWeight && r < p.count && ZS_RANGE_OK(kSiteHeadRow, p.first + r, 1, a.vocab)) row = a.dweight + (p.first + r) * a.dweight_stride + j0;
                     store_rows<2>(staging, lane, reinterpret_cast<char*>(row), columns, [&](int j) {
                         uint32_t x[4];
 #pragma unroll
@@ -710,16 +716,16 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
     // issued have counted their copies (of a step that one of the two did not reach,
     // that one's are made up for).
     if ((load_from_peer(&ring.failed, 0) | load_from_peer(&ring.failed, CTAS - 1)) != 0 && rank == 0 && threadIdx.x == 32) {
-            signal_after_products<CTAS>(&ring.done);
-            drain(&ring.done, 0);
-            const int32_t mine = ring.issued, other = load_from_peer(&ring.issued, CTAS - 1);
-            const int32_t most = mine > other ? mine : other;
-            for (int32_t i = most > kStages ? most - kStages : 0; i < most; ++i) {
-                const int s = i % kStages;
-                if (i >= mine) mbar_expect(&ring.full[s], (uint32_t)load_from_peer((const int32_t*)&ring.bytes[s], CTAS - 1));
-                if (i >= other) mbar_give(&ring.full[s], ring.bytes[s]);
-                drain(&ring.full[s], (uint32_t)(i / kStages) & 1u);
-            }
+        signal_after_products<CTAS>(&ring.done);
+        drain(&ring.done, 0);
+        const int32_t mine = ring.issued, other = load_from_peer(&ring.issued, CTAS - 1);
+        const int32_t most = mine > other ? mine : other;
+        for (int32_t i = most > kStages ? most - kStages : 0; i < most; ++i) {
+            const int s = i % kStages;
+            if (i >= mine) mbar_expect(&ring.full[s], (uint32_t)load_from_peer((const int32_t*)&ring.bytes[s], CTAS - 1));
+            if (i >= other) mbar_give(&ring.full[s], ring.bytes[s]);
+            drain(&ring.full[s], (uint32_t)(i / kStages) & 1u);
+        }
     }
     __syncwarp();
     __syncthreads();
@@ -852,7 +858,7 @@ int32_t launch_product(const ProductArgs& p, const CUtensorMap& map_a, const CUt
 }
 
 bool valid_stride(int64_t rows, int64_t width, int64_t stride) {
-    return rows <= 1 || (stride >= width && stride <= 1ll << 40);
+    return rows <= 1 || (stride >= width && stride <= 1ll << 38);  // (tensor maps: bytes below 2^40)
 }
 
 int32_t check_head(const zs_head* h) {
