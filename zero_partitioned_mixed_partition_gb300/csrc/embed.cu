@@ -443,9 +443,9 @@ Plan plan_of(int64_t tokens, int64_t width) {
     return p;
 }
 
-// Whether every row starts on a boundary of 16 bytes and has whole vectors of them.
-bool vectors_fit(const void* p, int64_t stride, int64_t width, int64_t size) {
-    return zs::aligned_to(p, 16) && stride * size % 16 == 0 && width * size % 16 == 0;
+// Whether every row starts on a boundary of `bytes` and has whole vectors of them.
+bool vectors_fit(const void* p, int64_t stride, int64_t width, int64_t size, int64_t bytes = 16) {
+    return zs::aligned_to(p, (uintptr_t)bytes) && stride * size % bytes == 0 && width * size % bytes == 0;
 }
 
 template <typename T, int V>
@@ -522,8 +522,12 @@ ZS_API int32_t zero_embed_async(const zs_embed* e, void* out, int64_t out_stride
     a.out_stride = e->tokens > 1 ? out_stride : e->width;
     return with_elem(e->type, [&](auto t) {
         using T = decltype(t);
-        const bool wide = vectors_fit(a.table, a.table_stride, a.width, sizeof(T)) && vectors_fit(out, a.out_stride, a.width, sizeof(T));
-        return wide ? launch_lookup<T, 16 / sizeof(T)>(a, (cudaStream_t)stream) : launch_lookup<T, 1>(a, (cudaStream_t)stream);
+        auto fit = [&](int64_t bytes) {
+            return vectors_fit(a.table, a.table_stride, a.width, sizeof(T), bytes) && vectors_fit(out, a.out_stride, a.width, sizeof(T), bytes);
+        };
+        if (fit(16)) return launch_lookup<T, 16 / sizeof(T)>(a, (cudaStream_t)stream);
+        // (two elements of 16 bits to an access where rows allow it)
+        return fit(4) ? launch_lookup<T, 4 / sizeof(T)>(a, (cudaStream_t)stream) : launch_lookup<T, 1>(a, (cudaStream_t)stream);
     });
 }
 
@@ -570,8 +574,11 @@ ZS_API int32_t zero_embed_grad_async(const zs_embed* e, const void* dout, int64_
             constexpr int V = 16 / sizeof(T);
             const bool wide = vectors_fit(dout, a.dout_stride, a.width, sizeof(T)) &&
                               vectors_fit(dtable, a.dtable_stride, a.width, sizeof(G));
-            return wide ? launch_grad<T, G, V>(a, p.chunks, (cudaStream_t)stream)
-                        : launch_grad<T, G, 1>(a, p.chunks, (cudaStream_t)stream);
+            if (wide) return launch_grad<T, G, V>(a, p.chunks, (cudaStream_t)stream);
+            if constexpr (sizeof(T) == 2)  // (two elements to an access where rows allow it)
+                if (vectors_fit(dout, a.dout_stride, a.width, 2, 4) && vectors_fit(dtable, a.dtable_stride, a.width, sizeof(G), 2 * sizeof(G)))
+                    return launch_grad<T, G, 2>(a, p.chunks, (cudaStream_t)stream);
+            return launch_grad<T, G, 1>(a, p.chunks, (cudaStream_t)stream);
         };
         return dtable_type == ZS_F32 ? go(float()) : go(t);
     });

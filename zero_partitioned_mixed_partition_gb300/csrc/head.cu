@@ -48,6 +48,7 @@ struct Counts {
     int32_t live;     // rows that are not left out
     float scale;      // d's power of 2
     float unscale;    // its inverse
+    int32_t split;    // parts of dH's sums
 };
 // A live row.
 struct __align__(16) Row {
@@ -129,7 +130,28 @@ struct HeadArgs {
     float* label_logit;
     uint16_t* d;                 // [rows_pad][piece]
     int64_t rows_pad, tiles, piece, sums_room;
+    int32_t pairs;               // that make dH
 };
+
+constexpr int kStep = 64;  // k of a stage of the products' ring
+__host__ __device__ constexpr int32_t tiles_of(int64_t n) { return (int32_t)((n + kTile - 1) / kTile); }
+__host__ __device__ constexpr int32_t steps_of(int64_t n) { return (int32_t)((n + kStep - 1) / kStep); }
+
+// The number of parts of dH's sums: with few tiles the CTA pairs would be idle.  The least
+// cost, estimated in steps: rounds of tiles, each with a start and an end of some 12 steps,
+// and what the parts cost to write and read.  A lane of the warp weighs a number.
+__device__ int32_t split_of(const HeadArgs& a, int32_t live, int lane) {
+    const int32_t m_tiles = tiles_of(live > 0 ? live : 1), tiles = m_tiles * tiles_of(a.width);
+    const int32_t steps = steps_of(a.vocab < a.piece ? a.vocab : a.piece);  // (the same for every piece: the first one's)
+    const int32_t room = (int32_t)(a.sums_room / (m_tiles * kTile)), s = lane + 1;
+    float cost = 3.4e38f;
+    if (s == 1 || (s <= kMaxSplit && s <= room && s * 8 <= steps))
+        cost = (float)((tiles * s + a.pairs - 1) / a.pairs) * ((float)((steps + s - 1) / s) + 12.0f) +
+               (s > 1 ? 0.3f * (float)(tiles * s) : 0.0f);
+    float least = cost;
+    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    return __ffs(__ballot_sync(0xffffffffu, cost == least));
+}
 
 constexpr int kRowThreads = 1024;
 // Rows of one pass of the rows kernel's block; up to so many are numbered by every block of
@@ -137,22 +159,26 @@ constexpr int kRowThreads = 1024;
 constexpr int kRowsEach = 8, kFewRows = 1024;
 
 // Numbers live rows in their order, EACH to a thread, whose loads are under way together,
-// and writes what `emit` is called with: a row, its label and dlogp, its number or -1.  Called by the
+// and calls `emit` with a row, its number or -1, and what the products need of it.  Called by the
 // whole block of THREADS; returns the number of live rows up to here.
 template <int THREADS, int EACH, typename F>
 __device__ int32_t number_rows(const HeadArgs& a, int64_t from, int32_t before, F emit) {
     constexpr int kWarps = THREADS / 32, kCounts = EACH * kWarps;
+    const float factor = loss_scale_of(a.ctrl) * a.it;
     static_assert(kCounts % 32 == 0, "a warp scans the counts");
     __shared__ int32_t s_count[kCounts + 1];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int64_t label[EACH];
-    float dlogp[EACH];
+    float dlogp[EACH], top[EACH], log_sum[EACH];
     uint32_t votes[EACH];
 #pragma unroll
     for (int k = 0; k < EACH; ++k) {
         const int64_t i = from + k * THREADS + threadIdx.x;
+        const bool grad = i < a.rows && a.dlogp != nullptr;
         label[k] = i < a.rows ? a.labels[i] : -1;
-        dlogp[k] = i < a.rows && a.dlogp != nullptr ? a.dlogp[i] : 1.0f;
+        dlogp[k] = grad ? a.dlogp[i] : 1.0f;
+        top[k] = grad ? a.saved[2 * i] : 0.0f;
+        log_sum[k] = grad ? a.saved[2 * i + 1] : 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < EACH; ++k) {
@@ -188,21 +214,12 @@ __device__ int32_t number_rows(const HeadArgs& a, int64_t from, int32_t before, 
         const int64_t i = from + k * THREADS + threadIdx.x;
         if (i >= a.rows) break;
         const int32_t r = s_count[k * kWarps + warp] + __popc(votes[k] & ((1u << lane) - 1u));
-        emit(i, label[k], dlogp[k], votes[k] >> lane & 1u ? r : -1);
+        // (a row of nothing but -inf has no gradient)
+        const float coef = a.dlogp == nullptr || log_sum[k] == -__int_as_float(0x7f800000) ? 0.0f : factor * dlogp[k];
+        emit(i, votes[k] >> lane & 1u ? r : -1, Row{top[k], log_sum[k], coef, (int32_t)label[k]});
     }
     __syncthreads();
     return all;
-}
-// What the products need of a live row.
-__device__ __forceinline__ Row row_of(const HeadArgs& a, int64_t i, int64_t label, float dlogp, float factor) {
-    Row row = {0.0f, 0.0f, 0.0f, (int32_t)label};
-    if (a.dlogp != nullptr) {
-        row.top = a.saved[2 * i];
-        row.log_sum = a.saved[2 * i + 1];
-        // (a row of nothing but -inf has no gradient)
-        row.coef = row.log_sum == -__int_as_float(0x7f800000) ? 0.0f : factor * dlogp;
-    }
-    return row;
 }
 // From the largest finite |c| of each thread: the numbers, and the power of 2 that takes it
 // to [2^14, 2^15).  Called by the whole block of THREADS.
@@ -212,11 +229,12 @@ __device__ void write_counts(const HeadArgs& a, int32_t live, float top) {
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (threadIdx.x % 32 == 0) s_top[threadIdx.x / 32] = top;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < 32) {
+        const int32_t split = a.dlogp != nullptr ? split_of(a, live, threadIdx.x) : 1;
         for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, s_top[w]);
         int e = top > 0.0f ? 14 - ilogbf(top) : 0;
         e = e > 120 ? 120 : e < -120 ? -120 : e;
-        *a.counts = Counts{live, scalbnf(1.0f, e), scalbnf(1.0f, -e)};
+        if (threadIdx.x == 0) *a.counts = Counts{live, scalbnf(1.0f, e), scalbnf(1.0f, -e), split};
     }
 }
 __device__ __forceinline__ float larger_finite(float top, float c) {
@@ -227,14 +245,12 @@ __device__ __forceinline__ float larger_finite(float top, float c) {
 __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const __grid_constant__ HeadArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    const float factor = loss_scale_of(a.ctrl) * a.it;
     float top = 0.0f;
     int32_t live = 0;
     for (int64_t from = 0; from < a.rows; from += kRowsEach * kRowThreads)
-        live = number_rows<kRowThreads, kRowsEach>(a, from, live, [&](int64_t i, int64_t label, float dlogp, int32_t r) {
+        live = number_rows<kRowThreads, kRowsEach>(a, from, live, [&](int64_t i, int32_t r, const Row& row) {
             a.slot[i] = r;
             if (r < 0) return;
-            const Row row = row_of(a, i, label, dlogp, factor);
             top = larger_finite(top, row.coef);
             a.index[r] = (int32_t)i;
             a.row[r] = row;
@@ -254,12 +270,10 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
     const int32_t vectors = (int32_t)(a.width / 8);
     int32_t live;
     if (FEW) {
-        const float factor = loss_scale_of(a.ctrl) * a.it;
         float top = 0.0f;
-        live = number_rows<256, kFewRows / 256>(a, 0, 0, [&](int64_t i, int64_t label, float dlogp, int32_t r) {
+        live = number_rows<256, kFewRows / 256>(a, 0, 0, [&](int64_t i, int32_t r, const Row& row) {
             s_slot[i] = r;
             if (r < 0 || blockIdx.x != 0) return;
-            const Row row = row_of(a, i, label, dlogp, factor);
             top = larger_finite(top, row.coef);
             a.index[r] = (int32_t)i;
             a.row[r] = row;
@@ -312,7 +326,6 @@ __device__ __forceinline__ float infinity() { return __int_as_float(0x7f800000);
 //   kDWeight   d^T H: the piece's rows of dW
 enum { kLogits, kGrad, kDHidden, kDWeight };
 
-constexpr int kStep = 64;                                   // k of a stage of the ring
 constexpr int kRowBytes = kStep * 2;                        // of an operand's row in a stage
 constexpr int kBoxBytes = 64 * kRowBytes;                   // 64 m of 64 k, across k
 constexpr int kBytesA = 128 * kRowBytes;                    // A's stage in a CTA
@@ -344,27 +357,8 @@ struct ProductArgs {
 struct Tiles {
     int32_t m_tiles, n_tiles, split, steps;  // steps of kStep in the whole sum
 };
-// The number of parts of dH's sums: with few tiles the CTA pairs would be idle.
-// Estimated in steps: rounds of tiles, each with a start and an end of some 12 steps,
-// and what the parts cost to write and read.
-__device__ int32_t split_of(int32_t tiles, int32_t steps, int32_t pairs, int32_t room) {
-    int32_t best = 1;
-    float least = 3.4e38f;
-    for (int32_t s = 1; s <= kMaxSplit && s <= room && s * 8 <= steps; ++s) {
-        const float rounds = (float)((tiles * s + pairs - 1) / pairs);
-        const float cost = rounds * ((float)((steps + s - 1) / s) + 12.0f) + (s > 1 ? 0.3f * (float)(tiles * s) : 0.0f);
-        if (cost < least) {
-            least = cost;
-            best = s;
-        }
-    }
-    return best;
-}
-__device__ __forceinline__ int32_t tiles_of(int64_t n) { return (int32_t)((n + kTile - 1) / kTile); }
-__device__ __forceinline__ int32_t steps_of(int64_t n) { return (int32_t)((n + kStep - 1) / kStep); }
-
 template <int MODE>
-__device__ __forceinline__ Tiles work_of(const ProductArgs& p, int32_t live, int32_t pairs) {
+__device__ __forceinline__ Tiles work_of(const ProductArgs& p, int32_t live) {
     Tiles w;
     w.split = 1;
     if (MODE == kLogits || MODE == kGrad) {
@@ -375,9 +369,7 @@ __device__ __forceinline__ Tiles work_of(const ProductArgs& p, int32_t live, int
         w.m_tiles = tiles_of(live);
         w.n_tiles = tiles_of(p.h.width);
         w.steps = steps_of(p.count);
-        // (the same for every piece: the first one's number of steps)
-        const int64_t whole = p.h.vocab < p.h.piece ? p.h.vocab : p.h.piece;
-        if (live > 0) w.split = split_of(w.m_tiles * w.n_tiles, steps_of(whole), pairs, (int32_t)(p.h.sums_room / (w.m_tiles * kTile)));
+        w.split = p.h.counts->split;
     } else {
         w.m_tiles = tiles_of(p.count);
         w.n_tiles = tiles_of(p.h.width);
@@ -514,7 +506,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
     griddep_wait();
     const uint32_t sums = ring.sums;
     const int32_t live = a.counts->live;
-    const Tiles w = work_of<MODE>(p, live, pairs);
+    const Tiles w = work_of<MODE>(p, live);
     const int32_t units = w.m_tiles * w.n_tiles * w.split;
 
     if (warp < 4) give_registers<kFewRegisters>();
@@ -777,11 +769,11 @@ __global__ void __launch_bounds__(512) head_join_kernel(const __grid_constant__ 
 
 // Joins the parts of dH's sums: a block to a row.
 template <typename T>
-__global__ void __launch_bounds__(256) head_dhidden_kernel(const __grid_constant__ ProductArgs p, int32_t pairs) {
+__global__ void __launch_bounds__(256) head_dhidden_kernel(const __grid_constant__ ProductArgs p) {
     griddep_wait();
     const HeadArgs& a = p.h;
     const int32_t live = a.counts->live;
-    const Tiles w = work_of<kDHidden>(p, live, pairs);
+    const Tiles w = work_of<kDHidden>(p, live);
     if (w.split == 1 && p.first == 0) return;  // (one piece: the product wrote dH)
     const float unscale = a.counts->unscale;
     const int64_t part = (int64_t)w.m_tiles * kTile * a.width;
@@ -925,7 +917,7 @@ int32_t launch_logp(const HeadArgs& a, cudaStream_t stream) {
 }
 
 template <typename T, int CTAS>
-int32_t launch_grad(const HeadArgs& a, cudaStream_t stream) {
+int32_t launch_grad(HeadArgs a, cudaStream_t stream) {
     // the operands of the three products: H, W and d, along k or across it
     CUtensorMap rows, entries, d_rows, w_across, d_across, h_across;
     ZS_TRY(make_map(&rows, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
@@ -936,6 +928,7 @@ int32_t launch_grad(const HeadArgs& a, cudaStream_t stream) {
     ZS_TRY(make_map(&h_across, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 64));
     const int pairs = pairs_of<T, kGrad, CTAS>(), pairs_h = pairs_of<T, kDHidden, CTAS>(), pairs_w = pairs_of<T, kDWeight, 2>();
     if (pairs < 1 || pairs_h < 1 || pairs_w < 1) return ZS_ERR_CUDA;
+    a.pairs = pairs_h;
     ZS_TRY(launch_rows(a, stream));
     ProductArgs p = {a, 0, 0, 0};
     for (p.first = 0;; p.first += a.piece) {
@@ -949,7 +942,7 @@ int32_t launch_grad(const HeadArgs& a, cudaStream_t stream) {
     if (a.dhidden == nullptr) return ZS_OK;
     const int64_t most = 8 * zs::device_sm_count();
     return launch(head_dhidden_kernel<T>, dim3((unsigned)(a.rows_pad < most ? a.rows_pad : most)), 256, stream,
-                  "head_dhidden_kernel", p, (int32_t)pairs_h);
+                  "head_dhidden_kernel", p);
 }
 
 // Calls f with a value of the type, and the CTAs of a tile as a constant: one for up to

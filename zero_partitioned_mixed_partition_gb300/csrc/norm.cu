@@ -557,13 +557,13 @@ int32_t with_warps(int warps, F f) {
     default: return f(std::integral_constant<int, 16>());
     }
 }
-// Whether rows of these matrices (row strides in elements) and the parameters can be
-// accessed as 16-byte vectors.
+// Whether rows of these matrices (row strides in elements) can be accessed as vectors of v
+// elements, and the parameters next to them.
 template <typename... M>
-bool vectors_fit(int64_t width, int64_t size, const void* gamma, const void* beta, M... matrices) {
-    const int64_t v = 16 / size;
+bool vectors_fit(int v, int64_t width, int64_t size, const void* gamma, const void* beta, M... matrices) {
+    const uintptr_t bytes = (uintptr_t)(v * size);
     if (width % v != 0 || !zs::aligned_to(gamma, 16) || !zs::aligned_to(beta, 16)) return false;
-    auto fits = [&](const void* p, int64_t stride) { return zs::aligned_to(p, 16) && stride % v == 0; };
+    auto fits = [&](const void* p, int64_t stride) { return zs::aligned_to(p, bytes) && stride % v == 0; };
     return (fits(matrices.first, matrices.second) && ...);
 }
 struct Matrix {
@@ -589,11 +589,17 @@ int32_t launch_long(const NormArgs& a, cudaStream_t stream, T) {
 template <typename T, typename P>
 int32_t launch_forward(const NormArgs& a, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T), M = 4;
-    const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, a.beta, Matrix{a.x, a.x_stride}, Matrix{a.y, a.y_stride});
+    auto fit = [&](int v) { return vectors_fit(v, a.width, sizeof(T), a.gamma, a.beta, Matrix{a.x, a.x_stride}, Matrix{a.y, a.y_stride}); };
+    const bool wide = fit(V);
     const Shape s = shape_of(a.width, wide ? V : 1, wide ? M : kElements);
     if (s.warps == 0) return launch_long(a, stream, T());
     if (!wide)
-        return with_warps(s.warps, [&](auto w) { return launch_rows<T, P, 1, kElements, decltype(w)::value>(a, stream); });
+        return with_warps(s.warps, [&](auto w) {
+            // (rows of 16-bit elements on 4-byte boundaries: two elements to an access)
+            if constexpr (sizeof(T) == 2)
+                if (fit(2)) return launch_rows<T, P, 2, kElements / 2, decltype(w)::value>(a, stream);
+            return launch_rows<T, P, 1, kElements, decltype(w)::value>(a, stream);
+        });
     if (s.c == 1) return launch_rows<T, P, V, 1, 1>(a, stream);
     if (s.c == 2) return launch_rows<T, P, V, 2, 1>(a, stream);
     return with_warps(s.warps, [&](auto w) { return launch_rows<T, P, V, M, decltype(w)::value>(a, stream); });
@@ -620,8 +626,11 @@ template <typename T>
 int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T), M = 16 / V;
     const bool params = a.dgamma != nullptr || a.dbeta != nullptr;
-    const bool wide = vectors_fit(a.width, sizeof(T), a.gamma, nullptr, Matrix{a.x, a.x_stride}, Matrix{a.dy, a.dy_stride},
-                                  Matrix{a.dx, a.dx_stride});
+    auto fit = [&](int v) {
+        return vectors_fit(v, a.width, sizeof(T), a.gamma, nullptr, Matrix{a.x, a.x_stride}, Matrix{a.dy, a.dy_stride},
+                           Matrix{a.dx, a.dx_stride});
+    };
+    const bool wide = fit(V);
     const Shape s = shape_of(a.width, wide ? V : 1, wide ? M : kElements);
     if (s.warps == 0) {
         if (params) {
@@ -637,7 +646,11 @@ int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
         return launch(norm_long_dx_kernel<T>, dim3(grid), kMaxThreads, stream, "norm_long_dx_kernel", a);
     }
     if (!wide)
-        return with_warps(s.warps, [&](auto w) { return launch_grad_rows<T, 1, kElements, decltype(w)::value>(a, stream); });
+        return with_warps(s.warps, [&](auto w) {
+            if constexpr (sizeof(T) == 2)
+                if (fit(2)) return launch_grad_rows<T, 2, kElements / 2, decltype(w)::value>(a, stream);
+            return launch_grad_rows<T, 1, kElements, decltype(w)::value>(a, stream);
+        });
     if (s.c == 1) return launch_grad_rows<T, V, 1, 1>(a, stream);
     return with_warps(s.warps, [&](auto w) { return launch_grad_rows<T, V, M, decltype(w)::value>(a, stream); });
 }
