@@ -180,6 +180,8 @@ EXPORTED = tuple(_SIGNATURES)
 def lib():
     """The loaded library.  Raises if it has not been built."""
     global _lib
+    if _lib is not None:      # (a call's common case: no lock)
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -869,12 +871,21 @@ def _scratch(work: Optional[torch.Tensor]):
     return (None, 0) if work is None else (_dev_ptr(work, torch.uint8, "work"), work.numel())
 
 
+def _rows(t: torch.Tensor, what: str):
+    """Pointer, rows, width and row stride of a matrix, as _matrix checks it."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype not in _TYPES or not t.is_cuda or len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
+        _matrix(t, what)      # says what is wrong
+    # a single row's stride is never used; torch may report any
+    return t.data_ptr(), shape[0], shape[1], stride[0] if shape[0] > 1 else shape[1]
+
+
 def _same_matrix(t: torch.Tensor, like: torch.Tensor, what: str):
     """Pointer and row stride of a matrix of the type and shape of another."""
-    ptr = _matrix(t, what)
+    ptr, _, _, stride = _rows(t, what)
     if t.dtype != like.dtype or t.shape != like.shape:
         raise TypeError(f"{what}: expected {tuple(like.shape)} of {like.dtype}, got {tuple(t.shape)} of {t.dtype}")
-    return ptr, _row_stride(t)
+    return ptr, stride
 
 
 def new_head_work(rows: int, width: int, vocab: int, gradient: bool = True, piece: int = 0, device="cuda") -> torch.Tensor:
@@ -885,13 +896,13 @@ def new_head_work(rows: int, width: int, vocab: int, gradient: bool = True, piec
 
 
 def _head(hidden: torch.Tensor, weight: torch.Tensor, inv_temperature: float) -> Head:
-    h, w = _matrix(hidden, "hidden"), _matrix(weight, "weight")
+    h, rows, width, h_stride = _rows(hidden, "hidden")
+    w, vocab, w_width, w_stride = _rows(weight, "weight")
     if hidden.dtype != weight.dtype or hidden.dtype == torch.float32:
         raise TypeError(f"hidden, weight: expected both float16 or both bfloat16, got {hidden.dtype}, {weight.dtype}")
-    if hidden.shape[1] != weight.shape[1]:
-        raise ValueError(f"hidden is {hidden.shape[1]} wide, weight {weight.shape[1]}")
-    return Head(h, w, hidden.shape[0], weight.shape[0], hidden.shape[1], _row_stride(hidden), _row_stride(weight),
-                _TYPES[hidden.dtype], 0, float(inv_temperature))
+    if width != w_width:
+        raise ValueError(f"hidden is {width} wide, weight {w_width}")
+    return Head(h, w, rows, vocab, width, h_stride, w_stride, _TYPES[hidden.dtype], 0, inv_temperature)
 
 
 def zero_head_logp_async(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, logp: torch.Tensor,
@@ -927,29 +938,27 @@ def zero_head_logp_grad_async(hidden: torch.Tensor, weight: torch.Tensor, labels
     _check(rc, "zero_head_logp_grad_async")
 
 
-def _norm(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], like, eps: float) -> Norm:
-    """The C description; gamma, beta and what ``like`` holds share one type."""
-    ptr, width, kind = _matrix(x, "x"), x.shape[1], None
-    for t, what in ((gamma, "gamma"), (beta, "beta"), *like):
-        if t is None:
-            continue
-        if t.dtype not in _TYPES or kind not in (None, t.dtype):
-            raise TypeError(f"{what}: expected float32, float16 or bfloat16, the same for all of the norm's vectors")
-        if t.numel() != width:
-            raise ValueError(f"{what}: {t.numel()} elements, rows have {width}")
-        kind = t.dtype
-    part = lambda t, what: None if t is None else _dev_ptr(t, t.dtype, what)
-    return Norm(ptr, part(gamma, "gamma"), part(beta, "beta"), x.shape[0], width, _row_stride(x), _TYPES[x.dtype],
-                ZS_F32 if kind is None else _TYPES[kind], float(eps))
+def _norm_vector(t: Optional[torch.Tensor], width: int, kind, what: str):
+    """Pointer of one of a norm's vectors (None: NULL), and the type they share."""
+    if t is None:
+        return None, kind
+    if t.dtype not in _TYPES or kind not in (None, t.dtype):
+        raise TypeError(f"{what}: expected float32, float16 or bfloat16, the same for all of the norm's vectors")
+    if t.numel() != width:
+        raise ValueError(f"{what}: {t.numel()} elements, rows have {width}")
+    return _dev_ptr(t, t.dtype, what), t.dtype
 
 
 def zero_layer_norm_async(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], y: torch.Tensor,
                           saved: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None):
     """Layer norm of the rows of ``x`` into ``y`` (which may be ``x``); ``saved``
     ([rows, 2] fp32: mean, 1 / deviation) is what the gradient needs."""
-    n = _norm(x, gamma, beta, (), eps)
-    out, stride = _same_matrix(y, x, "y")
-    rc = lib().zero_layer_norm_async(ctypes.byref(n), out, stride, _vector(saved, torch.float32, 2 * n.rows, "saved"),
+    ptr, rows, width, stride = _rows(x, "x")
+    g, kind = _norm_vector(gamma, width, None, "gamma")
+    b, kind = _norm_vector(beta, width, kind, "beta")
+    n = Norm(ptr, g, b, rows, width, stride, _TYPES[x.dtype], _TYPES.get(kind, ZS_F32), eps)
+    out, out_stride = _same_matrix(y, x, "y")
+    rc = lib().zero_layer_norm_async(ctypes.byref(n), out, out_stride, _vector(saved, torch.float32, 2 * rows, "saved"),
                                      _stream_of(stream, x))
     _check(rc, "zero_layer_norm_async")
 
@@ -964,25 +973,28 @@ def zero_layer_norm_grad_async(dy: torch.Tensor, x: torch.Tensor, gamma: Optiona
                                work: Optional[torch.Tensor] = None, stream=None):
     """Gradients of the norm's input (``dx`` may be ``dy`` or ``x``), weight and
     bias; any of the three may be None."""
-    n = _norm(x, gamma, None, ((dgamma, "dgamma"), (dbeta, "dbeta")), 0.0)
+    ptr, rows, width, stride = _rows(x, "x")
+    g, kind = _norm_vector(gamma, width, None, "gamma")
+    dg, kind = _norm_vector(dgamma, width, kind, "dgamma")
+    db, kind = _norm_vector(dbeta, width, kind, "dbeta")
+    n = Norm(ptr, g, None, rows, width, stride, _TYPES[x.dtype], _TYPES.get(kind, ZS_F32), 0.0)
     dy_ptr, dy_stride = _same_matrix(dy, x, "dy")
     dx_ptr, dx_stride = (None, 0) if dx is None else _same_matrix(dx, x, "dx")
-    part = lambda t, what: None if t is None else _dev_ptr(t, t.dtype, what)
     rc = lib().zero_layer_norm_grad_async(ctypes.byref(n), dy_ptr, dy_stride,
-                                          _vector(saved, torch.float32, 2 * n.rows, "saved"), dx_ptr, dx_stride,
-                                          part(dgamma, "dgamma"), part(dbeta, "dbeta"), *_scratch(work),
-                                          _stream_of(stream, x))
+                                          _vector(saved, torch.float32, 2 * rows, "saved"), dx_ptr, dx_stride, dg, db,
+                                          *_scratch(work), _stream_of(stream, x))
     _check(rc, "zero_layer_norm_grad_async")
 
 
 def zero_embed_async(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0, stream=None):
     """Rows of ``table`` at ``ids`` (any shape; out of range: zeros) times ``scale``."""
-    ptr, out_ptr = _matrix(table, "table"), _matrix(out, "out")
-    if out.dtype != table.dtype or tuple(out.shape) != (ids.numel(), table.shape[1]):
+    ptr, vocab, width, stride = _rows(table, "table")
+    out_ptr, rows, out_width, out_stride = _rows(out, "out")
+    n = ids.numel()
+    if out.dtype != table.dtype or rows != n or out_width != width:
         raise TypeError("out: expected one row of the table's type and width for each id")
-    e = Embed(ptr, _dev_ptr(ids, torch.int64, "ids"), ids.numel(), table.shape[0], table.shape[1], _row_stride(table),
-              _TYPES[table.dtype], 0, float(scale))
-    _check(lib().zero_embed_async(ctypes.byref(e), out_ptr, _row_stride(out), _stream_of(stream, table)), "zero_embed_async")
+    e = Embed(ptr, _dev_ptr(ids, torch.int64, "ids"), n, vocab, width, stride, _TYPES[table.dtype], 0, scale)
+    _check(lib().zero_embed_async(ctypes.byref(e), out_ptr, out_stride, _stream_of(stream, table)), "zero_embed_async")
 
 
 def new_embed_work(tokens: int, width: int, device="cuda") -> torch.Tensor:
@@ -994,16 +1006,16 @@ def zero_embed_grad_async(ids: torch.Tensor, dout: torch.Tensor, dtable: torch.T
                           scale: float = 1.0, accumulate: bool = False, stream=None):
     """Gradient of the table from that of the looked-up rows; ``accumulate`` adds to
     the rows of ``dtable`` whose ids occur and leaves the others as they are."""
-    ptr, grad = _matrix(dout, "dout"), _matrix(dtable, "dtable")
-    if dout.shape[0] != ids.numel() or dout.shape[1] != dtable.shape[1]:
+    ptr, rows, width, stride = _rows(dout, "dout")
+    grad, vocab, grad_width, grad_stride = _rows(dtable, "dtable")
+    n = ids.numel()
+    if rows != n or width != grad_width:
         raise TypeError("dout: expected one row of the table's width for each id")
-    if dtable.dtype not in (dout.dtype, torch.float32):
+    if dtable.dtype is not torch.float32 and dtable.dtype != dout.dtype:
         raise TypeError(f"dtable: expected {dout.dtype} or float32, got {dtable.dtype}")
-    e = Embed(None, _dev_ptr(ids, torch.int64, "ids"), ids.numel(), dtable.shape[0], dtable.shape[1], 0,
-              _TYPES[dout.dtype], 0, float(scale))
-    rc = lib().zero_embed_grad_async(ctypes.byref(e), ptr, _row_stride(dout), grad, _row_stride(dtable),
-                                     _TYPES[dtable.dtype], 1 if accumulate else 0, *_scratch(work),
-                                     _stream_of(stream, dout))
+    e = Embed(None, _dev_ptr(ids, torch.int64, "ids"), n, vocab, width, 0, _TYPES[dout.dtype], 0, scale)
+    rc = lib().zero_embed_grad_async(ctypes.byref(e), ptr, stride, grad, grad_stride, _TYPES[dtable.dtype],
+                                     1 if accumulate else 0, *_scratch(work), _stream_of(stream, dout))
     _check(rc, "zero_embed_grad_async")
 
 

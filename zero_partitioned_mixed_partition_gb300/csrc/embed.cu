@@ -334,13 +334,14 @@ __device__ __noinline__ void join_run(const EmbedArgs& a, int64_t chunks, int32_
     const int64_t k = q * V;
     float sum[V];
     unpack<float, V>(load_part<V>(part_at<V>(a, first, true, k)), sum);
-    for (int64_t j = first + 1; j <= last; j += 4) {
-        Pack<float, V> x[4];
+    constexpr int kAtOnce = V == 8 ? 4 : 8;  // (8 of 8 floats: registers; 31 us for 27 in the batch case)
+    for (int64_t j = first + 1; j <= last; j += kAtOnce) {
+        Pack<float, V> x[kAtOnce];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < kAtOnce; ++u)
             if (j + u <= last) x[u] = load_part<V>(part_at<V>(a, j + u, false, k));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kAtOnce; ++u) {
             if (j + u > last) break;
             float f[V];
             unpack<float, V>(x[u], f);
@@ -418,8 +419,14 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
 
 // ------------------------------------------------------------------- launches ---
 
-// Tokens of a chunk: few where there are few tokens, for more blocks.
-int32_t chunk_of(int64_t tokens) { return tokens >= 65536 ? 64 : tokens >= 32768 ? 32 : tokens >= 8192 ? 16 : 8; }
+// Tokens of a chunk, a power of 2: few where there are few tokens, for more blocks (some 1200,
+// each of up to 1024 of the width); many where there are enough blocks, for fewer parts of runs.
+int32_t chunk_of(int64_t tokens, int64_t width) {
+    const int64_t blocks = tokens * (width > 1024 ? width / 1024 : 1);
+    int32_t chunk = tokens >= 8192 ? 16 : 8;
+    while (chunk < kMaxChunk && (int64_t)chunk * 1216 < blocks) chunk *= 2;
+    return chunk;
+}
 
 // The parts of the scratch buffer, as offsets.
 struct Plan {
@@ -434,7 +441,7 @@ Plan plan_of(int64_t tokens, int64_t width) {
         return here;
     };
     for (int64_t& l : p.list) l = take(4 * tokens);
-    const int32_t chunk = chunk_of(tokens);
+    const int32_t chunk = chunk_of(tokens, width);
     p.chunks = (tokens + chunk - 1) / chunk;
     p.part = take(8 * p.chunks * width);
     p.arrivals = p.chunks * ((width + kThreads - 1) / kThreads);
@@ -461,10 +468,8 @@ int32_t launch_lookup(const EmbedArgs& a, cudaStream_t stream) {
 template <typename T, typename G, int V>
 int32_t launch_grad(const EmbedArgs& a, int64_t chunks, cudaStream_t stream) {
     // the sort's cluster, and clusters that fill the other SMs with zeroing blocks
-    const void* sort = (const void*)embed_sort_kernel<G, V>;
-    cudaError_t err = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortShared);
-    const int most = err == cudaSuccess ? active_clusters(sort, kSortThreads, kSortCtas, kSortShared, &err) : 0;
-    if (most < 1) return zs::cuda_fail(err, "embed_sort_kernel");
+    const int most = clusters_of((const void*)embed_sort_kernel<G, V>, kSortThreads, kSortCtas, kSortShared);
+    if (most < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_clusters(embed_sort_kernel<G, V>, a.accumulate ? 1 : most > 1 ? most : 2, kSortCtas, kSortThreads, kSortShared,
                            stream, a, "embed_sort_kernel"));
     if (chunks == 0) return ZS_OK;
@@ -560,7 +565,7 @@ ZS_API int32_t zero_embed_grad_async(const zs_embed* e, const void* dout, int64_
     uint32_t** const lists[] = {&a.keys, &a.places, &a.other_keys, &a.other_places};
     for (int i = 0; i < 4; ++i) *lists[i] = (uint32_t*)((char*)work_dev + p.list[i]);
     a.part = (float*)((char*)work_dev + p.part);
-    a.chunk = chunk_of(e->tokens);
+    a.chunk = chunk_of(e->tokens, e->width);
     a.arrived = (uint32_t*)((char*)work_dev + p.arrived);
     a.arrivals = p.arrivals;
     int32_t bits = 1;  // of the largest key, `vocab`

@@ -822,14 +822,10 @@ int32_t make_map(CUtensorMap* map, int32_t type, const void* base, int64_t rows,
     return rc == CUDA_SUCCESS ? ZS_OK : zs::fail_with(ZS_ERR_CUDA, "cuTensorMapEncodeTiled: refused a matrix of the head");
 }
 
-// Pairs of CTAs (CTAS = 1: CTAs) that run at once; 0: a CUDA error, reported.
+// Pairs of CTAs (CTAS = 1: CTAs) that run at once; 0: a CUDA error, recorded.
 template <typename T, int MODE, int CTAS>
 int pairs_of() {
-    const void* kernel = (const void*)head_product_kernel<T, MODE, CTAS>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductShared);
-    const int pairs = err == cudaSuccess ? active_clusters(kernel, kProductThreads, CTAS, kProductShared, &err) : 0;
-    if (pairs < 1) zs::cuda_fail(err, "head_product_kernel");
-    return pairs;
+    return clusters_of((const void*)head_product_kernel<T, MODE, CTAS>, kProductThreads, CTAS, kProductShared);
 }
 template <typename T, int MODE, int CTAS>
 int32_t launch_product(const ProductArgs& p, const CUtensorMap& map_a, const CUtensorMap& map_b, int pairs,

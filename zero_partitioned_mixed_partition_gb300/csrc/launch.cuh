@@ -1,7 +1,6 @@
 // launch.cuh -- launches of the head, norm and embedding kernels: with
 // programmatic serialization, so that every kernel waits by griddep_wait() before it
-// touches global memory.  Included inside an anonymous namespace, cluster_counts.h
-// before it, outside.
+// touches global memory.  Included inside an anonymous namespace after loss_common.cuh.
 #pragma once
 
 template <typename... P, typename... A>
@@ -50,6 +49,20 @@ unsigned grid_of(const void* kernel, int threads, size_t shared, int64_t work) {
         return 0;
     }
     return (unsigned)(work < 1 ? 1 : work < most ? work : most);
+}
+
+// Clusters of `ctas` blocks of a kernel that run at once on the current device; 0 and the
+// error recorded if that could not be found.
+int clusters_of(const void* kernel, int threads, int ctas, size_t shared) {
+    static zs::ClusterCounts counts;
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    const int most = err != cudaSuccess ? 0 : counts.get(device, kernel, ctas, (int)shared, [&] {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        return err == cudaSuccess ? active_clusters(kernel, threads, ctas, (int)shared, &err) : 0;
+    });
+    if (most < 1) zs::cuda_fail(err != cudaSuccess ? err : cudaErrorInvalidConfiguration, "clusters_of");
+    return most;
 }
 
 #define ZS_TRY(call)                          \

@@ -12,8 +12,8 @@ namespace {
 
 #include "step_common.cuh"
 #include "step_end.cuh"
+#include "loss_common.cuh"
 #include "elem.cuh"
-#include "packed.cuh"
 #include "launch.cuh"
 
 [[maybe_unused]] constexpr uint32_t kSiteNormRow = 18;
@@ -595,9 +595,8 @@ int32_t launch_forward(const NormArgs& a, cudaStream_t stream) {
     if (s.warps == 0) return launch_long(a, stream, T());
     if (!wide)
         return with_warps(s.warps, [&](auto w) {
-            // (rows of 16-bit elements on 4-byte boundaries: two elements to an access)
-            if constexpr (sizeof(T) == 2)
-                if (fit(2)) return launch_rows<T, P, 2, kElements / 2, decltype(w)::value>(a, stream);
+            // (rows on boundaries of two elements: two to an access)
+            if (fit(2)) return launch_rows<T, P, 2, kElements / 2, decltype(w)::value>(a, stream);
             return launch_rows<T, P, 1, kElements, decltype(w)::value>(a, stream);
         });
     if (s.c == 1) return launch_rows<T, P, V, 1, 1>(a, stream);
@@ -647,8 +646,7 @@ int32_t launch_grad(const NormArgs& a, cudaStream_t stream) {
     }
     if (!wide)
         return with_warps(s.warps, [&](auto w) {
-            if constexpr (sizeof(T) == 2)
-                if (fit(2)) return launch_grad_rows<T, 2, kElements / 2, decltype(w)::value>(a, stream);
+            if (fit(2)) return launch_grad_rows<T, 2, kElements / 2, decltype(w)::value>(a, stream);
             return launch_grad_rows<T, 1, kElements, decltype(w)::value>(a, stream);
         });
     if (s.c == 1) return launch_grad_rows<T, V, 1, 1>(a, stream);
