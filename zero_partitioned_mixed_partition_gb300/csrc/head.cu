@@ -426,9 +426,10 @@ struct Ring {
 
 // The 128 columns of a thread's row, as 16-bit numbers or fp32, from registers to
 // memory by way of the warp's staging place, so that a row's 128 bytes go out together.
-// `row`: the lane's row in memory, NULL: none.  Only the first `columns`.
-template <int ELEM, typename F>
-__device__ __forceinline__ void store_rows(uint8_t* staging, int lane, char* row, int32_t columns, F vector_of) {
+// row_at(r): the place of row r of the warp's 32 in memory, NULL: nowhere; called by all
+// lanes together.  Only the first `columns`.
+template <int ELEM, typename R, typename F>
+__device__ __forceinline__ void store_rows(uint8_t* staging, int lane, int32_t columns, R row_at, F vector_of) {
     constexpr int kEach = 16 / ELEM, kColumns = 128 / ELEM;  // of a vector; of 128 bytes
 #pragma unroll
     for (int part = 0; part < 128 / kColumns; ++part) {
@@ -439,7 +440,7 @@ __device__ __forceinline__ void store_rows(uint8_t* staging, int lane, char* row
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             const int r = t * 4 + lane / 8, q = lane % 8;
-            char* const to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
+            char* const to = row_at(r);
             const int32_t column = part * kColumns + q * kEach;
             if (to != nullptr && column < columns)
                 *reinterpret_cast<uint4*>(to + column * ELEM) =
@@ -620,7 +621,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 for (int i = 0; i < 128; ++i) v[i] = quiet_nan();
             }
             if (!mine) continue;
-            const int64_t r = (int64_t)t.m * (CTAS * 128) + rank * 128 + quarter * 32 + lane;  // the thread's row of the tile,
+            const int64_t r0 = (int64_t)t.m * (CTAS * 128) + rank * 128 + quarter * 32, r = r0 + lane;  // the thread's row of the tile,
             const int64_t j0 = (int64_t)t.n * kTile + side * 128;                        // and its first column
             if (MODE == kLogits) {
                 const int32_t label = a.row[r].label - (int32_t)j0;
@@ -659,8 +660,9 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 }
                 // (rows that only fill the tile are 0, whatever W holds)
                 const bool none = coef == 0.0f;
-                const bool in = ZS_RANGE_OK(kSiteHeadSum, r, 1, a.rows_pad) && ZS_RANGE_OK(kSiteHeadSum, j0, 128, a.piece);
-                store_rows<2>(staging, lane, in ? reinterpret_cast<char*>(a.d + r * a.piece + j0) : nullptr, 128, [&](int j) {
+                const bool in = ZS_RANGE_OK(kSiteHeadSum, r0, 32, a.rows_pad) && ZS_RANGE_OK(kSiteHeadSum, j0, 128, a.piece);
+                char* const to = reinterpret_cast<char*>(a.d + r0 * a.piece + j0);
+                store_rows<2>(staging, lane, in ? 128 : 0, [&](int i) { return to + i * a.piece * 2; }, [&](int j) {
                     return none ? make_uint4(0, 0, 0, 0)
                                 : make_uint4(narrow2<T>(v[j], v[j + 1]), narrow2<T>(v[j + 2], v[j + 3]),
                                              narrow2<T>(v[j + 4], v[j + 5]), narrow2<T>(v[j + 6], v[j + 7]));
@@ -669,9 +671,12 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 const int64_t left = a.width - j0;
                 const int32_t columns = left < 128 ? (int32_t)left : 128;
                 if (MODE == kDHidden && !(w.split == 1 && p.first == 0 && p.last)) {
-                    const int64_t at = (int64_t)t.part * w.m_tiles * kTile + r;
-                    float* const row = r < live && ZS_RANGE_OK(kSiteHeadSum, at, 1, a.sums_room) ? (float*)a.part + at * a.width + j0 : nullptr;
-                    if (p.first > 0 && row != nullptr) {
+                    // (rows that only fill the tile have room as well)
+                    const int64_t at = (int64_t)t.part * w.m_tiles * kTile + r0;
+                    const bool in = ZS_RANGE_OK(kSiteHeadSum, at, 32, a.sums_room);
+                    float* const to = (float*)a.part + at * a.width + j0;
+                    if (p.first > 0 && in) {
+                        const float* const row = to + lane * a.width;
 #pragma unroll
                         for (int i = 0; i < 128; i += 4) {
                             if (i >= columns) break;
@@ -680,16 +685,25 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                         }
                     }
                     __syncwarp();
-                    store_rows<4>(staging, lane, reinterpret_cast<char*>(row), columns, [&](int j) {
+                    store_rows<4>(staging, lane, in ? columns : 0, [&](int i) { return reinterpret_cast<char*>(to + i * a.width); }, [&](int j) {
                         return make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
                                           __float_as_uint(v[j + 3]));
                     });
                 } else {
                     const float unscale = a.counts->unscale;
+                    // the lane's row of dH lies anywhere, a row of dW after the one before
                     uint16_t* row = nullptr;
-                    if (MODE == kDHidden && r < live && ZS_RANGE_OK(kSiteHeadRow, a.index[r], 1, a.rows)) row = a.dhidden + a.index[r] * a.dhidden_stride + j0;
-                    if (MODE == kDWeight && r < p.count && ZS_RANGE_OK(kSiteHeadRow, p.first + r, 1, a.vocab)) row = a.dweight + (p.first + r) * a.dweight_stride + j0;
-                    store_rows<2>(staging, lane, reinterpret_cast<char*>(row), columns, [&](int j) {
+                    if (MODE == kDHidden && r < live && ZS_RANGE_OK(kSiteHeadRow, a.index[r], 1, a.rows))
+                        row = a.dhidden + a.index[r] * a.dhidden_stride + j0;
+                    uint16_t* const to = a.dweight + (p.first + r0) * a.dweight_stride + j0;
+                    const int32_t rows = (int32_t)(p.count - r0 < 32 ? p.count - r0 : 32);
+                    const bool in = MODE == kDHidden || rows < 1 || ZS_RANGE_OK(kSiteHeadRow, p.first + r0, rows, a.vocab);
+                    auto row_at = [&](int i) {
+                        if (MODE == kDHidden)
+                            return reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), i));
+                        return i < rows ? reinterpret_cast<char*>(to + i * a.dweight_stride) : nullptr;
+                    };
+                    store_rows<2>(staging, lane, in ? columns : 0, row_at, [&](int j) {
                         uint32_t x[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) x[i] = narrow2<T>(v[j + 2 * i] * unscale, v[j + 2 * i + 1] * unscale);
@@ -767,29 +781,32 @@ __global__ void __launch_bounds__(512) head_join_kernel(const __grid_constant__ 
     }
 }
 
-// Joins the parts of dH's sums: a block to a row.
+// Joins the parts of dH's sums: a warp to 128 columns of a row.
 template <typename T>
 __global__ void __launch_bounds__(256) head_dhidden_kernel(const __grid_constant__ ProductArgs p) {
     griddep_wait();
     const HeadArgs& a = p.h;
-    const int32_t live = a.counts->live;
-    const Tiles w = work_of<kDHidden>(p, live);
-    if (w.split == 1 && p.first == 0) return;  // (one piece: the product wrote dH)
+    const int32_t live = a.counts->live, split = a.counts->split;
+    if (split == 1 && p.first == 0) return;  // (one piece: the product wrote dH)
+    const int lane = threadIdx.x % 32;
     const float unscale = a.counts->unscale;
-    const int64_t part = (int64_t)w.m_tiles * kTile * a.width;
-    for (int64_t r = blockIdx.x; r < live; r += gridDim.x) {
-        const float* from = (const float*)a.part + r * a.width;
-        uint16_t* to = a.dhidden + (int64_t)a.index[r] * a.dhidden_stride;
-        for (int64_t k = 4 * threadIdx.x; k < a.width; k += 4 * blockDim.x) {
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int32_t q = 0; q < w.split; ++q) {
-                const float4 x = *reinterpret_cast<const float4*>(from + q * part + k);
-                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
-            }
-            *reinterpret_cast<uint2*>(to + k) =
-                make_uint2(narrow2<T>(s.x * unscale, s.y * unscale), narrow2<T>(s.z * unscale, s.w * unscale));
+    const int64_t part = (int64_t)tiles_of(live) * kTile * a.width;
+    const int32_t each = (int32_t)((a.width + 127) / 128);
+    for (int64_t u = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; u < (int64_t)live * each; u += (int64_t)gridDim.x * 8) {
+        const int64_t r = u / each, k = (u - r * each) * 128 + lane * 4;
+        if (k >= a.width) continue;
+        const float* from = (const float*)a.part + r * a.width + k;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int32_t q = 0; q < split; q += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(from + (q + i < split ? q + i : split - 1) * part);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (q + i < split) s = make_float4(s.x + x[i].x, s.y + x[i].y, s.z + x[i].z, s.w + x[i].w);
         }
+        *reinterpret_cast<uint2*>(a.dhidden + (int64_t)a.index[r] * a.dhidden_stride + k) =
+            make_uint2(narrow2<T>(s.x * unscale, s.y * unscale), narrow2<T>(s.z * unscale, s.w * unscale));
     }
 }
 
@@ -936,9 +953,8 @@ int32_t launch_grad(HeadArgs a, cudaStream_t stream) {
         if (p.last) break;
     }
     if (a.dhidden == nullptr) return ZS_OK;
-    const int64_t most = 8 * zs::device_sm_count();
-    return launch(head_dhidden_kernel<T>, dim3((unsigned)(a.rows_pad < most ? a.rows_pad : most)), 256, stream,
-                  "head_dhidden_kernel", p);
+    const int64_t most = 8 * zs::device_sm_count(), blocks = a.rows * ((a.width + 127) / 128) / 8 + 1;
+    return launch(head_dhidden_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), 256, stream, "head_dhidden_kernel", p);
 }
 
 // Calls f with a value of the type, and the CTAs of a tile as a constant: one for up to
