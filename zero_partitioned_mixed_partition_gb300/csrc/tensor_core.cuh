@@ -80,7 +80,15 @@ __device__ __forceinline__ void tensor_load(uint32_t at, float* v) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
+// Until the loads have come.  (What uses the values has to stay behind this: `loaded` on each
+// 32 of them, which is no instruction, says so to the compiler.)
 __device__ __forceinline__ void tensor_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void loaded(float* v) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                          "+f"(v[i + 6]), "+f"(v[i + 7]) :: "memory");
+}
 
 // ------------------------------------------------------------------ products ---
 
