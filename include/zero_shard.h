@@ -965,7 +965,9 @@ ZS_API int64_t zero_embed_work_bytes(int64_t tokens, int64_t width);
  *            dtable_stride >= width
  *   accumulate  0: every row is written (zeros where no token has the id); 1: rows
  *            of ids that occur are added to, the others are left as they are
- *            (a table tied to the head adds to zero_head_logp_grad_async's dweight)
+ *            (a table tied to the head adds to zero_head_logp_grad_async's dweight).
+ *            Added to an fp32 table, subnormal sums and elements may count as 0.
+ *            dtable may not overlap dout.
  *   work_dev DEVICE scratch on a 16-byte boundary, work_bytes >=
  *            zero_embed_work_bytes(tokens, width); holds nothing between calls
  * Source: derivative of zero_embed_async. */
@@ -1090,8 +1092,8 @@ ZS_API int64_t zero_kernel_launches(void);
 ZS_API int32_t zero_debug_checks(uint64_t* first_fault);
 
 /* Debug build: sets how many tries, 0 to 2^20 (the ordinary build's number), the
- * waits of the logits kernels and the head's products make for their own copies and warps before they
- * give up, and returns 1.  With few tries waits run out that would have been met,
+ * waits of the logits kernels and of the head's products make for their own copies
+ * and warps before they give up, and returns 1.  With few tries waits run out that would have been met,
  * which shows what a call does then (see zero_token_logp_async).  Synchronises
  * the device.  The ordinary build changes nothing and returns 0.
  * Source: no counterpart in the pages (a property of this library). */

@@ -5,7 +5,15 @@
 // The gradient sorts the tokens by id (stable, so that the order of a sum is that of
 // the tokens), takes the sorted list in chunks of equal length, however often an id
 // comes, sums each run of one id within a chunk in fp32, and joins the runs that go
-// across chunks.  No floating-point atomics; the same bits in every call.
+// across chunks.  No floating-point sum depends on the order of arrivals; the same bits in
+// every call.
+//
+// Bound by memory where tables and batches are large.  Measured on one GB300 (6772 GB/s copied):
+// lookup 65536 x 4096 bf16 from 32000 rows 104 us, 6.2 TB/s (rows in blocks as they come; in
+// blocks that stay 117 us).  Gradient of 65536 tokens added to 32000 x 4096 fp32 208 us, 4.7 TB/s:
+// some 25 us of it sort.  8192 tokens, 50257 x 768 bf16 27 us for a floor of 13: filling 77 MB with
+// zeros takes 12 to 15, the sums after it wait for their loads one after the other.  (Leaving
+// part of the zeros to the sums' launch: 31 us.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>

@@ -1,4 +1,18 @@
 // norm.cu -- layer norm and its gradient.
+//
+//   xh = (x - mean) rstd,   y = xh gamma + beta,
+//   dx = rstd (a - mean(a) - xh mean(a xh)) with a = dy gamma,
+//   dgamma = sum_rows dy xh,   dbeta = sum_rows dy.
+//
+// Rows are read once and written once, so memory bounds the large cases: a row lies in the
+// registers of a team of warps between its sums and its output, the rows after it are on their
+// way into shared memory, and the gradient keeps its columns' sums over rows in registers.
+// Measured on one GB300 (6772 GB/s copied): 16384 x 1600 bf16 23.7 us, 4.4 TB/s; gradient
+// 16384 x 4096 bf16 71 us, 5.7 TB/s.  The first issues 0.48 instructions a cycle and
+// scheduler, 14 for an element, of which a third turn bf16 into fp32 (three times, since the
+// row is held as it was read; held as fp32 the rows ahead no longer fit the registers, 35 us).  The
+// gradient reaches 84 % of the copy rate.  Earlier forms of it: next row in registers instead of shared
+// memory 87 us; team size at run time 90 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
