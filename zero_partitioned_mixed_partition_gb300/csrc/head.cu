@@ -342,7 +342,9 @@ __device__ __forceinline__ float infinity() { return __int_as_float(0x7f800000);
 //   kGrad      the same over one piece of the vocabulary: d
 //   kDHidden   d W over one piece
 //   kDWeight   d^T H: the piece's rows of dW
-enum { kLogits, kGrad, kDHidden, kDWeight };
+//   kBack      both in one launch, since small calls wait for launches
+enum { kLogits, kGrad, kDHidden, kDWeight, kBack };
+constexpr bool of_logits(int mode) { return mode == kLogits || mode == kGrad; }
 
 constexpr int kRowBytes = kStep * 2;                        // of an operand's row in a stage
 constexpr int kBoxBytes = 64 * kRowBytes;                   // 64 m of 64 k, across k
@@ -370,46 +372,48 @@ struct ProductArgs {
     int32_t last;          // its end is the vocabulary's
 };
 
-// The tiles of a product over the live rows, and how the long sum of kDHidden is
-// split among several sums joined afterwards.
+// The tensor maps of a launch: A and B; else d and W for dH, d and H for dW.
+struct Maps {
+    CUtensorMap m[4];
+};
+
+// A product's tiles, and how many parts its sum is split into.
 struct Tiles {
     int32_t m_tiles, n_tiles, split, steps;  // steps of kStep in the whole sum
+    __device__ __forceinline__ int32_t units() const { return m_tiles * n_tiles * split; }
 };
-template <int MODE>
-__device__ __forceinline__ Tiles work_of(const ProductArgs& p, int32_t live) {
-    Tiles w;
-    w.split = 1;
-    if (MODE == kLogits || MODE == kGrad) {
-        w.m_tiles = tiles_of(live);
-        w.n_tiles = tiles_of(p.count);
-        w.steps = steps_of(p.h.width);
-    } else if (MODE == kDHidden) {
-        w.m_tiles = tiles_of(live);
-        w.n_tiles = tiles_of(p.h.width);
-        w.steps = steps_of(p.count);
-        w.split = p.h.counts->split;
-    } else {
-        w.m_tiles = tiles_of(p.count);
-        w.n_tiles = tiles_of(p.h.width);
-        w.steps = steps_of(live);
-    }
+// Of a launch over the live rows: `back` is dW's, else empty.
+struct Work2 {
+    Tiles front, back;
+};
+template <int MODE, int CTAS>
+__device__ __forceinline__ Work2 work_of(const ProductArgs& p, int32_t live) {
+    Work2 w = {};
+    if (of_logits(MODE)) w.front = Tiles{tiles_of(live), tiles_of(p.count), 1, steps_of(p.h.width)};
+    if (MODE == kDHidden || MODE == kBack) w.front = Tiles{tiles_of(live), tiles_of(p.h.width), p.h.counts->split, steps_of(p.count)};
+    if (MODE == kDWeight || MODE == kBack)
+        w.back = Tiles{(int32_t)((p.count + CTAS * 128 - 1) / (CTAS * 128)), tiles_of(p.h.width), 1, steps_of(live)};
     return w;
 }
 
-// One tile of the pair, in the order in which they are taken.  Logits: groups of 16
-// tiles of rows go through the vocabulary together, so that a tile of W is read from
-// memory once for each group and the group's rows stay in L2.  The others: tiles of
-// the width run fastest (they share d), then rows.
+// One tile, in the order in which they are taken.  Logits: groups of 16 tiles of rows go
+// through the vocabulary together, so that a tile of W is read from memory once for each
+// group and the group's rows stay in L2.  The others: tiles of the width run fastest (they
+// share d), then rows.
 struct Tile {
     int32_t m, n, part, from, to;  // from, to: steps
+    bool weight;                   // of dW
 };
 template <int MODE>
-__device__ __forceinline__ Tile tile_of(const Tiles& w, int32_t u) {
+__device__ __forceinline__ Tile tile_of(const Work2& both, int32_t u) {
     Tile t;
+    t.weight = MODE == kDWeight || (MODE == kBack && u >= both.front.units());
+    const Tiles& w = t.weight ? both.back : both.front;
+    if (MODE == kBack && t.weight) u -= both.front.units();
     t.part = 0;
     t.from = 0;
     t.to = w.steps;
-    if (MODE == kLogits || MODE == kGrad) {
+    if (of_logits(MODE)) {
         const int32_t group = 16 * w.n_tiles, g = u / group, first = g * 16, rest = u - g * group;
         const int32_t high = w.m_tiles - first < 16 ? w.m_tiles - first : 16;
         t.m = first + rest % high;
@@ -417,9 +421,9 @@ __device__ __forceinline__ Tile tile_of(const Tiles& w, int32_t u) {
     } else {
         t.n = u % w.n_tiles;
         const int32_t q = u / w.n_tiles;
-        t.m = q % w.m_tiles;
-        if (MODE == kDHidden) {
-            t.part = q / w.m_tiles;
+        t.part = q / w.m_tiles;
+        t.m = q - t.part * w.m_tiles;
+        if (w.split > 1) {
             t.from = (int32_t)((int64_t)w.steps * t.part / w.split);
             t.to = (int32_t)((int64_t)w.steps * (t.part + 1) / w.split);
         }
@@ -429,7 +433,7 @@ __device__ __forceinline__ Tile tile_of(const Tiles& w, int32_t u) {
 // Columns of B in a tile: 128 where the width's last tile has no more.
 template <int MODE>
 __device__ __forceinline__ int32_t wide_of(const ProductArgs& p, int32_t n) {
-    return (MODE == kDHidden || MODE == kDWeight) && p.h.width - (int64_t)n * kTile <= 128 ? 128 : (int32_t)kTile;
+    return !of_logits(MODE) && p.h.width - (int64_t)n * kTile <= 128 ? 128 : (int32_t)kTile;
 }
 
 struct Ring {
@@ -488,10 +492,9 @@ __device__ __forceinline__ float pick(const float* v, int32_t i) {
 // products is of rows that are not there.
 template <typename T, int MODE, int CTAS>
 __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 1)
-    head_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                        const __grid_constant__ ProductArgs p) {
+    head_product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ProductArgs p) {
     constexpr int kStages = stages_of(CTAS), kStage = stage_bytes(CTAS);
-    constexpr bool kAlongA = MODE != kDWeight, kAlongB = MODE == kLogits || MODE == kGrad;  // operands along k
+    constexpr bool kAlongB = of_logits(MODE);  // B along k; A is too, but for dW
     extern __shared__ uint8_t s_raw[];
     __shared__ Ring ring;
     uint8_t* const stage0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
@@ -513,8 +516,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
         ring.failed = 0;
         ring.issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_map(&map_a);
-        prefetch_map(&map_b);
+        for (int i = 0; i < 4; ++i) prefetch_map(&maps.m[i]);
     }
     if (warp == 2) tensor_alloc<CTAS>(&ring.sums);
     tensor_fence_before();
@@ -525,8 +527,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
     griddep_wait();
     const uint32_t sums = ring.sums;
     const int32_t live = a.counts->live;
-    const Tiles w = work_of<MODE>(p, live);
-    const int32_t units = w.m_tiles * w.n_tiles * w.split;
+    const Work2 w = work_of<MODE, CTAS>(p, live);
+    const int32_t units = w.front.units() + w.back.units();
 
     if (warp < 4) give_registers<kFewRegisters>();
     if (warp == 0 && lane == 0) {
@@ -538,6 +540,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
             const Tile t = tile_of<MODE>(w, u);
             const int32_t mine = wide_of<MODE>(p, t.n) / CTAS;  // columns of B in this CTA
             const uint32_t bytes = (uint32_t)(kBytesA + mine * kRowBytes);
+            const CUtensorMap* const map_a = &maps.m[t.weight ? 2 : 0];
+            const CUtensorMap* const map_b = &maps.m[t.weight ? 3 : 1];
             const int32_t m0 = t.m * (CTAS * 128) + (int32_t)rank * 128, n0 = t.n * (int32_t)kTile + (int32_t)rank * mine;
             for (int32_t k = t.from; k < t.to; ++k, ++at) {
                 const int s = at % kStages;
@@ -552,17 +556,17 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 uint8_t* const to_a = stage0 + s * kStage;
                 uint8_t* const to_b = to_a + kBytesA;
                 const int32_t x = k * kStep;
-                if (kAlongA) {
-                    copy_box<CTAS>(to_a, &map_a, x, m0, full);
+                if (!t.weight) {
+                    copy_box<CTAS>(to_a, map_a, x, m0, full);
                 } else {
-                    copy_box<CTAS>(to_a, &map_a, m0, x, full);
-                    copy_box<CTAS>(to_a + kBoxBytes, &map_a, m0 + 64, x, full);
+                    copy_box<CTAS>(to_a, map_a, m0, x, full);
+                    copy_box<CTAS>(to_a + kBoxBytes, map_a, m0 + 64, x, full);
                 }
                 if (kAlongB) {
-                    copy_box<CTAS>(to_b, &map_b, x, (int32_t)p.first + n0, full);
+                    copy_box<CTAS>(to_b, map_b, x, (int32_t)p.first + n0, full);
                 } else {
-                    const int32_t y = MODE == kDHidden ? (int32_t)p.first + x : x;
-                    for (int32_t c = 0; c < mine; c += 64) copy_box<CTAS>(to_b + c * kRowBytes, &map_b, n0 + c, y, full);
+                    const int32_t y = t.weight ? x : (int32_t)p.first + x;
+                    for (int32_t c = 0; c < mine; c += 64) copy_box<CTAS>(to_b + c * kRowBytes, map_b, n0 + c, y, full);
                 }
             }
         }
@@ -574,7 +578,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
         bool ok = true;
         for (int32_t u = pair; u < units && ok; u += pairs) {
             const Tile t = tile_of<MODE>(w, u);
-            const uint32_t kind = product_kind<CTAS, T, kAlongA, kAlongB>((uint32_t)wide_of<MODE>(p, t.n));
+            const uint32_t kind = product_kind<CTAS, T>((uint32_t)wide_of<MODE>(p, t.n), !t.weight, kAlongB);
             for (int32_t k = t.from; k < t.to; ++turn) {
                 const int set = turn & 1;
                 const int32_t stop = k + kRun < t.to ? k + kRun : t.to;
@@ -587,12 +591,12 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                     if (!ok) break;
                     tensor_fence_after();
                     const uint8_t* const from = stage0 + s * kStage;
-                    uint64_t da = operand<kAlongA>(from, kBoxBytes), db = operand<kAlongB>(from + kBytesA, kBoxBytes);
+                    uint64_t da = operand(from, kBoxBytes, !t.weight), db = operand(from + kBytesA, kBoxBytes, kAlongB);
 #pragma unroll
                     for (int q = 0; q < kStep / 16; ++q) {
                         multiply<CTAS>(sums + (uint32_t)set * 256u, da, db, kind, add || q > 0);
-                        da += operand_step<kAlongA>();
-                        db += operand_step<kAlongB>();
+                        da += operand_step(!t.weight);
+                        db += operand_step(kAlongB);
                     }
                     arrive_after_products<CTAS>(&ring.empty[s]);
                 }
@@ -613,8 +617,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
             float v[128];
             // (a tile's first sums straight to their place, but dW's added to 0: with a few
             // rows, where its tiles are one step each, 155934 x 1104 took 143 us that way, 114 so)
-            constexpr bool kStraight = MODE != kDWeight;
-            if (!kStraight || t.from == t.to || !mine) {
+            if (t.weight || t.from == t.to || !mine) {
 #pragma unroll
                 for (int i = 0; i < 128; ++i) v[i] = 0.0f;
             }
@@ -623,7 +626,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                 ok = ok && all_lanes(mbar_wait<true, true>(&ring.sums_full[set], (uint32_t)(turn / 2) & 1u, &ring.failed));
                 tensor_fence_after();
                 const uint32_t from = sums + (uint32_t)(set * 256 + side * 128) + ((uint32_t)quarter * 32u << 16);
-                if (kStraight && mine && ok && k == t.from) {
+                if (!t.weight && mine && ok && k == t.from) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tensor_load(from + (uint32_t)c * 32u, v + c * 32);
                     tensor_load_wait();
@@ -700,9 +703,9 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
             } else {
                 const int64_t left = a.width - j0;
                 const int32_t columns = left < 128 ? (int32_t)left : 128;
-                if (MODE == kDHidden && !(w.split == 1 && p.first == 0 && p.last)) {
+                if (!t.weight && !(w.front.split == 1 && p.first == 0 && p.last)) {
                     // (rows that only fill the tile have room as well)
-                    const int64_t at = (int64_t)t.part * w.m_tiles * kTile + r0;
+                    const int64_t at = (int64_t)t.part * w.front.m_tiles * kTile + r0;
                     const bool in = ZS_RANGE_OK(kSiteHeadSum, at, 32, a.sums_room);
                     float* const to = (float*)a.part + at * a.width + j0;
                     if (p.first > 0 && in) {
@@ -723,13 +726,13 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kProductThreads, 
                     const float unscale = a.counts->unscale;
                     // the lane's row of dH lies anywhere, a row of dW after the one before
                     uint16_t* row = nullptr;
-                    if (MODE == kDHidden && r < live && ZS_RANGE_OK(kSiteHeadRow, a.index[r], 1, a.rows))
+                    if (!t.weight && r < live && ZS_RANGE_OK(kSiteHeadRow, a.index[r], 1, a.rows))
                         row = a.dhidden + a.index[r] * a.dhidden_stride + j0;
                     uint16_t* const to = a.dweight + (p.first + r0) * a.dweight_stride + j0;
                     const int32_t rows = (int32_t)(p.count - r0 < 32 ? p.count - r0 : 32);
-                    const bool in = MODE == kDHidden || rows < 1 || ZS_RANGE_OK(kSiteHeadRow, p.first + r0, rows, a.vocab);
+                    const bool in = !t.weight || rows < 1 || ZS_RANGE_OK(kSiteHeadRow, p.first + r0, rows, a.vocab);
                     auto row_at = [&](int i) {
-                        if (MODE == kDHidden)
+                        if (!t.weight)
                             return reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), i));
                         return i < rows ? reinterpret_cast<char*>(to + i * a.dweight_stride) : nullptr;
                     };
@@ -875,8 +878,7 @@ int pairs_of() {
     return clusters_of((const void*)head_product_kernel<T, MODE, CTAS>, kProductThreads, CTAS, kProductShared);
 }
 template <typename T, int MODE, int CTAS>
-int32_t launch_product(const ProductArgs& p, const CUtensorMap& map_a, const CUtensorMap& map_b, int pairs,
-                       cudaStream_t stream) {
+int32_t launch_product(const ProductArgs& p, const Maps& maps, int pairs, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(CTAS * pairs));
     cfg.blockDim = dim3(kProductThreads);
@@ -887,7 +889,7 @@ int32_t launch_product(const ProductArgs& p, const CUtensorMap& map_a, const CUt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, head_product_kernel<T, MODE, CTAS>, map_a, map_b, p);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, head_product_kernel<T, MODE, CTAS>, maps, p);
     if (err != cudaSuccess) return zs::cuda_fail(err, "head_product_kernel");
     return zs::check_launch("head_product_kernel");
 }
@@ -949,37 +951,50 @@ template <> constexpr int32_t type_of<__nv_bfloat16>() { return ZS_BF16; }
 
 template <typename T, int CTAS>
 int32_t launch_logp(const HeadArgs& a, cudaStream_t stream) {
-    CUtensorMap rows, entries;
-    ZS_TRY(make_map(&rows, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
-    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, columns_of(CTAS)));
+    Maps maps;
+    ZS_TRY(make_map(&maps.m[0], type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
+    ZS_TRY(make_map(&maps.m[1], type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, columns_of(CTAS)));
+    maps.m[2] = maps.m[3] = maps.m[1];
     const int pairs = pairs_of<T, kLogits, CTAS>();
     if (pairs < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
-    ZS_TRY((launch_product<T, kLogits, CTAS>(ProductArgs{a, 0, a.vocab, 1}, rows, entries, pairs, stream)));
+    ZS_TRY((launch_product<T, kLogits, CTAS>(ProductArgs{a, 0, a.vocab, 1}, maps, pairs, stream)));
     return launch(head_join_kernel, dim3((unsigned)(round_up(a.rows, 32) / 32)), 512, stream, "head_join_kernel", a);
 }
 
 template <typename T, int CTAS>
 int32_t launch_grad(HeadArgs a, cudaStream_t stream) {
-    // the operands of the three products: H, W and d, along k or across it
-    CUtensorMap rows, entries, d_rows, w_across, d_across, h_across;
-    ZS_TRY(make_map(&rows, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
-    ZS_TRY(make_map(&entries, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, columns_of(CTAS)));
-    ZS_TRY(make_map(&d_rows, type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 128));
-    ZS_TRY(make_map(&w_across, type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 64));
-    ZS_TRY(make_map(&d_across, type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 64));
-    ZS_TRY(make_map(&h_across, type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 64));
-    const int pairs = pairs_of<T, kGrad, CTAS>(), pairs_h = pairs_of<T, kDHidden, CTAS>(), pairs_w = pairs_of<T, kDWeight, 2>();
-    if (pairs < 1 || pairs_h < 1 || pairs_w < 1) return ZS_ERR_CUDA;
-    a.pairs = pairs_h;
+    // the operands: H and W along k; d along k and W across, d and H across
+    Maps logits, back;
+    ZS_TRY(make_map(&logits.m[0], type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 128));
+    ZS_TRY(make_map(&logits.m[1], type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, columns_of(CTAS)));
+    logits.m[2] = logits.m[3] = logits.m[1];
+    ZS_TRY(make_map(&back.m[0], type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 128));
+    ZS_TRY(make_map(&back.m[1], type_of<T>(), a.weight, a.vocab, a.width, a.weight_stride, 64));
+    ZS_TRY(make_map(&back.m[2], type_of<T>(), a.d, a.rows_pad, a.piece, a.piece, 64));
+    ZS_TRY(make_map(&back.m[3], type_of<T>(), a.compact, a.rows_pad, a.width, a.width, 64));
+    const int pairs = pairs_of<T, kGrad, CTAS>();
+    // dH and dW in one launch where that takes some 100 us (4728 x 4116 x 1104 117 us for 135).
+    // With longer ones the tiles, dealt in turn, come out less even, and a kernel that
+    // looks at each tile's kind is slower (2048 x 50257 x 1600 580 us for 568, 7 x 155934 x 1104, of
+    // 256 rows in tiles, 349 for 304).
+    const bool together = a.dhidden != nullptr && a.dweight != nullptr &&
+                          6.0 * (double)a.rows_pad * (double)a.vocab * (double)a.width < 2e11;
+    a.pairs = together ? pairs_of<T, kBack, CTAS>() : pairs_of<T, kDHidden, CTAS>();
+    const int pairs_w = pairs_of<T, kDWeight, 2>();
+    if (pairs < 1 || a.pairs < 1 || pairs_w < 1) return ZS_ERR_CUDA;
     ZS_TRY(launch_rows(a, stream));
     ProductArgs p = {a, 0, 0, 0};
     for (p.first = 0;; p.first += a.piece) {
         p.last = p.first + a.piece >= a.vocab;
         p.count = p.last ? a.vocab - p.first : a.piece;
-        ZS_TRY((launch_product<T, kGrad, CTAS>(p, rows, entries, pairs, stream)));
-        if (a.dhidden != nullptr) ZS_TRY((launch_product<T, kDHidden, CTAS>(p, d_rows, w_across, pairs_h, stream)));
-        if (a.dweight != nullptr) ZS_TRY((launch_product<T, kDWeight, 2>(p, d_across, h_across, pairs_w, stream)));
+        ZS_TRY((launch_product<T, kGrad, CTAS>(p, logits, pairs, stream)));
+        if (together) {
+            ZS_TRY((launch_product<T, kBack, CTAS>(p, back, a.pairs, stream)));
+        } else {
+            if (a.dhidden != nullptr) ZS_TRY((launch_product<T, kDHidden, CTAS>(p, back, a.pairs, stream)));
+            if (a.dweight != nullptr) ZS_TRY((launch_product<T, kDWeight, 2>(p, back, pairs_w, stream)));
+        }
         if (p.last) break;
     }
     if (a.dhidden == nullptr) return ZS_OK;

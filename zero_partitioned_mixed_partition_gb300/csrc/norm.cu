@@ -8,8 +8,8 @@
 // registers of a team of warps between its sums and its output, the rows after it are on their
 // way into shared memory, and the gradient keeps its columns' sums over rows in registers.
 // Measured on one GB300 (6772 GB/s copied): 16384 x 1600 bf16 23.7 us, 4.4 TB/s; gradient
-// 16384 x 4096 bf16 71 us, 5.7 TB/s.  The first issues 0.48 instructions a cycle and
-// scheduler, 14 for an element, of which a third turn bf16 into fp32 (three times, since the
+// 16384 x 4096 bf16 71 us, 5.7 TB/s.  The first issues 0.58 instructions a cycle and
+// scheduler, 18 for an element, of which a fourth turn bf16 into fp32 (three times, since the
 // row is held as it was read; held as fp32 the rows ahead no longer fit the registers, 35 us).  The
 // gradient reaches 84 % of the copy rate.  Earlier forms of it: next row in registers instead of shared
 // memory 87 us; team size at run time 90 us.

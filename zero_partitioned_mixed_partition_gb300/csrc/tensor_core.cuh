@@ -93,25 +93,24 @@ __device__ __forceinline__ void loaded(float* v) {
 // ------------------------------------------------------------------ products ---
 
 // An operand in shared memory, in 128-byte rows with the 128-byte swizzle (groups of
-// eight rows, 1024 bytes).  Along k (K_MAJOR): a row holds 64 k of one m (or n).
-// Across k: a row holds 64 m of one k, and the next 64 m lie `next` bytes on.
-template <bool K_MAJOR>
-__device__ __forceinline__ uint64_t operand(const void* p, uint32_t next) {
-    const uint64_t lead = K_MAJOR ? 1 : next >> 4, group = 1024 >> 4;
+// eight rows, 1024 bytes).  Along k: a row holds 64 k of one m (or n).  Across k: a row
+// holds 64 m of one k, and the next 64 m lie `next` bytes on.
+__device__ __forceinline__ uint64_t operand(const void* p, uint32_t next, bool along) {
+    const uint64_t lead = along ? 1 : next >> 4, group = 1024 >> 4;
     return (uint64_t)((smem_addr(p) >> 4) & 0x3fff) | lead << 16 | group << 32 | 1ull << 46 | 2ull << 61;
 }
 // The step of 16 k of an operand's descriptor: 32 bytes along a row, or 16 rows.
-template <bool K_MAJOR> __device__ __forceinline__ uint64_t operand_step() { return (K_MAJOR ? 32 : 2048) >> 4; }
+__device__ __forceinline__ uint64_t operand_step(bool along) { return (along ? 32 : 2048) >> 4; }
 
 // What an instruction multiplies: A of 128 rows to a CTA and B of n columns in all, an
 // even share in each CTA, 16-bit types, fp32 sums.
 template <typename T> constexpr uint32_t operand_type();
 template <> constexpr uint32_t operand_type<__half>() { return 0; }
 template <> constexpr uint32_t operand_type<__nv_bfloat16>() { return 1; }
-template <int CTAS, typename T, bool A_K_MAJOR, bool B_K_MAJOR>
-__device__ __forceinline__ uint32_t product_kind(uint32_t n) {
-    return 1u << 4 | operand_type<T>() << 7 | operand_type<T>() << 10 | (A_K_MAJOR ? 0u : 1u) << 15 |
-           (B_K_MAJOR ? 0u : 1u) << 16 | (n >> 3) << 17 | (128u * CTAS >> 4) << 24;
+template <int CTAS, typename T>
+__device__ __forceinline__ uint32_t product_kind(uint32_t n, bool a_along, bool b_along) {
+    return 1u << 4 | operand_type<T>() << 7 | operand_type<T>() << 10 | (a_along ? 0u : 1u) << 15 | (b_along ? 0u : 1u) << 16 |
+           (n >> 3) << 17 | (128u * CTAS >> 4) << 24;
 }
 // sums [+]= A B over 16 k, by one thread of the (first) CTA.
 template <int CTAS>
