@@ -358,3 +358,34 @@ def test_large_offsets(zs, cuda_device):
     zs.zero_head_logp_grad_async(h, small, y, saved, ones, a, c, work)
     zs.zero_head_logp_grad_async(h, w, y, saved, ones, b, dw, work)
     assert torch.equal(a, b) and torch.equal(c, dw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,vocab,width", [(30, 5003, 264), (200, 9001, 520), (1300, 7000, 64)])
+def test_pieces_and_parts(zs, cuda_device, rows, vocab, width, dtype):
+    """Pieces of the vocabulary whose sums of dhidden are split into parts as well, the
+    last piece shorter: against the whole vocabulary in one piece."""
+    h, w, y, g = _inputs(rows, vocab, width, dtype, rows + width)
+    logp, saved = torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+    whole = zs.new_head_work(rows, width, vocab)
+    zs.zero_head_logp_async(h, w, y, logp, whole, saved=saved)
+    dlogp = torch.randn(rows, generator=g, device="cuda") / rows
+    want_h, want_w = torch.empty_like(h), torch.empty_like(w)
+    zs.zero_head_logp_grad_async(h, w, y, saved, dlogp, want_h, want_w, whole)
+    d = torch.softmax(h.double() @ w.double().t(), 1) * dlogp.double().abs()[:, None]
+    d[torch.arange(rows, device="cuda"), y] += dlogp.double().abs()
+    size = d @ w.double().abs()
+    for piece in (1024, 2048, 4096, 4352):
+        for both in (True, False):
+            dh, dw = torch.full_like(h, 7.0), torch.full_like(w, 7.0)
+            work, buf = _scratch(zs, rows, width, vocab, True, piece)
+            if both:
+                zs.zero_head_logp_grad_async(h, w, y, saved, dlogp, dh, dw, work)
+            else:
+                zs.zero_head_logp_grad_async(h, w, y, saved, dlogp, dh, None, work)
+                zs.zero_head_logp_grad_async(h, w, y, saved, dlogp, None, dw, work)
+            assert torch.equal(dw, want_w)
+            # the same products in another grouping: fp32 sums, then one rounding, perhaps to a neighbour
+            tol = (vocab / 16 + 40) * 8 * U * size + 2 * HALF[dtype] * want_h.double().abs() + TINY[dtype]
+            _close(dh, want_h.double(), tol, "dhidden")
+            assert (buf[:512] == 255).all() and (buf[512 + work.numel():] == 255).all()

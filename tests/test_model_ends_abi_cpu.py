@@ -25,6 +25,8 @@ def test_work_bytes(zs):
         assert 0 < one[0] <= one[1] and one[0] <= one[2]
         assert L.zero_head_work_bytes(rows, width, vocab, 0, 0) > 0
         assert L.zero_head_work_bytes(rows, width, vocab, 100, 1) == one[0]
+        whole = L.zero_head_work_bytes(rows, width, vocab, vocab, 1)
+        assert all(L.zero_head_work_bytes(rows, width, vocab, p, 1) == whole for p in (vocab + 1, 1 << 40, (1 << 63) - 1))
     # a large batch's scratch stays far below its logits: one piece of them, and fp32 sums of dhidden
     assert L.zero_head_work_bytes(8192, 4096, 131072, 0, 1) < 2 * 8192 * 131072
     for bad in ((-1, 4), (1 << 31, 4), (1, 0), (1, (1 << 24) + 1)):
@@ -64,7 +66,7 @@ def test_head_refusals(zs):
             assert call(_head(zs, **kw)) == arg, kw
         for kw in (dict(hidden=A + 8), dict(weight=B + 2), dict(hidden_stride=68), dict(weight_stride=65)):
             assert call(_head(zs, **kw)) == align, kw
-        for kw in (dict(labels=None), dict(work=None), dict(size=0), dict(size=-1), dict(size=1000)):
+        for kw in (dict(labels=None), dict(work=None), dict(size=0), dict(size=-1), dict(size=-(1 << 63)), dict(size=1000)):
             assert call(_head(zs), **kw) == arg, kw
         assert call(_head(zs), labels=C + 4) == align and call(_head(zs), work=A + 64) == align
         assert call(_head(zs), saved=C + 2) == align

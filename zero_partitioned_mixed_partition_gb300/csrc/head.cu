@@ -96,8 +96,7 @@ Plan plan_of(int64_t rows, int64_t width, int64_t vocab, int64_t piece, bool gra
     p.hidden = take(2 * p.rows_pad * width);
     if (gradient) {
         if (piece <= 0) piece = kPieceBytes / (2 * p.rows_pad);
-        p.piece = piece < kTile ? kTile : round_up(piece, kTile);
-        if (p.piece > p.tiles * kTile) p.piece = p.tiles * kTile;
+        p.piece = piece < kTile ? kTile : piece > p.tiles * kTile ? p.tiles * kTile : round_up(piece, kTile);
         // fp32 sums of dH, several of them where there are few tiles
         const int64_t tiles = p.rows_pad / kTile * (round_up(width, kTile) / kTile);
         const int64_t parts = round_up(160, tiles) / tiles;
@@ -118,11 +117,11 @@ bool valid_sizes(int64_t rows, int64_t width, int64_t vocab) {
 // The plan with the largest piece that fits; total = 0: none does.
 Plan plan_within(int64_t rows, int64_t width, int64_t vocab, int64_t bytes) {
     Plan p = plan_of(rows, width, vocab, kTile, true);
-    const int64_t more = (bytes - p.total) / (2 * p.rows_pad * kTile);
     if (bytes < p.total) {
         p.total = 0;
         return p;
     }
+    const int64_t more = (bytes - p.total) / (2 * p.rows_pad * kTile);
     return plan_of(rows, width, vocab, (more + 1) * kTile, true);
 }
 
@@ -438,12 +437,12 @@ __device__ __forceinline__ int32_t wide_of(const ProductArgs& p, int32_t n) {
 
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];  // full: the first CTA's counts both CTAs' copies
-    uint64_t sums_full[2], sums_empty[2];    // sums_empty: the first CTA's counts both CTAs' warps
+    uint64_t sums_full[2], sums_empty[2];          // sums_empty: the first CTA's counts both CTAs' warps
     uint64_t done;
-    uint32_t sums;                           // address of the tensor memory
-    int32_t failed;                          // a wait ran out
-    int32_t issued;                          // steps whose copies were issued,
-    uint32_t bytes[kMaxStages];                 // and what each CTA copied in the last ones
+    uint32_t sums;               // address of the tensor memory
+    int32_t failed;              // a wait ran out
+    int32_t issued;              // steps whose copies were issued,
+    uint32_t bytes[kMaxStages];  // and what each CTA copied in the last ones
 };
 
 // The 128 columns of a thread's row, as 16-bit numbers or fp32, from registers to
