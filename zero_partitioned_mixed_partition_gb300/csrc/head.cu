@@ -17,10 +17,10 @@
 //
 // The products are bound by the tensor cores and the power limit where they are large.
 // Measured on one GB300 (cuBLAS: 1921 TFLOP/s in a burst, 1718 sustained; 6772 GB/s
-// copied): log-probabilities 8192 x 50257 x 768 bf16, a quarter left out, 314 us (1510
+// copied): log-probabilities 8192 x 50257 x 768 bf16, a quarter left out, 316 us (1500
 // TFLOP/s), 4 x 32000 x 4096 bf16 55 us (4.8 TB/s: W is read once); gradient 2048 x 50257 x
-// 1600 fp16, 30 % left out, 563 us (1230 TFLOP/s), 8192 x 131072 x 4096 bf16, a tenth left out,
-// 15.0 ms (1580 TFLOP/s).  In the first case the tensor pipe is active in 74 % of the product's
+// 1600 fp16, 30 % left out, 578 us (1200 TFLOP/s), 8192 x 131072 x 4096 bf16, a tenth left out,
+// 15.2 ms (1560 TFLOP/s).  In the first case the tensor pipe is active in 79 % of the product's
 // cycles; two SMs' tile of 256 x 256 reads 64 bytes a cycle and SM from L2 and leaves shared
 // memory as many, its limit.  Rounds of tiles (the third case's are 5 % idle) and the rows that fill
 // a tile (7 % there) come on top.
