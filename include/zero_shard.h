@@ -896,8 +896,9 @@ typedef struct zs_norm {
  * differences from the mean), y rounded once to `type`.
  *   y        DEVICE [rows][width], y_stride >= width; may be x (same stride)
  *   saved    DEVICE fp32[2 rows] or NULL: mean, rstd
- * A row with a NaN or an infinity gives NaN.  A constant row with eps = 0 has
- * rstd = +inf and gives NaN.
+ * A constant row's mean is its value: xh is 0, and with eps = 0, rstd = +inf and the row
+ * is NaN.  A row with a NaN or an infinity, or whose sum passes fp32's range, gives
+ * NaN; one whose sum of squares does has rstd = 0.
  * Source: layer normalization (Ba, Kiros, Hinton); the pages' models have it
  * ("ln 2 x 768"), no step of the pages computes it. */
 ZS_API int32_t zero_layer_norm_async(const zs_norm* n, void* y, int64_t y_stride, float* saved, void* stream);
