@@ -859,8 +859,9 @@ ZS_API int32_t zero_head_logp_async(const zs_head* h, const int64_t* labels, flo
  * end.  Every sum has a fixed order.
  *   saved    DEVICE fp32[2 rows] of zero_head_logp_async (or of
  *            zero_token_logp_async from the same logits)
- *   dlogp    DEVICE fp32[rows].  Rows with dlogp = 0 are left out, as ignored
- *            ones are: dhidden 0, nothing added to dweight.
+ *   dlogp    DEVICE fp32[rows].  Rows with dlogp = 0, and rows of nothing but -inf
+ *            (saved[2 i + 1] = -inf), are left out, as ignored ones are: their hidden
+ *            state is not used, dhidden 0, nothing added to dweight.
  *   dhidden  DEVICE [rows][width], dhidden_stride >= width, or NULL
  *   dweight  DEVICE [vocab][width], dweight_stride >= width, or NULL; every row
  *            is written.  One of the two at least.  They may not overlap the inputs

@@ -4,8 +4,9 @@
 // With x = H W^T, t near a row's largest logit and lnS = ln sum_j exp((x_j - t) it):
 //   logp = (x_y - t) it - lnS,      d_ij = c_i (1[j = y_i] - p_ij),
 //   dH = d W,   dW = d^T H,         c_i = L it dlogp_i.
-// Rows that are left out (ignored labels, dlogp = 0) are taken out first: the
-// live rows' hidden states are copied together, so that prompts cost nothing.
+// Rows that are left out (ignored labels; in the gradient also dlogp = 0, and rows whose logits
+// are all -inf) are taken out first: the live rows' hidden states are copied together, so
+// that prompts cost nothing and what such rows hold meets no product.
 //
 // Log-probabilities are one product whose epilogue keeps a maximum and a sum for each
 // row and half tile (16 bytes for 256 logits), joined afterwards.  The gradient forms the
@@ -199,7 +200,9 @@ __device__ int32_t number_rows(const HeadArgs& a, int64_t from, int32_t before, 
     }
 #pragma unroll
     for (int k = 0; k < EACH; ++k) {
-        votes[k] = __ballot_sync(0xffffffffu, label[k] >= 0 && label[k] < a.vocab && dlogp[k] != 0.0f);
+        // (a row of nothing but -inf has no gradient, and perhaps an infinite hidden state)
+        votes[k] = __ballot_sync(0xffffffffu, label[k] >= 0 && label[k] < a.vocab && dlogp[k] != 0.0f &&
+                                                  log_sum[k] != -__int_as_float(0x7f800000));
         if (lane == 0) s_count[k * kWarps + warp] = __popc(votes[k]);
     }
     __syncthreads();
@@ -231,8 +234,7 @@ __device__ int32_t number_rows(const HeadArgs& a, int64_t from, int32_t before, 
         const int64_t i = from + k * THREADS + threadIdx.x;
         if (i >= a.rows) break;
         const int32_t r = s_count[k * kWarps + warp] + __popc(votes[k] & ((1u << lane) - 1u));
-        // (a row of nothing but -inf has no gradient)
-        const float coef = a.dlogp == nullptr || log_sum[k] == -__int_as_float(0x7f800000) ? 0.0f : factor * dlogp[k];
+        const float coef = a.dlogp == nullptr ? 0.0f : factor * dlogp[k];
         emit(i, votes[k] >> lane & 1u ? r : -1, Row{top[k], log_sum[k], coef, (int32_t)label[k]});
     }
     __syncthreads();
