@@ -959,8 +959,10 @@ ZS_API int32_t zero_embed_async(const zs_embed* e, void* out, int64_t out_stride
 ZS_API int64_t zero_embed_work_bytes(int64_t tokens, int64_t width);
 
 /* Gradient of the table: dtable_v = [dtable_v +] scale sum over the tokens i of
- * id v of dout_i, summed in fp32 in a fixed order over the tokens sorted by id, rounded
- * once to dtable_type.
+ * id v of dout_i, summed in fp32 in a fixed order over the tokens sorted by id.  The sum
+ * times scale is rounded to fp32; added to an fp32 table, that result is rounded again; a
+ * 16-bit table takes the sum times scale plus the element, rounded to fp32 together and
+ * then to its type.
  *   e        e->table is not used (may be NULL); e->type is dout's
  *   dout     DEVICE [tokens][width], dout_stride >= width
  *   dtable   DEVICE [vocab][width] of dtable_type (e->type or ZS_F32),
@@ -968,7 +970,8 @@ ZS_API int64_t zero_embed_work_bytes(int64_t tokens, int64_t width);
  *   accumulate  0: every row is written (zeros where no token has the id); 1: rows
  *            of ids that occur are added to, the others are left as they are
  *            (a table tied to the head adds to zero_head_logp_grad_async's dweight).
- *            Added to an fp32 table, subnormal sums and elements may count as 0.
+ *            Added to an fp32 table, subnormal products, elements and sums may count as 0.
+ *            The bits do not depend on where the rows lie.
  *            dtable may not overlap dout.
  *   work_dev DEVICE scratch on a 16-byte boundary, work_bytes >=
  *            zero_embed_work_bytes(tokens, width); holds nothing between calls

@@ -257,18 +257,31 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
 
 constexpr int kMaxChunk = 64;
 
+template <int V>
+__device__ __forceinline__ void add_in_memory(float* to, const float* x) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + i), "f"(x[i]), "f"(x[i + 1]), "f"(x[i + 2]),
+                         "f"(x[i + 3]) : "memory");
+    } else if constexpr (V == 2) {
+        asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(to), "f"(x[0]), "f"(x[1]) : "memory");
+    } else {
+        asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to), "f"(x[0]) : "memory");
+    }
+}
 template <typename G, int V>
 __device__ __forceinline__ void add_to_table(const EmbedArgs& a, uint32_t key, int64_t k, const float* sum) {
     if (!ZS_RANGE_OK(kSiteTable, key, 1, a.vocab)) return;
     Pack<G, V>* to = reinterpret_cast<Pack<G, V>*>((G*)a.dtable + (int64_t)key * a.dtable_stride + k);
-    if constexpr (sizeof(G) == 4 && V % 4 == 0) {
+    if constexpr (sizeof(G) == 4) {
         // added in L2: nothing waits for the row (an element is added to once in a call, so
-        // no order can matter)
+        // no order can matter).  The same additions whatever the row's boundary allows to go out together.
         if (a.accumulate) {
+            float y[V];
 #pragma unroll
-            for (int i = 0; i < V; i += 4)
-                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"((float*)to + i), "f"(sum[i] * a.scale),
-                             "f"(sum[i + 1] * a.scale), "f"(sum[i + 2] * a.scale), "f"(sum[i + 3] * a.scale) : "memory");
+            for (int i = 0; i < V; ++i) y[i] = __fmul_rn(sum[i], a.scale);
+            add_in_memory<V>(reinterpret_cast<float*>(to), y);
             return;
         }
     }
