@@ -19,6 +19,7 @@
 #include <stdint.h>
 
 #include "cluster_counts.h"
+#include "run_reach.h"
 #include "zs_internal.h"
 
 namespace {
@@ -323,23 +324,18 @@ __device__ __noinline__ void join_run(const EmbedArgs& a, int64_t chunks, int32_
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        auto key_at = [&](int64_t j) { return a.keys[j * a.chunk]; };
-        int64_t first = c, last = c;  // chunks whose first token has the key, 32 at a time; and the one it starts in
+        // chunks whose first token has the key, and the one that the run starts in
+        auto goes_on = [&](int64_t j) { return j >= 0 && j < chunks && a.keys[j * a.chunk] == key; };
+        int64_t first = c;
         if (started_before) {
-            for (bool more = true; more;) {
-                const int64_t j = first - 1 - lane;
-                const uint32_t votes = __ballot_sync(0xffffffffu, j >= 0 && key_at(j < 0 ? 0 : j) == key);
-                first -= votes == 0xffffffffu ? 32 : __ffs(~votes) - 1;
-                more = votes == 0xffffffffu;
-            }
+            first -= zs::run_reach([&](int64_t at, int64_t stride) {
+                return __ballot_sync(0xffffffffu, goes_on(c - at - stride * (lane + 1)));
+            });
             if (first > 0 && a.keys[first * a.chunk - 1] == key) --first;
         }
-        for (bool more = true; more;) {
-            const int64_t j = last + 1 + lane;
-            const uint32_t votes = __ballot_sync(0xffffffffu, j < chunks && key_at(j < chunks ? j : 0) == key);
-            last += votes == 0xffffffffu ? 32 : __ffs(~votes) - 1;
-            more = votes == 0xffffffffu;
-        }
+        const int64_t last = c + zs::run_reach([&](int64_t at, int64_t stride) {
+            return __ballot_sync(0xffffffffu, goes_on(c + at + stride * (lane + 1)));
+        });
         if (lane == 0) {
             s_first = first;
             s_last = last;
