@@ -446,9 +446,12 @@ int32_t chunk_of(int64_t tokens, int64_t width) {
 }
 
 // With two tokens and more to an id some runs are long, and the longest chain of loads is a
-// chunk's tokens, eight at a time, then the parts of the most frequent id, four at a time: with
-// a tenth of the tokens it is least for chunks of some sqrt(tokens / 6).  (17133 tokens of 127
-// ids, 568 wide fp32: 26 us for 40; 9292 of 11420, 472 wide bf16: 32 for 26, so not there.)
+// chunk's tokens, eight at a time, then the parts of the most frequent id, four (of eight floats)
+// or eight at a time.  Where that id has a tenth of the tokens the chain is least for chunks of
+// some sqrt(tokens / 5) or sqrt(tokens / 10); the rule takes sqrt(tokens / 8), from the sizes alone, whatever
+// the ids.  (17133 tokens of 127 ids, 568 wide fp32: 26 us for 40; 9292 of 11420, 472 wide
+// bf16: 32 for 26, so not there.  An id with more of the tokens waits for more parts: 65536
+// tokens of one id, 1024 wide bf16, 180 us.)
 int32_t chunk_of_runs(int64_t tokens, int64_t width, int64_t vocab) {
     int32_t chunk = chunk_of(tokens, width);
     if (tokens / 2 < vocab) return chunk;

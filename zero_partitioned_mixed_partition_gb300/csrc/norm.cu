@@ -7,12 +7,13 @@
 // Rows are read once and written once, so memory bounds the large cases: a row lies in the
 // registers of a team of warps between its sums and its output, the rows after it are on their
 // way into shared memory, and the gradient keeps its columns' sums over rows in registers.
-// Measured on one GB300 (6772 GB/s copied): 16384 x 1600 bf16 23.7 us, 4.4 TB/s; gradient
-// 16384 x 4096 bf16 71 us, 5.7 TB/s.  The first issues 0.58 instructions a cycle and
-// scheduler, 18 for an element, of which a fourth turn bf16 into fp32 (three times, since the
-// row is held as it was read; held as fp32 the rows ahead no longer fit the registers, 35 us).  The
-// gradient reaches 84 % of the copy rate.  Earlier forms of it: next row in registers instead of shared
-// memory 87 us; team size at run time 90 us.
+// Measured on one GB300 (6772 GB/s copied): 16384 x 1600 bf16 24.3 us, 4.3 TB/s, fp32 41.2 us, 5.1
+// TB/s; gradient 16384 x 4096 bf16 71 us, 5.7 TB/s, 84 % of the copy rate.  The first issues some 0.6
+// instructions a cycle and scheduler, 19 for an element, of which a fourth turn bf16 into fp32
+// (three times, since the row is held as it was read; held as fp32 the rows ahead no longer fit
+// the registers, 35 us): neither issue nor memory is its limit, but a row's two barriers and
+// exchanges, with a third of the warps resident.  Earlier forms of the gradient: next row in
+// registers instead of shared memory 87 us; team size at run time 90 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
