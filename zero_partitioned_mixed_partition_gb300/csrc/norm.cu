@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Team<WARPS>::kBlock, 1024 / Team<WARPS>::kBloc
         // fp32 numbers are some units off: there the differences from the first mean are summed as
         // well as their squares, and correct it.  In a constant row the difference d is a few units,
         // both sums, w d and w d^2, and the quotient are exact, and the deviation is 0.  (Correcting
-        // 16-bit rows too took 31.4 us for 29.3 at 16384 x 1600; fp32, 45.8 for 43.7.)
+        // 16-bit rows too took 31.4 us for 29.3 at 16384 x 1600; fp32 takes 47 for 43.7.)
         constexpr bool kCorrect = sizeof(T) == 4;
         const float sum = t.sum(sum_of(add2(s[0], s[1])));
         const float near = kCorrect ? __fmul_rn(sum, a.inv_width) : __fdiv_rn(sum, a.float_width);
